@@ -60,7 +60,7 @@ def _stream(stream):
 
 
 def _opts(scale, causal, softcap, sink, window=None, top_left=False, alibi=None, bias=None,
-          scale_p=None, scale_o=None):
+          scale_p=None, scale_o=None, sink_tokens=0):
     o = _lib.attn_opts()
     o.scale = float(scale) if scale is not None else 0.0
     o.causal = 1 if causal else 0
@@ -78,6 +78,7 @@ def _opts(scale, causal, softcap, sink, window=None, top_left=False, alibi=None,
         o.bias_strides = _lib.attn_strides(*_bias_strides(bias))
     o.scale_p = float(scale_p) if scale_p else 0.0
     o.scale_o = float(scale_o) if scale_o else 0.0
+    o.sink_tokens = int(sink_tokens)
     return o
 
 
@@ -124,10 +125,11 @@ def _check_sink(sink, Hq, device):
 
 def attn_fwd(q, k, v, o=None, lse=True, causal=False, scale=None, softcap=0.0, sink=None,
              stream=None, window=None, top_left=False, alibi_slopes=None, bias=None,
-             scale_p=None, scale_o=None):
+             scale_p=None, scale_o=None, sink_tokens=0):
     """Dense attention.  q [B,Hq,Lq,d], k/v [B,Hkv,Lk,d] (any strides with d-stride 1).
     ``window`` = (left, right) keeps keys i+Lk-Lq-left <= j <= i+Lk-Lq+right (a
-    negative side is unbounded); ``top_left`` drops the Lk-Lq shift.
+    negative side is unbounded); ``top_left`` drops the Lk-Lq shift; the first ``sink_tokens``
+    keys stay visible left of the window.
     ``alibi_slopes``: fp32 [Hq] or [B,Hq]; ``bias``: [B|1,Hq|1,Lq,Lk] in the input
     dtype, added to the scaled score.  float8_e4m3fn inputs (d = 128) run the FP8 path: O is
     e4m3, scale_o * scale_p * softmax(S) V saturated.  Returns (o [B,Hq,Lq,d], lse fp32
@@ -146,7 +148,7 @@ def attn_fwd(q, k, v, o=None, lse=True, causal=False, scale=None, softcap=0.0, s
     if bias is not None and (bias.dtype != q.dtype or bias.device != q.device):
         raise ValueError("bias must have the input dtype and device")
     opts = _opts(scale, causal, softcap, sink, window, top_left, alibi_slopes, bias, scale_p,
-                 scale_o)
+                 scale_o, sink_tokens)
     st = library().attn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse_t), B, Hq, Hkv, Lq, Lk,
                             d, _dtype_code(q), _strides_bhld(q), _strides_bhld(k),
                             _strides_bhld(v), _strides_bhld(o), ctypes.byref(opts),
@@ -157,7 +159,7 @@ def attn_fwd(q, k, v, o=None, lse=True, causal=False, scale=None, softcap=0.0, s
 
 def attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, o=None, lse=True,
                     causal=False, scale=None, softcap=0.0, sink=None, stream=None, window=None,
-                    top_left=False, alibi_slopes=None, scale_p=None, scale_o=None):
+                    top_left=False, alibi_slopes=None, scale_p=None, scale_o=None, sink_tokens=0):
     """Group mode.  q [total_q,Hq,d], k/v [total_k,Hkv,d], cu_seqlens int32 [B+1] on the
     device.  Returns (o [total_q,Hq,d], lse fp32 [Hq,total_q] or None)."""
     total_q, Hq, d = q.shape
@@ -176,7 +178,7 @@ def attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, o=None, l
     sink = _check_sink(sink, Hq, q.device)
     alibi_slopes = _check_alibi(alibi_slopes, B, Hq, q.device)
     opts = _opts(scale, causal, softcap, sink, window, top_left, alibi_slopes, None, scale_p,
-                 scale_o)
+                 scale_o, sink_tokens)
     st = library().attn_fwd_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse_t),
                                    _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), B, total_q, total_k,
                                    int(max_seqlen_q), Hq, Hkv, d, _dtype_code(q),
@@ -195,9 +197,9 @@ def attn_paged_auto_splits(B, Hkv, max_pages_per_seq) -> int:
 
 
 def attn_paged_window_pages(Lq, page_size, max_pages_per_seq, window=None, causal=False,
-                            top_left=False) -> int:
+                            top_left=False, sink_tokens=0) -> int:
     """Pages of one sequence the paged split layout tiles (W of attn_fwd_paged)."""
-    opts = _opts(None, causal, 0.0, None, window, top_left)
+    opts = _opts(None, causal, 0.0, None, window, top_left, sink_tokens=sink_tokens)
     return int(library().attn_paged_window_pages(Lq, page_size, max_pages_per_seq,
                                                  ctypes.byref(opts)))
 
@@ -209,13 +211,14 @@ def gqa_pack(Hq, Hkv) -> int:
     return g if g in (2, 4, 8, 16) else 1
 
 
-def attn_dense_schedule(B, Hq, Lq, Lk, grid, causal=False, window=None, top_left=False, Hkv=None):
+def attn_dense_schedule(B, Hq, Lq, Lk, grid, causal=False, window=None, top_left=False, Hkv=None,
+                        sink_tokens=0):
     """The static schedule attn_fwd runs on `grid` CTAs for a dense masked
     problem: a list of `grid` lists of work items (CTA by CTA, in run order),
     or None where the problem keeps the plain snake order.  Hkv defaults to
     Hq (no head packing)."""
     Hkv = Hq if Hkv is None else Hkv
-    opts = _opts(None, causal, 0.0, None, window, top_left)
+    opts = _opts(None, causal, 0.0, None, window, top_left, sink_tokens=sink_tokens)
     pack = gqa_pack(Hq, Hkv)
     per = 256 // pack
     n = B * (Hq // pack) * ((Lq + per - 1) // per) if Lq > 0 else 0
@@ -230,7 +233,7 @@ def attn_dense_schedule(B, Hq, Lq, Lk, grid, causal=False, window=None, top_left
 
 def attn_fwd_paged(q, k_pool, v_pool, block_table, seqlens_k, num_splits=0, o=None, lse=True,
                    causal=False, scale=None, softcap=0.0, sink=None, workspace=None,
-                   stream=None, window=None, top_left=False, alibi_slopes=None):
+                   stream=None, window=None, top_left=False, alibi_slopes=None, sink_tokens=0):
     """Paged KV.  q [B,Lq,Hq,d], pools [num_pages,page,Hkv,d], block_table int32
     [B,max_pages], seqlens_k int32 [B] (all on the device, contiguous).
     Returns (o [B,Lq,Hq,d], lse fp32 [B,Hq,Lq] or None)."""
@@ -244,7 +247,8 @@ def attn_fwd_paged(q, k_pool, v_pool, block_table, seqlens_k, num_splits=0, o=No
         num_splits = 1  # chunked prefill: the prefill kernel, no split-KV scratch
     elif num_splits == 0:
         num_splits = attn_paged_auto_splits(
-            B, Hkv, attn_paged_window_pages(Lq, page, max_pages, window, causal, top_left))
+            B, Hkv, attn_paged_window_pages(Lq, page, max_pages, window, causal, top_left,
+                                            sink_tokens))
     if o is None:
         o = torch.empty((B, Lq, Hq, d), dtype=q.dtype, device=q.device)
     lse_t = None
@@ -262,7 +266,8 @@ def attn_fwd_paged(q, k_pool, v_pool, block_table, seqlens_k, num_splits=0, o=No
         lse_part = workspace[num_splits * rows * d: need]
     sink = _check_sink(sink, Hq, q.device)
     alibi_slopes = _check_alibi(alibi_slopes, B, Hq, q.device)
-    opts = _opts(scale, causal, softcap, sink, window, top_left, alibi_slopes)
+    opts = _opts(scale, causal, softcap, sink, window, top_left, alibi_slopes,
+                 sink_tokens=sink_tokens)
     st = library().attn_fwd_paged(_ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_table),
                                   _ptr(seqlens_k), _ptr(o), _ptr(lse_t), B, Lq, Hq, Hkv, d,
                                   _dtype_code(q), page, num_pages, max_pages, num_splits,
@@ -274,7 +279,8 @@ def attn_fwd_paged(q, k_pool, v_pool, block_table, seqlens_k, num_splits=0, o=No
 
 def attn_fwd_paged_noalloc(q, k_pool, v_pool, block_table, seqlens_k, num_splits=0, o=None,
                            lse=True, causal=False, scale=None, softcap=0.0, sink=None,
-                           stream=None, window=None, top_left=False, alibi_slopes=None):
+                           stream=None, window=None, top_left=False, alibi_slopes=None,
+                           sink_tokens=0):
     """attn_fwd_paged for callers that cannot allocate device scratch: the split
     partials live in a fixed 16 MiB array inside the library (shared by all
     calls on a GPU; calls overlapping on the GPU race).  Outputs are allocated
@@ -290,7 +296,8 @@ def attn_fwd_paged_noalloc(q, k_pool, v_pool, block_table, seqlens_k, num_splits
         lse_t = lse
     sink = _check_sink(sink, Hq, q.device)
     alibi_slopes = _check_alibi(alibi_slopes, B, Hq, q.device)
-    opts = _opts(scale, causal, softcap, sink, window, top_left, alibi_slopes)
+    opts = _opts(scale, causal, softcap, sink, window, top_left, alibi_slopes,
+                 sink_tokens=sink_tokens)
     st = library().attn_fwd_paged_noalloc(_ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_table),
                                           _ptr(seqlens_k), _ptr(o), _ptr(lse_t), B, Lq, Hq, Hkv,
                                           d, _dtype_code(q), page, num_pages,

@@ -135,6 +135,17 @@ void resolve_window(const attn_opts* opts, int* wl, int* wr) {
   if (opts->causal) *wr = 0;  // any window_right >= 0 is looser than causal
 }
 
+// First tokens that stay visible left of the window; without a left bound
+// every earlier key is visible anyway.
+int resolve_keep(const attn_opts* opts) {
+  return (opts != nullptr && opts->use_window && opts->window_left >= 0) ? opts->sink_tokens : 0;
+}
+
+int prefill_mask(const PrefillParams& p) {
+  if (p.win_left < 0 && p.win_right < 0) return kMaskNone;
+  return p.sink_tokens > 0 ? kMaskBandKeep : kMaskBand;
+}
+
 // PackGQA (FlashAttention-3 epilogue, PackGQA row <-> (head, query) mapping):
 // the g = Hq / Hkv query heads of a kv head share each 128-row tile, 128 / g
 // queries of each, when g is a power of two from 2 to 16 (the tile then
@@ -176,6 +187,7 @@ void fill_common(PrefillParams& p, const attn_opts* opts, int d) {
   p.softcap_inv = cap > 0.0f ? 1.0f / cap : 0.0f;
   p.sink = opts != nullptr ? opts->sink : nullptr;
   resolve_window(opts, &p.win_left, &p.win_right);
+  p.sink_tokens = resolve_keep(opts);
   p.top_left = (opts != nullptr && opts->top_left) ? 1 : 0;
   p.inv_scale = 1.0f / scale;
   p.o_scale = ((opts != nullptr && opts->scale_p > 0.0f) ? opts->scale_p : 1.0f) *
@@ -193,6 +205,7 @@ attn_status check_opts(const attn_opts* opts, int Hq, bool allow_bias) {
   if (opts == nullptr) return ATTN_OK;
   if (opts->sink != nullptr && (reinterpret_cast<uintptr_t>(opts->sink) & 3u))
     return ATTN_ERR_INVALID;
+  if (opts->sink_tokens < 0) return ATTN_ERR_INVALID;
   const bool alibi = opts->alibi_slopes != nullptr, bias = opts->bias != nullptr;
   if (alibi && ((reinterpret_cast<uintptr_t>(opts->alibi_slopes) & 3u) ||
                 (opts->alibi_stride != 0 && opts->alibi_stride < Hq)))
@@ -231,18 +244,24 @@ cudaError_t launch_decode(const DecodeParams& p, int d, bool bf16, bool softcap,
   return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_prefill(const PrefillParams& p, int grid, int d, int dt, bool masked,
+cudaError_t launch_prefill(const PrefillParams& p, int grid, int d, int dt, int mask,
                            int xf, cudaStream_t stream, char* name, size_t name_len) {
-  const char* mask = !masked ? "nomask"
-                     : (p.win_left < 0 && p.win_right == 0) ? "causal"
-                                                            : "window";
+  const char* mask_name = mask == kMaskNone                        ? "nomask"
+                          : mask == kMaskBandKeep                  ? "window_keep"
+                          : (p.win_left < 0 && p.win_right == 0) ? "causal"
+                                                                 : "window";
   static const char* const kXfName[4] = {"plain", "softcap", "alibi", "bias"};
   snprintf(name, name_len, "attn_prefill_tcgen05_d%d_%s_%s%s_%s_m256n128_persistent", d,
-           dt == kDtE4M3 ? "e4m3" : dt == kDtBF16 ? "bf16" : "f16", mask,
+           dt == kDtE4M3 ? "e4m3" : dt == kDtBF16 ? "bf16" : "f16", mask_name,
            p.top_left ? "_topleft" : "",
            kXfName[(xf >= 0 && xf < 4) ? xf : 0]);
-  if (d == 64) return launch_prefill_d<64>(p, grid, dt, masked, xf, stream);
-  if (d == 128) return launch_prefill_d<128>(p, grid, dt, masked, xf, stream);
+  if (mask == kMaskBandKeep) {
+    if (d == 64) return launch_prefill_keep_d<64>(p, grid, dt, xf, stream);
+    if (d == 128) return launch_prefill_keep_d<128>(p, grid, dt, xf, stream);
+    return cudaErrorInvalidValue;
+  }
+  if (d == 64) return launch_prefill_d<64>(p, grid, dt, mask != kMaskNone, xf, stream);
+  if (d == 128) return launch_prefill_d<128>(p, grid, dt, mask != kMaskNone, xf, stream);
   return cudaErrorInvalidValue;
 }
 }  // namespace attn
@@ -307,7 +326,7 @@ int dense_block_steps(const PrefillParams& p, int mb) {
   const int qpt = 1 << p.qpt_log2;  // queries per tile
   const int m0 = mb * 2 * qpt;
   const int diag = p.top_left ? 0 : p.Lk - p.Lq;
-  int jb = INT_MAX, je = 0;
+  int jb = INT_MAX, je = 0, keep = 0;
   for (int t = 0; t < 2; ++t) {
     const int mt = m0 + t * qpt;
     if (mt >= p.Lq) continue;
@@ -319,15 +338,17 @@ int dense_block_steps(const PrefillParams& p, int mb) {
       jb = std::min(jb, kbeg / BN);
       je = std::max(je, (kend + BN - 1) / BN);
     }
+    keep = std::max(keep, (std::min(p.sink_tokens, kend) + BN - 1) / BN);
   }
-  return je > jb ? je - jb : 0;
+  if (je <= jb) return std::max(keep, 0);
+  return je - jb + std::max(0, std::min(keep, jb));
 }
 
 std::shared_ptr<const Schedule> dense_schedule(const PrefillParams& p, int grid) {
   static std::mutex mu;
-  static std::map<std::array<int, 9>, std::shared_ptr<const Schedule>> cache;
-  const std::array<int, 9> key = {p.B, p.units, p.Lq, p.Lk, p.win_left, p.win_right, p.top_left,
-                                  p.qpt_log2, grid};
+  static std::map<std::array<int, 10>, std::shared_ptr<const Schedule>> cache;
+  const std::array<int, 10> key = {p.B, p.units, p.Lq, p.Lk, p.win_left, p.win_right, p.top_left,
+                                   p.qpt_log2, grid, p.sink_tokens};
   {
     std::lock_guard<std::mutex> lock(mu);
     const auto f = cache.find(key);
@@ -568,11 +589,10 @@ attn_status attn_fwd(const void* q, const void* k, const void* v, void* o, float
     p.bias_head = opts->bias_strides.head;
     p.bias_batch = opts->bias_strides.batch;
   }
-  const bool masked = p.win_left >= 0 || p.win_right >= 0;
   p.num_items = p.num_m_blocks * B * p.units;
   const int grid = p.num_items < num_sms ? p.num_items : num_sms;  // persistent: one CTA per SM
   attach_schedule(p, grid);
-  return finish_launch(launch_prefill(p, grid, d, dt, masked, score_xf(p),
+  return finish_launch(launch_prefill(p, grid, d, dt, prefill_mask(p), score_xf(p),
                                       static_cast<cudaStream_t>(stream), g_last_name,
                                       sizeof(g_last_name)));
 }
@@ -658,10 +678,9 @@ attn_status attn_fwd_varlen(const void* q, const void* k, const void* v, void* o
   p.num_m_blocks = m_blocks(max_seqlen_q, p.pack);
   p.err = err;
   fill_common(p, opts, d);
-  const bool masked = p.win_left >= 0 || p.win_right >= 0;
   p.num_items = p.num_m_blocks * B * p.units;
   const int grid = p.num_items < num_sms ? p.num_items : num_sms;  // persistent: one CTA per SM
-  return finish_launch(launch_prefill(p, grid, d, dt, masked, score_xf(p),
+  return finish_launch(launch_prefill(p, grid, d, dt, prefill_mask(p), score_xf(p),
                                       static_cast<cudaStream_t>(stream), g_last_name,
                                       sizeof(g_last_name)));
 }
@@ -720,11 +739,10 @@ attn_status paged_prefill(const void* q, const void* k_pool, const void* v_pool,
   p.page_size = page_size;
   p.max_pages = max_pages;
   p.num_pages = num_pages;
-  const bool masked = p.win_left >= 0 || p.win_right >= 0;
   p.num_items = p.num_m_blocks * B * p.units;
   const int grid = p.num_items < num_sms ? p.num_items : num_sms;
-  return finish_launch(launch_prefill(p, grid, d, bf16 ? kDtBF16 : kDtF16, masked, score_xf(p), stream, g_last_name,
-                                      sizeof(g_last_name)));
+  return finish_launch(launch_prefill(p, grid, d, bf16 ? kDtBF16 : kDtF16, prefill_mask(p), score_xf(p),
+                                      stream, g_last_name, sizeof(g_last_name)));
 }
 }  // namespace
 
@@ -752,6 +770,7 @@ attn_status attn_dense_schedule(int B, int Hq, int Hkv, int Lq, int Lk, const at
   p.Lq = Lq;
   p.Lk = Lk;
   resolve_window(opts, &p.win_left, &p.win_right);
+  p.sink_tokens = resolve_keep(opts);
   p.top_left = (opts != nullptr && opts->top_left) ? 1 : 0;
   p.num_m_blocks = m_blocks(Lq, p.pack);
   p.num_items = static_cast<int>(n);
@@ -770,7 +789,9 @@ int attn_paged_window_pages(int Lq, int page_size, int max_pages_per_seq, const 
   if (wl < 0 || Lq < 0 || page_size <= 0 || max_pages_per_seq <= 0 ||
       (opts != nullptr && opts->top_left))
     return max_pages_per_seq;
-  const int64_t w = (static_cast<int64_t>(Lq) + wl + page_size - 1) / page_size + 1;
+  const int64_t keep = opts != nullptr && opts->sink_tokens > 0 ? opts->sink_tokens : 0;
+  const int64_t w = (static_cast<int64_t>(Lq) + wl + page_size - 1) / page_size + 1 +
+                    (keep + page_size - 1) / page_size;
   return w < max_pages_per_seq ? static_cast<int>(w) : max_pages_per_seq;
 }
 
@@ -894,6 +915,7 @@ attn_status attn_fwd_paged(const void* q, const void* k_pool, const void* v_pool
   p.softcap = (opts != nullptr && opts->softcap > 0.0f) ? opts->softcap : 0.0f;
   p.softcap_inv = p.softcap > 0.0f ? 1.0f / p.softcap : 0.0f;
   resolve_window(opts, &p.win_left, &p.win_right);
+  p.sink_tokens = resolve_keep(opts);
   p.top_left = (opts != nullptr && opts->top_left) ? 1 : 0;
   p.alibi = opts != nullptr ? opts->alibi_slopes : nullptr;
   p.alibi_stride = opts != nullptr ? opts->alibi_stride : 0;

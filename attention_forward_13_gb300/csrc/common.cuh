@@ -48,6 +48,10 @@ enum ErrBits : uint32_t {
 // widened to fp16 on chip for P.V, O scaled and saturated to e4m3).
 enum PrefillDt : int { kDtF16 = 0, kDtBF16 = 1, kDtE4M3 = 2 };
 
+// Mask of a prefill instantiation: none, the causal / window band, or the band
+// with the first sink_tokens keys visible left of it.
+enum PrefillMask : int { kMaskNone = 0, kMaskBand = 1, kMaskBandKeep = 2 };
+
 // Score transform of a prefill instantiation (applied to the raw score
 // before masking).
 enum ScoreXf : int { kXfNone = 0, kXfSoftcap = 1, kXfAlibi = 2, kXfBias = 3 };
@@ -99,6 +103,7 @@ struct PrefillParams {
   // <= j <= i + Lk - Lq + win_right; a negative bound is unbounded.  Causal
   // masking is win_right = 0.  Only read by the masked instantiations.
   int win_left, win_right;
+  int sink_tokens;                 // keys j < sink_tokens stay visible left of the band (win_left >= 0)
   int top_left;                    // masks and ALiBi aligned top-left (row i on key i)
   float o_scale;                   // FP8 static quantisation: scale_p * scale_o on O
   float inv_scale;                 // 1 / scale (bias and ALiBi go to raw-score units)
@@ -139,6 +144,7 @@ struct DecodeParams {
   int B, Lq, Hq, Hkv, page_size, num_pages, max_pages, num_splits, chunk_pages;
   float scale_log2, scale, softcap, softcap_inv;
   int win_left, win_right;  // as in PrefillParams (causal is win_right = 0)
+  int sink_tokens;
   int top_left;
   const float* alibi;       // ALiBi slopes as in PrefillParams, or nullptr
   int alibi_stride;

@@ -145,10 +145,18 @@ __global__ void __launch_bounds__(192, 2)
   // is the lowest.
   const int diag0 = p.top_left ? 0 : L - p.Lq;  // key on query row 0's diagonal
   const int k_lo = (FEAT > 0 && p.win_left >= 0) ? max(0, diag0 - p.win_left) : 0;
-  const int pg0 = k_lo / P + split * p.chunk_pages;
-  const int pg1 = min(pg0 + p.chunk_pages, pages_b);
+  // Pages are numbered without the hole between the pages of the first
+  // sink_tokens keys and the band: packed page v is logical page v below
+  // keep_pages, else v + gap.  Keys follow their pages, so that the splits
+  // and the 128-key blocks run over a dense range and no page of the hole is
+  // read (a streaming cache may have freed it).
+  const int band_page = k_lo / P;
+  const int keep_pages = FEAT > 0 ? min((p.sink_tokens + P - 1) / P, band_page) : 0;
+  const int gap = band_page - keep_pages;
+  const int pg0 = split * p.chunk_pages;
+  const int pg1 = min(pg0 + p.chunk_pages, pages_b - gap);
   const int k0 = pg0 * P;
-  const int k1 = min(pg1 * P, L);
+  const int k1 = min(pg1 * P, L - gap * P);
   const int nblk = (k1 > k0) ? (k1 - k0 + C::BK - 1) / C::BK : 0;
   const bool partial_out = p.num_splits > 1;
   const int64_t rows_total = static_cast<int64_t>(p.B) * p.Hq * p.Lq;
@@ -248,10 +256,11 @@ __global__ void __launch_bounds__(192, 2)
           const int key = kb + r0;
           int row = oob_row;
           if (key < k1) {
-            const int lp = key / P;
+            const int vp = key / P;  // packed page
+            const int lp = vp + (FEAT > 0 && vp >= keep_pages ? gap : 0);
             const int phys = lp < p.max_pages ? bt[lp] : -1;
             if (phys >= 0 && phys < p.num_pages) {
-              row = phys * P + (key - lp * P);
+              row = phys * P + (key - vp * P);
             } else if (p.err) {
               atomicOr(p.err, 1u << kErrDecodeBadPage);
             }
@@ -392,7 +401,8 @@ __global__ void __launch_bounds__(192, 2)
         tmem_ld_wait();
         reg_fence(sr);
       }
-      const int key = k0 + i * C::BK + tid;
+      const int vkey = k0 + i * C::BK + tid;  // key in packed pages
+      const int key = FEAT > 0 && vkey >= keep_pages * P ? vkey + gap * P : vkey;
       float x[C::NR];
 #pragma unroll
       for (int r = 0; r < C::NR; ++r) {
@@ -404,10 +414,11 @@ __global__ void __launch_bounds__(192, 2)
         }
         if constexpr (FEAT == 2)
           s = fmaf(-al[r], fabsf(static_cast<float>((r / g) + diag - key)), s);
-        bool valid = (key < k1) && (r < R);
+        bool valid = (vkey < k1) && (r < R);
         if constexpr (FEAT > 0) {
           if (p.win_right >= 0) valid = valid && (key <= (r / g) + diag + p.win_right);
-          if (p.win_left >= 0) valid = valid && (key >= (r / g) + diag - p.win_left);
+          if (p.win_left >= 0)
+            valid = valid && (key >= (r / g) + diag - p.win_left || key < p.sink_tokens);
         }
         x[r] = valid ? s : -INFINITY;
       }
@@ -441,7 +452,7 @@ __global__ void __launch_bounds__(192, 2)
       }
       // The last block: zero V rows past the split end so stale cache
       // contents can never reach the MMA (0 * NaN would).
-      if (i == nblk - 1 && key >= k1) {
+      if (i == nblk - 1 && vkey >= k1) {
         const int it = (nblk == 1) ? 1 : 2 * nblk - 1;
         if (wait_raw_d(&sm.full[it % C::NSLOT], (it / C::NSLOT) & 1, w.deadline)) {
           uint8_t* vb = sm.ring[it % C::NSLOT];

@@ -1,6 +1,8 @@
 // prefill_kernel.cuh -- fused attention forward for dense and varlen
 // (group-mode) problems on sm_103a, compiled once per head dimension
-// (prefill_d64.cu, prefill_d128.cu define ATTN_PREFILL_D and include this): TMA loads into 128B-swizzled shared memory behind
+// (prefill_d64.cu, prefill_d128.cu define ATTN_PREFILL_D and include this;
+// prefill_keep_d64.cu, prefill_keep_d128.cu also ATTN_PREFILL_KEEP, the
+// windows whose first tokens stay visible): TMA loads into 128B-swizzled shared memory behind
 // mbarrier rings, S = Q K^T and O += P V on the 5th-generation tensor cores
 // (tcgen05.mma, accumulators in tensor memory), online softmax in registers.
 //
@@ -327,11 +329,22 @@ __device__ __forceinline__ bool wait_raw(uint64_t* bar, uint32_t parity, uint64_
 // 128 / g queries of each of the g query heads h .. h + g - 1 of kv head hk.
 struct PrefillItem {
   int b, h, hk, rq0, rk0, bcoord, Lq, Lk, m0;
-  int jb;     // first K/V tile of the item
+  int jb;     // first K/V tile of the item (of its band)
   int cnt;    // K/V tiles streamed for the item (0: nothing to compute)
+  int nkeep;  // kMaskBandKeep: the first nkeep steps are K/V tiles 0 .. nkeep-1
+  int gap;    // ... and step u >= nkeep is tile u + gap
+  int klo;    // first key of the band any row of the item keeps
   int ub[2];  // query tile t takes part in steps [ub[t], ue[t]) of the item
   int ue[2];
 };
+
+// K/V tile of step u of an item: the band's tiles in order, with kMaskBandKeep
+// after the tiles of the first sink_tokens keys (the hole between is skipped).
+template <int MASK>
+__device__ __forceinline__ int kv_tile(const PrefillItem& it, int u) {
+  if constexpr (MASK == kMaskBandKeep) return u < it.nkeep ? u : u + it.gap;
+  return it.jb + u;
+}
 
 // One 128-key K or V tile of sequence it.b gathered from a paged pool
 // (Composable Kernel page block navigator: key j is row j mod page of
@@ -340,8 +353,9 @@ struct PrefillItem {
 // Pieces past the sequence end, or behind a block-table entry outside
 // [0, num_pages) (an error: device error word bit), load from one row past
 // the pool, which the copy engine fills with zeros, so every tile delivers
-// its full byte count.
-template <class C>
+// its full byte count.  So do pieces without a key that some row of the item
+// keeps: behind a window's left edge the table may name freed pages.
+template <class C, int MASK>
 __device__ __forceinline__ void load_paged_tile(const PrefillParams& p, const PrefillItem& it,
                                                 int key0, const CUtensorMap* map, uint8_t* dst,
                                                 uint64_t* bar, uint64_t pol) {
@@ -352,7 +366,9 @@ __device__ __forceinline__ void load_paged_tile(const PrefillParams& p, const Pr
   for (int r0 = 0; r0 < C::BN; r0 += BR) {
     const int key = key0 + r0;
     int row = oob_row;
-    if (key < it.Lk) {
+    const bool seen = MASK == kMaskNone || key + BR > it.klo ||
+                      (MASK == kMaskBandKeep && key < p.sink_tokens);
+    if (key < it.Lk && seen) {
       const int lp = key / P;
       const int phys = lp < p.max_pages ? bt[lp] : -1;
       if (phys >= 0 && phys < p.num_pages)
@@ -376,7 +392,7 @@ __device__ __forceinline__ void load_paged_tile(const PrefillParams& p, const Pr
 // Key bounds per query row i (bottom-right aligned, Composable Kernel mask
 // from the left/right window): i + (Lk - Lq) - win_left <= j <= i + (Lk - Lq)
 // + win_right, a negative bound meaning unbounded; causal is win_right = 0.
-template <int BM, int BN, bool MASK>
+template <int BM, int BN, int MASK>
 __device__ __forceinline__ bool decode_pair(const PrefillParams& p, int b, int mb, int unit,
                                             PrefillItem& it) {
   it.h = unit * p.pack;  // first query head of the item
@@ -421,6 +437,8 @@ __device__ __forceinline__ bool decode_pair(const PrefillParams& p, int b, int m
       }
     }
   }
+  it.klo = (MASK && p.win_left >= 0) ? max(0, it.m0 + diag - p.win_left) : 0;
+  it.nkeep = it.gap = 0;
   const bool has0 = te[0] > tb[0], has1 = te[1] > tb[1];
   it.jb = has0 ? (has1 ? min(tb[0], tb[1]) : tb[0]) : tb[1];
   const int je = max(has0 ? te[0] : 0, has1 ? te[1] : 0);
@@ -430,6 +448,33 @@ __device__ __forceinline__ bool decode_pair(const PrefillParams& p, int b, int m
     const bool has = te[t] > tb[t];
     it.ub[t] = has ? tb[t] - it.jb : 0;
     it.ue[t] = has ? te[t] - it.jb : 0;
+  }
+  if constexpr (MASK == kMaskBandKeep) {
+    // The tiles of the first sink_tokens keys up to the last row's right
+    // bound (kend of the later tile), then the band's.  A query tile with any
+    // key takes part from step 0 on: a step whose keys are all masked for it
+    // adds nothing, and steps stay one range.
+    int kt[2];  // sink tiles each query tile keeps
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int mt = it.m0 + t * qpt;
+      int ks = 0;
+      if (mt < it.Lq) {
+        ks = min(p.sink_tokens, it.Lk);
+        if (p.win_right >= 0) ks = min(ks, min(mt + qpt - 1, it.Lq - 1) + diag + p.win_right + 1);
+      }
+      kt[t] = ks > 0 ? (ks + BN - 1) / BN : 0;
+    }
+    const int band = it.cnt;  // tiles of the band
+    it.nkeep = max(kt[0], kt[1]);
+    if (band > 0) it.nkeep = min(it.nkeep, it.jb);
+    it.gap = band > 0 ? it.jb - it.nkeep : 0;
+    it.cnt = band + it.nkeep;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      it.ue[t] = te[t] > tb[t] ? it.nkeep + it.ue[t] : min(kt[t], it.cnt);
+      it.ub[t] = 0;
+    }
   }
   return true;
 }
@@ -445,7 +490,7 @@ struct ItemOrder {
   int n;                 // slots in use; -1: plain order
 };
 
-template <int BM, int BN, bool MASK, bool ORD>
+template <int BM, int BN, int MASK, bool ORD>
 __device__ __forceinline__ bool decode_item(const PrefillParams& p, const ItemOrder& ord, int item,
                                             PrefillItem& it) {
   if constexpr (ORD) {
@@ -470,7 +515,7 @@ __device__ __forceinline__ bool decode_item(const PrefillParams& p, const ItemOr
 // its sequence's end; a histogram gives each cost's first position, heaviest
 // first, and one warp places the slots in slot order within a cost, so that
 // every CTA builds the same list.
-template <int BM, int BN, bool MASK, class C>
+template <int BM, int BN, int MASK, class C>
 __device__ void order_items(const PrefillParams& p, PrefillSmem<C, true>& sm) {
   const int nslots = p.num_m_blocks * p.B;
   if ((p.cu_q == nullptr && p.seqlens_k == nullptr) || nslots > kMaxSlots) {
@@ -538,7 +583,7 @@ __device__ __forceinline__ int item_of_round(const PrefillParams& p, int r) {
 // XF: score transform before masking (ScoreXf): none, soft-cap, ALiBi or an
 // elementwise bias (the last two are mutually exclusive with the soft-cap).
 // ORD: group mode or paged cache, work items in the sorted order (order_items).
-template <int D, int DT, bool MASK, int XF, bool ORD>
+template <int D, int DT, int MASK, int XF, bool ORD>
 __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
     attn_prefill_kernel(const __grid_constant__ PrefillParams p) {
   using C = PrefillCfg<D, DT>;
@@ -644,36 +689,36 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
           if (!(ok = w.wait(&sm.k_empty[s], ph ^ 1, kErrPrefillKEmpty))) break;
           mbar_arrive_expect_tx(&sm.k_full[s], C::TILE_BYTES);
           if (p.block_table != nullptr) {
-            load_paged_tile<C>(p, it, (it.jb + j) * C::BN, &p.tm_k, sm.k[s], &sm.k_full[s],
+            load_paged_tile<C, MASK>(p, it, kv_tile<MASK>(it, j) * C::BN, &p.tm_k, sm.k[s], &sm.k_full[s],
                                pol_kv);
           } else {
 #pragma unroll
             for (int c = 0; c < C::NCHUNK; ++c) {
               if constexpr (ATTN_L2_HINTS)
                 tma_load_4d_hint(sm.k[s] + c * C::CHUNK_BYTES, &p.tm_k, &sm.k_full[s],
-                                 c * C::ATOM, it.rk0 + (it.jb + j) * C::BN, it.hk, it.bcoord,
+                                 c * C::ATOM, it.rk0 + kv_tile<MASK>(it, j) * C::BN, it.hk, it.bcoord,
                                  pol_kv);
               else
                 tma_load_4d(sm.k[s] + c * C::CHUNK_BYTES, &p.tm_k, &sm.k_full[s],
-                            c * C::ATOM, it.rk0 + (it.jb + j) * C::BN, it.hk, it.bcoord);
+                            c * C::ATOM, it.rk0 + kv_tile<MASK>(it, j) * C::BN, it.hk, it.bcoord);
             }
           }
           ++k_armed;
           if (!(ok = w.wait(&sm.v_empty[s], ph ^ 1, kErrPrefillVEmpty))) break;
           mbar_arrive_expect_tx(&sm.v_full[s], C::TILE_BYTES);
           if (p.block_table != nullptr) {
-            load_paged_tile<C>(p, it, (it.jb + j) * C::BN, &p.tm_v, sm.v[s], &sm.v_full[s],
+            load_paged_tile<C, MASK>(p, it, kv_tile<MASK>(it, j) * C::BN, &p.tm_v, sm.v[s], &sm.v_full[s],
                                pol_kv);
           } else {
 #pragma unroll
             for (int c = 0; c < C::NCHUNK; ++c) {
               if constexpr (ATTN_L2_HINTS)
                 tma_load_4d_hint(sm.v[s] + c * C::CHUNK_BYTES, &p.tm_v, &sm.v_full[s],
-                                 c * C::ATOM, it.rk0 + (it.jb + j) * C::BN, it.hk, it.bcoord,
+                                 c * C::ATOM, it.rk0 + kv_tile<MASK>(it, j) * C::BN, it.hk, it.bcoord,
                                  pol_kv);
               else
                 tma_load_4d(sm.v[s] + c * C::CHUNK_BYTES, &p.tm_v, &sm.v_full[s],
-                            c * C::ATOM, it.rk0 + (it.jb + j) * C::BN, it.hk, it.bcoord);
+                            c * C::ATOM, it.rk0 + kv_tile<MASK>(it, j) * C::BN, it.hk, it.bcoord);
             }
           }
           ++v_armed;
@@ -766,6 +811,21 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
           else
             ok = w.wait(&sm.v_full[s], (gu / C::NS) & 1, kErrPrefillVFull);
           if (!ok) break;
+          if constexpr (ORD && !FP8) {
+            // Paged cache: rows of the last page behind the sequence's end
+            // may hold anything, and 0 * NaN in P.V is not 0: zero them.
+            const int live = it.Lk - kv_tile<MASK>(it, u) * C::BN;
+            if (p.block_table != nullptr && live > 0 && live < C::BN && live % p.page_size != 0) {
+              const int end = min(C::BN, (live + p.page_size - 1) / p.page_size * p.page_size);
+              for (int i = lane; i < (end - live) * C::NCHUNK * 8; i += 32) {
+                const int row = live + i / (C::NCHUNK * 8), c = (i >> 3) % C::NCHUNK;
+                *reinterpret_cast<uint4*>(sm.v[s] + c * C::CHUNK_BYTES + row * 128 + (i & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();  // the tensor core reads what these lanes wrote
+              __syncwarp();
+            }
+          }
           const bool next = u + 1 < it.cnt;
           if (next && !(ok = w.wait(&sm.k_full[(gu + 1) % C::NS], ((gu + 1) / C::NS) & 1,
                                     kErrPrefillKFull)))
@@ -884,11 +944,12 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
       // ahead (the valid bytes only).
       uint4 bn[W / 8];
       auto fetch_bias = [&](int jj) {  // registers for step jj, L2 for step jj + 1
-        const int k0 = (it.jb + it.ub[t] + jj) * C::BN;
+        const int k0 = kv_tile<MASK>(it, it.ub[t] + jj) * C::BN;
         load_bias_regs<W / 8>(bn, bias_row + k0, it.Lk - k0);
         if (jj + 1 < nt) {
-          const char* nb = reinterpret_cast<const char*>(bias_row + k0 + C::BN);
-          const int bytes = min(it.Lk - (k0 + C::BN), W) * static_cast<int>(sizeof(T));
+          const int k1 = kv_tile<MASK>(it, it.ub[t] + jj + 1) * C::BN;
+          const char* nb = reinterpret_cast<const char*>(bias_row + k1);
+          const int bytes = min(it.Lk - k1, W) * static_cast<int>(sizeof(T));
           if (bytes > 0) {
             prefetch_l2(nb);
             if (bytes > 128) prefetch_l2(nb + 128);
@@ -904,7 +965,7 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
         ++pc;
         tc_fence_after();
         uint32_t sr[W];
-        const int j0 = (it.jb + it.ub[t] + j) * C::BN;  // first key of this K/V tile
+        const int j0 = kv_tile<MASK>(it, it.ub[t] + j) * C::BN;  // first key of this K/V tile
         // Whether some key of this tile is masked for some row of the tile
         // (the tail past Lk, the causal / window band): the same for every
         // thread of the warpgroup.
@@ -1009,6 +1070,10 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
             if (lo <= 0) {  // no left bound inside the columns (plain causal or the tail)
 #pragma unroll
               for (int c = 0; c < W; ++c) s[c] = c <= hi ? s[c] : kDrop;
+            } else if constexpr (MASK == kMaskBandKeep) {
+              const int keep = p.sink_tokens - j0;  // columns below it are first tokens
+#pragma unroll
+              for (int c = 0; c < W; ++c) s[c] = (c <= hi && (c >= lo || c < keep)) ? s[c] : kDrop;
             } else {
 #pragma unroll
               for (int c = 0; c < W; ++c) s[c] = (c <= hi && c >= lo) ? s[c] : kDrop;
@@ -1256,7 +1321,7 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
   }
 }
 
-template <int D, int DT, bool MASK, int XF, bool ORD = false>
+template <int D, int DT, int MASK, int XF, bool ORD = false>
 static cudaError_t launch_prefill_t(const PrefillParams& p, int grid, cudaStream_t stream) {
   using C = PrefillCfg<D, DT>;
   auto kern = attn_prefill_kernel<D, DT, MASK, XF, ORD>;
@@ -1280,7 +1345,7 @@ static cudaError_t launch_prefill_t(const PrefillParams& p, int grid, cudaStream
   return cudaGetLastError();
 }
 
-template <int DT, bool MASK>
+template <int DT, int MASK>
 static cudaError_t launch_prefill_x(const PrefillParams& p, int grid, int xf,
                                    cudaStream_t stream) {
   // Group mode and paged caches take the sorted work order (no bias there).
@@ -1302,24 +1367,34 @@ static cudaError_t launch_prefill_x(const PrefillParams& p, int grid, int xf,
   }
 }
 
-template <>
-cudaError_t launch_prefill_d<ATTN_PREFILL_D>(const PrefillParams& p, int grid, int dt,
-                                             bool masked, int xf, cudaStream_t stream) {
-  if (dt == kDtBF16) return masked ? launch_prefill_x<kDtBF16, true>(p, grid, xf, stream)
-                                   : launch_prefill_x<kDtBF16, false>(p, grid, xf, stream);
-  if (dt == kDtF16) return masked ? launch_prefill_x<kDtF16, true>(p, grid, xf, stream)
-                                  : launch_prefill_x<kDtF16, false>(p, grid, xf, stream);
+// All types of one mask.
+template <int MASK>
+static cudaError_t launch_prefill_m(const PrefillParams& p, int grid, int dt, int xf,
+                                   cudaStream_t stream) {
+  if (dt == kDtBF16) return launch_prefill_x<kDtBF16, MASK>(p, grid, xf, stream);
+  if (dt == kDtF16) return launch_prefill_x<kDtF16, MASK>(p, grid, xf, stream);
 #if ATTN_PREFILL_D == 128
   // FP8 static quantisation: head dimension 128, no score transform.
-  if (dt == kDtE4M3 && xf == kXfNone) {
-    if (p.cu_q != nullptr)
-      return masked ? launch_prefill_t<128, kDtE4M3, true, kXfNone, true>(p, grid, stream)
-                    : launch_prefill_t<128, kDtE4M3, false, kXfNone, true>(p, grid, stream);
-    return masked ? launch_prefill_t<128, kDtE4M3, true, kXfNone>(p, grid, stream)
-                  : launch_prefill_t<128, kDtE4M3, false, kXfNone>(p, grid, stream);
-  }
+  if (dt == kDtE4M3 && xf == kXfNone)
+    return p.cu_q != nullptr ? launch_prefill_t<128, kDtE4M3, MASK, kXfNone, true>(p, grid, stream)
+                             : launch_prefill_t<128, kDtE4M3, MASK, kXfNone>(p, grid, stream);
 #endif
   return cudaErrorInvalidValue;
 }
+
+#ifdef ATTN_PREFILL_KEEP
+template <>
+cudaError_t launch_prefill_keep_d<ATTN_PREFILL_D>(const PrefillParams& p, int grid, int dt, int xf,
+                                                  cudaStream_t stream) {
+  return launch_prefill_m<kMaskBandKeep>(p, grid, dt, xf, stream);
+}
+#else
+template <>
+cudaError_t launch_prefill_d<ATTN_PREFILL_D>(const PrefillParams& p, int grid, int dt,
+                                             bool masked, int xf, cudaStream_t stream) {
+  return masked ? launch_prefill_m<kMaskBand>(p, grid, dt, xf, stream)
+                : launch_prefill_m<kMaskNone>(p, grid, dt, xf, stream);
+}
+#endif
 
 }  // namespace attn

@@ -78,6 +78,11 @@ typedef struct {
  * i + Lk - Lq.  Causal keeps keys j <= i + Lk - Lq.  A window keeps
  * i + Lk - Lq - window_left <= j <= i + Lk - Lq + window_right, a negative
  * bound meaning unbounded on that side; with causal also set both apply.
+ * sink_tokens > 0 keeps the keys j < sink_tokens visible left of the window
+ * as well (the page's sink_size: first tokens a streaming cache never drops);
+ * the right bound still applies to them, and without a left bound it changes
+ * nothing.  Over a paged cache the pages between those keys and the window
+ * are not read, and their table entries may hold anything.
  * A row that keeps no key (and has no sink) gives O = 0, LSE = -inf.
  */
 typedef struct {
@@ -110,6 +115,7 @@ typedef struct {
    * bias with ATTN_E4M3. */
   float scale_p;
   float scale_o;
+  int sink_tokens;   /* keys j < sink_tokens stay visible left of the window; 0: none */
 } attn_opts;
 /* Combinations not built: soft-cap with ALiBi or bias (the pages do not fix
  * the order), ALiBi with bias, bias outside attn_fwd: ATTN_ERR_UNSUPPORTED. */
@@ -168,7 +174,9 @@ attn_status attn_fwd_varlen(const void* q, const void* k, const void* v, void* o
  *   e_b = ceil(L_b/page_size) and W = max_pages_per_seq.  With a window the
  *   pages are those holding a key some query row keeps: f_b = floor(k_lo /
  *   page_size), e_b = ceil(k_hi / page_size) for the kept key range
- *   [k_lo, k_hi) of the sequence, and W = attn_paged_window_pages().
+ *   [k_lo, k_hi) of the sequence, and W = attn_paged_window_pages(); with
+ *   sink_tokens the splits tile the sequence's visible pages in order, the
+ *   ceil(sink_tokens / page_size) first ones and then f_b .. e_b - 1.
  *   When num_splits > 1, o_partial (fp32 [num_splits][B][Hq][Lq][d]) and
  *   lse_partial (fp32 [num_splits][B][Hq][Lq]) are caller-owned scratch of
  *   attn_paged_workspace_bytes() bytes in total, and attn_splitkv_combine is
@@ -236,7 +244,8 @@ int attn_paged_auto_splits(int B, int Hkv, int max_pages_per_seq);
 
 /* W of the paged split layout: the most logical pages of one sequence that
  * hold a key some query row keeps.  max_pages_per_seq without a left window,
- * else min(max_pages_per_seq, ceil((Lq + window_left) / page_size) + 1)
+ * else min(max_pages_per_seq, ceil((Lq + window_left) / page_size) + 1 +
+ * ceil(sink_tokens / page_size))
  * (the kept keys of a sequence of length L are [max(0, L - Lq - window_left),
  * L), as every row's right bound reaches the last key or beyond).
  * opts may be NULL. */
