@@ -10,9 +10,12 @@ raised.  Output tensors are allocated with torch when not given.
     o, lse = attn_fwd_varlen(q, k, v, cu_q, cu_k, max_q)    # [total,H,d]
     o, lse = attn_fwd_paged(q, k_pool, v_pool, block_table, seqlens_k)
     o, lse = attn_splitkv_combine(o_part, lse_part)
+    mask, depth = attn_tree_mask(parents)                   # drafted tokens' tree
+    o, lse = attn_fwd_paged_tree(q, k_pool, v_pool, block_table, seqlens_k, mask)
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -22,7 +25,8 @@ from . import _lib
 __all__ = ["attn_fwd", "attn_fwd_varlen", "attn_fwd_paged", "attn_splitkv_combine",
            "attn_paged_workspace_bytes", "attn_paged_auto_splits", "attn_device_error",
            "attn_selftest_timeout", "attn_last_kernel_name", "attn_paged_window_pages",
-           "attn_fwd_paged_noalloc", "attn_dense_schedule", "gqa_pack", "AttnError", "library"]
+           "attn_fwd_paged_noalloc", "attn_dense_schedule", "attn_tree_mask",
+           "attn_tree_workspace_bytes", "attn_fwd_paged_tree", "gqa_pack", "AttnError", "library"]
 
 
 class AttnError(RuntimeError):
@@ -57,6 +61,12 @@ def _ptr(t):
 def _stream(stream):
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _device_of(device):
+    """Makes ``device`` current for a call (its streams, its error word); CPU tensors are
+    left to the call's own checks."""
+    return torch.cuda.device(device) if device.type == "cuda" else contextlib.nullcontext()
 
 
 def _opts(scale, causal, softcap, sink, window=None, top_left=False, alibi=None, bias=None,
@@ -304,6 +314,83 @@ def attn_fwd_paged_noalloc(q, k_pool, v_pool, block_table, seqlens_k, num_splits
                                           block_table.shape[1], num_splits, ctypes.byref(opts),
                                           _stream(stream))
     _check(st, "attn_fwd_paged_noalloc")
+    return o, lse_t
+
+
+def _on_device(device, tensors, dtype, what):
+    """Each given tensor is contiguous, of ``dtype`` and on ``device``."""
+    for t in tensors:
+        if t is not None and (t.dtype != dtype or t.device != device or not t.is_contiguous()):
+            raise ValueError(f"{what} must be contiguous {dtype} on {device}")
+
+
+def attn_tree_mask(parents, tree_lens=None, mask=None, depth=None, stream=None):
+    """Visibility masks and depths of draft trees.  parents int32 [B,T] (-1: follows the
+    sequence's last token), tree_lens int32 [B] or None.  Returns (mask int32
+    [B,T,ceil(T/32)], its 32 bits per word the nodes a node sees, depth int32 [B,T])."""
+    B, T = parents.shape
+    dev = parents.device
+    if mask is None:
+        mask = torch.empty((B, T, (T + 31) // 32), dtype=torch.int32, device=dev)
+    if depth is None:
+        depth = torch.empty((B, T), dtype=torch.int32, device=dev)
+    _on_device(dev, (parents, tree_lens, mask, depth), torch.int32, "parents, tree_lens, mask and depth")
+    if mask.shape != (B, T, (T + 31) // 32) or depth.shape != (B, T) or \
+            (tree_lens is not None and tree_lens.shape != (B,)):
+        raise ValueError("tree_lens is [B], mask [B,T,ceil(T/32)], depth [B,T]")
+    with _device_of(dev):
+        st = library().attn_tree_mask(_ptr(parents), _ptr(tree_lens), _ptr(mask), _ptr(depth), B, T,
+                                      _stream(stream))
+    _check(st, "attn_tree_mask")
+    return mask, depth
+
+
+def attn_tree_workspace_bytes(T, Hq, Hkv, d) -> int:
+    return int(library().attn_tree_workspace_bytes(T, Hq, Hkv, d))
+
+
+def attn_fwd_paged_tree(q, k_pool, v_pool, block_table, seqlens_k, tree_mask, tree_lens=None,
+                        tree_depth=None, o=None, lse=True, scale=None, softcap=0.0, sink=None,
+                        workspace=None, stream=None, window=None, sink_tokens=0):
+    """Attention of drafted nodes over a paged cache.  q [B,T,Hq,d]; the nodes' K/V are the
+    last T (or tree_lens[b]) of the seqlens_k[b] positions; node i sees every earlier
+    position and the nodes of its tree_mask row (attn_tree_mask).  ``window`` = (left, -1)
+    with tree_depth limits the earlier positions, the first ``sink_tokens`` staying visible.
+    Returns (o [B,T,Hq,d], lse fp32 [B,Hq,T] or None)."""
+    B, T, Hq, d = q.shape
+    num_pages, page, Hkv, _ = k_pool.shape
+    dev = q.device
+    _on_device(dev, (q, k_pool, v_pool, o), q.dtype, "q, the pools and o")
+    _on_device(dev, (block_table, seqlens_k, tree_mask, tree_lens, tree_depth), torch.int32,
+               "block_table, seqlens_k and the tree tensors")
+    if o is None:
+        o = torch.empty_like(q)
+    lse_t = lse if isinstance(lse, torch.Tensor) else None
+    if lse is True:
+        lse_t = torch.empty((B, Hq, T), dtype=torch.float32, device=dev)
+    _on_device(dev, (lse_t,), torch.float32, "lse")
+    if k_pool.shape[3] != d or v_pool.shape != k_pool.shape or block_table.dim() != 2 or \
+            block_table.shape[0] != B or seqlens_k.shape != (B,) or \
+            tree_mask.shape != (B, T, (T + 31) // 32) or o.shape != q.shape or \
+            (tree_lens is not None and tree_lens.shape != (B,)) or \
+            (tree_depth is not None and tree_depth.shape != (B, T)) or \
+            (lse_t is not None and lse_t.shape != (B, Hq, T)):
+        raise ValueError("shapes: q, o [B,T,Hq,d], pools [pages,page,Hkv,d], block_table [B,max_pages], "
+                         "seqlens_k, tree_lens [B], tree_mask [B,T,ceil(T/32)], tree_depth [B,T], lse [B,Hq,T]")
+    need = attn_tree_workspace_bytes(T, Hq, Hkv, d)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous on the same device")
+    sink = _check_sink(sink, Hq, dev)
+    opts = _opts(scale, False, softcap, sink, window, sink_tokens=sink_tokens)
+    with _device_of(dev):
+        st = library().attn_fwd_paged_tree(
+            _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_table), _ptr(seqlens_k), _ptr(tree_mask),
+            _ptr(tree_lens), _ptr(tree_depth), _ptr(o), _ptr(lse_t), B, T, Hq, Hkv, d, _dtype_code(q),
+            page, num_pages, block_table.shape[1], _ptr(workspace),
+            workspace.numel() * workspace.element_size(), ctypes.byref(opts), _stream(stream))
+    _check(st, "attn_fwd_paged_tree")
     return o, lse_t
 
 

@@ -33,7 +33,8 @@ ATTN_F16, ATTN_BF16, ATTN_E4M3 = 0, 1, 2
 EXPORTS = ("attn_fwd", "attn_fwd_varlen", "attn_fwd_paged", "attn_splitkv_combine",
            "attn_paged_workspace_bytes", "attn_paged_auto_splits", "attn_status_string",
            "attn_last_kernel_name", "attn_device_error", "attn_selftest_timeout",
-           "attn_fwd_paged_noalloc", "attn_paged_window_pages", "attn_dense_schedule")
+           "attn_fwd_paged_noalloc", "attn_paged_window_pages", "attn_dense_schedule",
+           "attn_tree_mask", "attn_tree_workspace_bytes", "attn_fwd_paged_tree")
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
 _lock = threading.Lock()
@@ -63,6 +64,10 @@ def _declare(lib):
     IP = ctypes.POINTER(ctypes.c_int32)
     lib.attn_dense_schedule.argtypes = [_I, _I, _I, _I, _I, O, _I, IP, IP]
     lib.attn_dense_schedule.restype = _I
+    lib.attn_tree_mask.argtypes = [_P, _P, _P, _P, _I, _I, _P]
+    lib.attn_tree_workspace_bytes.argtypes = [_I, _I, _I, _I]
+    lib.attn_tree_workspace_bytes.restype = ctypes.c_size_t
+    lib.attn_fwd_paged_tree.argtypes = [_P] * 10 + [_I] * 9 + [_P, ctypes.c_size_t, O, _P]
     lib.attn_status_string.argtypes = [_I]
     lib.attn_status_string.restype = ctypes.c_char_p
     lib.attn_last_kernel_name.argtypes = []
@@ -70,7 +75,8 @@ def _declare(lib):
     lib.attn_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint)]
     lib.attn_selftest_timeout.argtypes = [ctypes.c_uint64, _P]
     for name in ("attn_fwd", "attn_fwd_varlen", "attn_fwd_paged", "attn_splitkv_combine",
-                 "attn_device_error", "attn_selftest_timeout", "attn_fwd_paged_noalloc"):
+                 "attn_device_error", "attn_selftest_timeout", "attn_fwd_paged_noalloc",
+                 "attn_tree_mask", "attn_fwd_paged_tree"):
         getattr(lib, name).restype = _I
 
 

@@ -4,6 +4,7 @@
 // stream.
 #include "../../include/attn_fwd.h"
 #include "common.cuh"
+#include "host.h"
 #include "launch.h"
 #include "ptx.cuh"
 
@@ -276,6 +277,27 @@ attn_status finish_launch(cudaError_t e) {
   if (log_enabled()) fprintf(stderr, "[attn] launched %s\n", g_last_name);
   return ATTN_OK;
 }
+
+}  // namespace
+
+namespace attn {
+attn_status host_device_state(unsigned int** err, int* num_sms) { return device_state(err, num_sms); }
+bool host_make_map(CUtensorMap* m, const void* base, bool bf16, int rank, const uint64_t* dims,
+                   const uint64_t* strides_bytes, const uint32_t* box) {
+  return make_map(m, base, bf16 ? ATTN_BF16 : ATTN_F16, rank, dims, strides_bytes, box);
+}
+attn_status host_check_opts(const attn_opts* opts, int Hq, bool allow_bias) {
+  return check_opts(opts, Hq, allow_bias);
+}
+float host_scale(const attn_opts* opts, int d) { return resolve_scale(opts, d); }
+uint64_t host_timeout_ns() { return kTimeoutNs; }
+attn_status host_finish(cudaError_t e, const char* name) {
+  snprintf(g_last_name, sizeof(g_last_name), "%s", name);
+  return finish_launch(e);
+}
+}  // namespace attn
+
+namespace {
 
 __global__ void attn_selftest_timeout_kernel(unsigned int* err, uint64_t timeout_ns) {
   __shared__ uint64_t bar;

@@ -41,6 +41,12 @@ enum ErrBits : uint32_t {
   kErrDecodeBadPage = 14,
   kErrDecodeTeardown = 15,
   kErrSelftest = 20,
+  kErrTreeWait = 21,
+  kErrTreeBadPage = 22,
+  kErrTreeTeardown = 23,
+  kErrTreeBadParent = 24,
+  kErrCacheBadIndex = 25,
+  kErrCacheFull = 26,
 };
 
 // Element types of a prefill instantiation: fp16 / bf16 end to end, or e4m3
@@ -148,6 +154,34 @@ struct DecodeParams {
   int top_left;
   const float* alibi;       // ALiBi slopes as in PrefillParams, or nullptr
   int alibi_stride;
+  unsigned int* err;
+  uint64_t timeout_ns;
+};
+
+// Tree attention over a paged cache (tree_kernel.cuh).
+constexpr int kTreeMaxCtas = 160;  // bounds the workspace; more SMs than that stay idle
+struct TreeParams {
+  CUtensorMap tm_q;  // 5-D (d, g, Hkv, T, B), box {64, g, 1, qpt, 1}
+  CUtensorMap tm_k;  // 3-D (d, Hkv, num_pages * page_size)
+  CUtensorMap tm_v;
+  const int32_t* block_table;
+  const int32_t* seqlens_k;
+  const int32_t* tree_lens;   // nodes per sequence, or nullptr: T each
+  const uint32_t* tree_mask;  // [B][T][words]
+  const int32_t* tree_depth;  // [B][T], or nullptr: 0
+  void* o;                    // [B][T][Hq][d]
+  float* lse;                 // [B][Hq][T] or nullptr
+  const float* sink;          // [Hq] or nullptr
+  float* o_part;              // [2 * grid][d / 4][rows][4], rows = 128 or 256
+  float2* ml_part;            // [2 * grid][rows]
+  int B, T, Hq, Hkv, g, words;
+  int qpt;                    // queries per 128-row tile
+  int two_tiles;              // units of two query tiles
+  int units;                  // (query block, kv head) pairs per sequence
+  int grid, min_share;        // CTAs, and the fewest tiles worth a CTA
+  int page_size, num_pages, max_pages;
+  int win_left, sink_tokens;
+  float scale_log2, scale, softcap, softcap_inv;
   unsigned int* err;
   uint64_t timeout_ns;
 };

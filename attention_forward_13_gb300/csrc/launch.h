@@ -32,6 +32,10 @@ template <int D>
 cudaError_t launch_decode_d(const DecodeParams& p, bool bf16, bool softcap, int feat,
                             cudaStream_t stream);
 
+// One per head dimension (tree_d64.cu, tree_d128.cu).
+template <int D>
+cudaError_t launch_tree_d(const TreeParams& p, bool bf16, bool softcap, cudaStream_t stream);
+
 cudaError_t launch_combine(const CombineParams& p, bool bf16, cudaStream_t stream, char* name,
                            size_t name_len);
 

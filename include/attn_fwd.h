@@ -220,6 +220,54 @@ attn_status attn_fwd_paged_noalloc(const void* q, const void* k_pool, const void
                                    void* stream);
 
 /*
+ * attn_tree_mask -- which drafted nodes each node of a draft tree sees.
+ * Speculative decoding drafts a tree of T tokens per sequence: node i follows
+ * node parents[b][i] (an earlier index), or the sequence's last token where
+ * that is -1.  A node sees itself and the nodes it descends from.
+ *   parents: device int32 [B][T]; a value outside [-1, i) is an error (device
+ *   error word bit) and read as -1.  tree_lens: device int32 [B], nodes in use
+ *   per sequence (clamped to [0, T]), or NULL: T each.
+ *   mask: device uint32 [B][T][ceil(T / 32)], bit j % 32 of word j / 32 of row
+ *   i set where node i sees node j; depth: device int32 [B][T], the nodes above
+ *   i (NULL: not wanted).  Nodes past a sequence's end get empty rows, depth 0.
+ *   T <= ATTN_TREE_MAX_NODES.
+ */
+#define ATTN_TREE_MAX_NODES 1024
+attn_status attn_tree_mask(const int32_t* parents, const int32_t* tree_lens, uint32_t* mask,
+                           int32_t* depth, int B, int T, void* stream);
+
+/*
+ * attn_fwd_paged_tree -- attention of drafted nodes over a paged KV cache.
+ * The keys and values of the T drafted nodes are in the cache already, the
+ * last n_b = tree_lens[b] (T without tree_lens) of the L_b = seqlens_k[b]
+ * positions: node j's at position base + j, base = L_b - n_b.  Query i (node
+ * i) sees every position below base and the nodes of mask row i (built by
+ * attn_tree_mask, or any other set of bits; bits of nodes >= n_b are ignored).
+ *   q/o [B][T][Hq][d] contiguous, pools, block_table and seqlens_k as for
+ *   attn_fwd_paged; lse fp32 [B][Hq][T] or NULL.  Rows of nodes >= n_b are
+ *   written as empty rows (O = 0, LSE = -inf or the sink); their q may hold
+ *   anything, and so may the pool's rows behind L_b.
+ *   opts: scale, softcap, sink; a window with window_right < 0 keeps of the
+ *   positions below base those >= base + depth_i - window_left and the first
+ *   sink_tokens (tree_depth, device int32 [B][T], is needed then; depths are
+ *   clamped to [0, n_b)), and the pages it leaves out are not read.  Causal,
+ *   top_left, window_right >= 0, ALiBi, bias: ATTN_ERR_UNSUPPORTED.
+ *   workspace: attn_tree_workspace_bytes() bytes of device memory, 16-byte
+ *   aligned, needed by every call; nothing in it has to be set, and calls that
+ *   may overlap on the GPU (also replays of captured graphs) each need one.
+ *   Hq / Hkv <= 128, T <= ATTN_TREE_MAX_NODES.  Results do not depend on what
+ *   else runs: sums are taken in a fixed order.
+ */
+size_t attn_tree_workspace_bytes(int T, int Hq, int Hkv, int d);
+attn_status attn_fwd_paged_tree(const void* q, const void* k_pool, const void* v_pool,
+                                const int32_t* block_table, const int32_t* seqlens_k,
+                                const uint32_t* tree_mask, const int32_t* tree_lens,
+                                const int32_t* tree_depth, void* o, float* lse, int B, int T, int Hq,
+                                int Hkv, int d, attn_dtype dtype, int page_size, int num_pages,
+                                int max_pages_per_seq, void* workspace, size_t workspace_bytes,
+                                const attn_opts* opts, void* stream);
+
+/*
  * attn_splitkv_combine -- LSE-weighted merge of split partials (derived from
  * the definition of LSE; FlashAttention-3 epilogue num_splits layout):
  *   M = max_s LSE_s,  w_s = exp(LSE_s - M),
