@@ -174,12 +174,14 @@ struct TreeParams {
   const float* sink;          // [Hq] or nullptr
   float* o_part;              // [2 * grid][d / 4][rows][4], rows = 128 or 256
   float2* ml_part;            // [2 * grid][rows]
+  int4* cut;                  // [grid] for the merge kernel: the unit to merge there
   int B, T, Hq, Hkv, g, words;
   int qpt;                    // queries per 128-row tile
   int two_tiles;              // units of two query tiles
   int units;                  // (query block, kv head) pairs per sequence
-  int grid, min_share;        // CTAs, and the fewest tiles worth a CTA
-  int page_size, num_pages, max_pages;
+  int grid, min_share;        // CTAs, and the fewest slots worth a CTA
+  int unit_cost;              // slots of the line that a unit takes beside its tiles (>= 1)
+  int page_size, page_log2, num_pages, max_pages;
   int win_left, sink_tokens;
   float scale_log2, scale, softcap, softcap_inv;
   unsigned int* err;

@@ -107,6 +107,14 @@ struct Waiter {
   __device__ __forceinline__ bool aborted() const { return *abort_flag != 0; }
 };
 
+// Programmatic dependent launch: let the next kernel of the stream (if it was
+// launched with the attribute) be set up now / wait until the kernels before
+// this one have finished and their writes are visible.
+__device__ __forceinline__ void pdl_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Hint: bring the 128-byte line holding `addr` into L2 (no data returned, no
 // fault on any address the caller may read).
 __device__ __forceinline__ void prefetch_l2(const void* addr) {
@@ -151,6 +159,17 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, u
       " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4),
       "r"(smem_u32(bar))
+      : "memory");
+}
+// Warp-wide form: every lane executes it (converged) and the one whose leader
+// flag is set issues, so that uniform operands stay on the uniform datapath.
+__device__ __forceinline__ void tma_load_3d_warp(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                                 int c0, int c1, int c2, uint32_t leader) {
+  asm volatile(
+      "{\n .reg .pred e;\n setp.ne.b32 e, %6, 0;\n"
+      " @e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];\n}\n" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar)), "r"(leader)
       : "memory");
 }
 // The same copies with an L2 eviction-priority policy (createpolicy below).

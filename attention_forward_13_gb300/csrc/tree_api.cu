@@ -104,7 +104,8 @@ attn_status attn_tree_mask(const int32_t* parents, const int32_t* tree_lens, uin
 size_t attn_tree_workspace_bytes(int T, int Hq, int Hkv, int d) {
   if (T <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Hq / Hkv > 128 || d <= 0) return 0;
   const size_t rows = T > queries_per_tile(Hq / Hkv) ? 256 : 128;
-  return 2 * static_cast<size_t>(kTreeMaxCtas) * rows * (static_cast<size_t>(d) + 2) * sizeof(float);
+  return 2 * static_cast<size_t>(kTreeMaxCtas) * rows * (static_cast<size_t>(d) + 2) * sizeof(float) +
+         kTreeMaxCtas * sizeof(int4);
 }
 
 attn_status attn_fwd_paged_tree(const void* q, const void* k_pool, const void* v_pool,
@@ -122,7 +123,8 @@ attn_status attn_fwd_paged_tree(const void* q, const void* k_pool, const void* v
     return ATTN_ERR_UNSUPPORTED;
   const int g = Hq / Hkv;
   if (static_cast<int64_t>(num_pages) * page_size > 0x7fffffffLL ||
-      static_cast<int64_t>(max_pages_per_seq) * page_size > 0x7fffffffLL || T > ATTN_TREE_MAX_NODES || g > 128)
+      static_cast<int64_t>(max_pages_per_seq) * page_size > 0x7fffffffLL || T > ATTN_TREE_MAX_NODES || g > 128 ||
+      Hq > 65535)
     return ATTN_ERR_UNSUPPORTED;
   if (B == 0 || T == 0) return ATTN_OK;
   if (q == nullptr || k_pool == nullptr || v_pool == nullptr || block_table == nullptr ||
@@ -158,6 +160,10 @@ attn_status attn_fwd_paged_tree(const void* q, const void* k_pool, const void* v
   p.two_tiles = T > p.qpt ? 1 : 0;
   const int per = p.qpt * (p.two_tiles ? 2 : 1);
   p.units = Hkv * ((T + per - 1) / per);
+  // Tile slots of the whole call, at most: the kernels count them in 32 bits.
+  if (static_cast<int64_t>(B) * p.units * ((static_cast<int64_t>(max_pages_per_seq) * page_size + 127) / 128 + 8) >
+      0x7fffffffLL)
+    return ATTN_ERR_UNSUPPORTED;
   {
     const uint64_t eb = 2, row = static_cast<uint64_t>(d) * eb;
     const uint64_t dims[5] = {(uint64_t)d, (uint64_t)g, (uint64_t)Hkv, (uint64_t)T, (uint64_t)B};
@@ -186,8 +192,10 @@ attn_status attn_fwd_paged_tree(const void* q, const void* k_pool, const void* v
   p.Hkv = Hkv;
   p.words = (T + 31) / 32;
   p.grid = num_sms < kTreeMaxCtas ? num_sms : kTreeMaxCtas;
-  p.min_share = 2;
+  p.min_share = 4;
+  p.unit_cost = 2;
   p.page_size = page_size;
+  while ((1 << p.page_log2) < page_size) ++p.page_log2;
   p.num_pages = num_pages;
   p.max_pages = max_pages_per_seq;
   p.win_left = left;
@@ -200,6 +208,7 @@ attn_status attn_fwd_paged_tree(const void* q, const void* k_pool, const void* v
   const size_t pieces = 2 * static_cast<size_t>(p.grid), rows = p.two_tiles ? 256 : 128;
   p.o_part = static_cast<float*>(workspace);
   p.ml_part = reinterpret_cast<float2*>(p.o_part + pieces * rows * d);
+  p.cut = reinterpret_cast<int4*>(p.ml_part + pieces * rows);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool cap = p.softcap > 0.0f;
   char name[128];

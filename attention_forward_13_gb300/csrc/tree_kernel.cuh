@@ -14,21 +14,27 @@
 //    whole queries per 128-row tile, row = query * g + head (the box of one
 //    5-D tensor map; any g up to 128).
 //  * one persistent CTA per SM.  The 128-key tiles of all (sequence, query
-//    block, kv head) units form one line, and CTA c takes the tiles
+//    block, kv head) units form one line, each unit preceded by unit_cost
+//    slots that stand for its start and epilogue, and CTA c takes the slots
 //    [c T / G, (c + 1) T / G) of it, wherever sequence ends fall: every SM
-//    reads the same number of bytes for any mix of lengths.  The lengths
-//    live on the device, so each CTA finds its place by a scan.  A unit that
+//    gets the same amount of work for any mix of lengths.  The lengths live
+//    on the device, so each CTA finds its place by a scan.  A unit that
 //    ends up on one CTA is finished there; of a unit cut in pieces each CTA
 //    writes (m, l, unnormalised O) to the workspace (at most two pieces per
 //    CTA: its first and its last) and a second kernel merges them.
+//  * where there are enough units to balance the CTAs without cuts (two to
+//    sixteen per CTA), whole units are dealt out instead, longest first in
+//    snake order, if the longest hand is not much above the mean (every CTA
+//    works that out alike from the lengths).
 //  * up to 128 rows per unit, one query tile is not enough to hide the chain
 //    S -> softmax -> P.V behind the loads: the two softmax warpgroups then take
 //    alternate K/V tiles of the unit, each with its own running maximum, sum
 //    and O accumulator, merged from tensor memory at the unit's end.  Above
 //    128 rows they take one query tile each and share every K/V tile.
 //  * K and V tiles pass through one ring of shared-memory slots in consumption
-//    order K0, K1, V0, K2, V1, ...; what Q does not take of shared memory is
-//    ring (d = 128: 6 slots of 32 KB, or 5 beside two query tiles).
+//    order (K0, K1, V0, K2, V1, ... for two streams, K0, V0, K1, V1, ... for two
+//    query tiles); what Q does not take of shared memory is ring (d = 128: 6
+//    slots of 32 KB, or 5 beside two query tiles).
 //  * only the tiles that hold drafted nodes, the sequence's end or a window's
 //    edge are masked, from a 128-bit visibility word per row.
 #pragma once
@@ -69,7 +75,9 @@ struct TreeSmem {
   uint64_t s_full[2], p_half[2], p_full[2], o_final[2], o_free, xch, xread;
   uint64_t teardown;
   float2 x[2][128];     // (m, l) of a row, per warpgroup
-  long long scan[16];
+  int scan[16];
+  int4 walk[8];         // each softmax warp's place (TreeWalk)
+  uint8_t order[256];   // unit mode: the sequences, most tiles first
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -79,7 +87,7 @@ struct TreeSeq {
   int L, base, n;     // keys, keys before the drafted nodes, nodes
   int nkeep, gap;     // tile of step k: k < nkeep ? k : k + gap
   int tiles;          // K/V tiles with a visible key
-  int slots;          // its share of the work line per unit: max(tiles, 1)
+  int slots;          // its share of the work line per unit: tiles + unit_cost
 };
 
 __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
@@ -92,93 +100,159 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
   s.nkeep = min((min(p.sink_tokens, s.base) + 127) / 128, jb);
   s.gap = jb - s.nkeep;
   s.tiles = s.n > 0 ? (s.L + 127) / 128 - s.gap : 0;  // without a node nothing is asked
-  s.slots = max(s.tiles, 1);
+  s.slots = s.tiles + p.unit_cost;
   return s;
 }
 
-// Block-wide scan over the sequences: the total number of tile slots of one
-// unit per sequence, and the sequence whose slots hold unit-slot x of the line
-// (x in [0, total * units)): cum is the slots before it.  Every thread returns
-// the same values.  At most 14 warps; scratch: 16 long longs.
-__device__ inline long long tree_total(const TreeParams& p, long long* scratch) {
-  long long v = 0;
-  for (int b = threadIdx.x; b < p.B; b += blockDim.x) v += tree_seq(p, b).slots;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-  __syncthreads();
-  long long t = 0;
-  for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) t += scratch[i];
-  return t;
+// The line of tile slots in equal parts: CTA c of G takes [start(c), start(c + 1)).
+struct TreeLine {
+  int len, G, q, rem;
+  __device__ __forceinline__ int start(int c) const { return c * q + min(c, rem); }
+  __device__ __forceinline__ int cta_of(int x) const {
+    const int big = rem * (q + 1);
+    return x < big ? x / (q + 1) : rem + (x - big) / q;
+  }
+};
+
+__device__ __forceinline__ TreeLine tree_line(const TreeParams& p, int total) {
+  TreeLine n;
+  n.len = total * p.units;
+  n.G = min((n.len + p.min_share - 1) / p.min_share, p.grid);
+  n.q = n.len / n.G;
+  n.rem = n.len - n.q * n.G;
+  return n;
 }
 
-__device__ inline void tree_locate(const TreeParams& p, long long x, long long* scratch, int& b_out,
-                                   long long& cum_out) {
+// The line, and the sequence whose slots hold this CTA's first one: b, with
+// cum slots per unit before it.  A block-wide scan over the sequences'
+// lengths; every thread returns the same values (b = -1: nothing for this
+// CTA).  Up to blockDim sequences it takes one pass.  At most 14 warps;
+// scratch: 16 ints.
+__device__ inline TreeLine tree_place(const TreeParams& p, int* scratch, int& b_out, int& cum_out) {
   const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  long long before = 0;
+  const bool one = p.B <= static_cast<int>(blockDim.x);
+  TreeLine line{};
+  int total = 0, x = 0;
+  if (!one) {
+    int v = 0;
+    for (int b = threadIdx.x; b < p.B; b += blockDim.x) v += tree_seq(p, b).slots;
+    v = __reduce_add_sync(0xffffffffu, v);
+    if (lane == 0) scratch[warp] = v;
+    __syncthreads();
+    for (int i = 0; i < warps; ++i) total += scratch[i];
+    line = tree_line(p, total);
+    x = line.start(blockIdx.x);
+  }
+  if (threadIdx.x == 0) scratch[14] = -1;
+  int before = 0;
   for (int b0 = 0; b0 < p.B; b0 += blockDim.x) {
     const int b = b0 + threadIdx.x;
-    const long long n = b < p.B ? tree_seq(p, b).slots : 0;
-    long long inc = n;
+    const int n = b < p.B ? tree_seq(p, b).slots : 0;
+    int inc = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += y;
     }
-    __syncthreads();
+    __syncthreads();  // the previous sums have been read
     if (lane == 31) scratch[warp] = inc;
     __syncthreads();
-    long long pre = before, all = before;
+    int pre = before, all = before;
     for (int i = 0; i < warps; ++i) {
       if (i < warp) pre += scratch[i];
       all += scratch[i];
     }
-    __syncthreads();
-    const bool mine = b < p.B && (pre + inc - n) * p.units <= x && x < (pre + inc) * p.units;
-    if (mine) {
+    if (one) {
+      line = tree_line(p, all);
+      x = line.start(blockIdx.x);
+    }
+    const int lo = (pre + inc - n) * p.units;
+    if (static_cast<int>(blockIdx.x) < line.G && b < p.B && lo <= x && x - lo < n * p.units) {
       scratch[14] = b;
       scratch[15] = pre + inc - n;
     }
-    __syncthreads();
-    if (x < all * p.units) break;  // found in this chunk
     before = all;
   }
-  b_out = static_cast<int>(scratch[14]);
+  __syncthreads();
+  b_out = scratch[14];
   cum_out = scratch[15];
+  return line;
 }
 
-// CTAs that share a line of `line` tile slots, and the first slot of CTA c.
-__device__ __forceinline__ int tree_ctas(const TreeParams& p, long long line) {
-  const long long want = (line + p.min_share - 1) / p.min_share;
-  return static_cast<int>(want < p.grid ? want : p.grid);
+// Unit mode: hand of CTA c is items c, 2G - 1 - c, 2G + c, ... of the B * units
+// units, sequences with most tiles first.
+__device__ __forceinline__ int tree_item(int G, int c, int round) {
+  return round * G + ((round & 1) ? G - 1 - c : c);
+}
+
+// Decides for the whole grid between the line and unit mode, and leaves the
+// sequences' order in `order`.  The limit: a cut costs a CTA another start and
+// epilogue (2 unit_cost) and the merge kernel about 8 tiles' time; the snake's
+// uneven hands cost up to a sixteenth there.  cost: 256 ints of scratch.
+__device__ inline bool tree_unit_mode(const TreeParams& p, const TreeLine& line, int* scratch, int* cost,
+                                      uint8_t* order) {
+  const int N = p.B * p.units, G = gridDim.x, warp = threadIdx.x >> 5;
+  if (p.B > 256 || N < 2 * G || N > 16 * G) return false;
+  const int b = threadIdx.x;
+  if (b < p.B) cost[b] = tree_seq(p, b).slots;
+  __syncthreads();
+  if (b < p.B) {
+    const int mine = cost[b];
+    int rank = 0;
+    for (int j = 0; j < p.B; ++j) rank += cost[j] > mine || (cost[j] == mine && j < b);
+    order[rank] = static_cast<uint8_t>(b);
+  }
+  __syncthreads();
+  int hand = 0;
+  if (b < G)
+    for (int k = 0, i; (i = tree_item(G, b, k)) < N; ++k) hand += cost[order[i / p.units]];
+  hand = __reduce_max_sync(0xffffffffu, hand);
+  if ((threadIdx.x & 31) == 0) scratch[warp] = hand;
+  __syncthreads();
+  for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) hand = max(hand, scratch[i]);
+  __syncthreads();
+  return hand <= line.q + line.q / 16 + 2 * p.unit_cost + 8;
 }
 
 // A CTA's walk along the line, one segment (a run of tiles of one unit) at a time.
 struct TreeWalk {
-  int b, u, k;    // next sequence, unit within it, tile slot
-  int rem;        // tile slots left
+  int b, u, k;    // next sequence, unit within it, slot; unit mode: -2, -, round
+  int rem;        // slots left
 };
 struct TreeSeg {
   TreeSeq q;
   int b, hk, m0;    // sequence, kv head, first query
   int k0, n;        // tile steps [k0, k0 + n) of the unit
   bool whole;       // the unit's only segment
-  bool first;       // the CTA's first segment
 };
 
-__device__ __forceinline__ bool tree_next(const TreeParams& p, TreeWalk& w, TreeSeg& s, bool first) {
+// (A segment of no tiles is a part of a unit's leading slots, with nothing to
+// do, unless the unit has no tile at all: its first segment is then whole.)
+__device__ __forceinline__ bool tree_next(const TreeParams& p, const uint8_t* order, TreeWalk& w, TreeSeg& s) {
   if (w.rem <= 0) return false;
+  if (w.b == -2) {
+    const int i = tree_item(gridDim.x, blockIdx.x, w.k);
+    if (i >= p.B * p.units) return false;
+    ++w.k;
+    s.b = order[i / p.units];
+    const int u = i % p.units, rb = u / p.Hkv;
+    s.hk = u - rb * p.Hkv;
+    s.m0 = rb * (p.two_tiles ? 2 : 1) * p.qpt;
+    s.q = tree_seq(p, s.b);
+    s.k0 = 0;
+    s.n = s.q.tiles;
+    s.whole = true;
+    return true;
+  }
   s.q = tree_seq(p, w.b);
   const int take = min(w.rem, s.q.slots - w.k);
   s.b = w.b;
   const int rb = w.u / p.Hkv;
   s.hk = w.u - rb * p.Hkv;
   s.m0 = rb * (p.two_tiles ? 2 : 1) * p.qpt;
-  s.k0 = w.k;
-  s.n = s.q.tiles > 0 ? take : 0;
-  s.whole = take == s.q.slots;
-  s.first = first;
+  s.k0 = max(w.k - p.unit_cost, 0);
+  s.n = max(w.k + take - p.unit_cost, 0) - s.k0;
+  s.whole = s.n == s.q.tiles && (s.n > 0 || w.k == 0);
   w.rem -= take;
   w.k += take;
   if (w.k == s.q.slots) {
@@ -193,34 +267,43 @@ __device__ __forceinline__ bool tree_next(const TreeParams& p, TreeWalk& w, Tree
 
 __device__ __forceinline__ int tree_tile(const TreeSeq& q, int k) { return k < q.nkeep ? k : k + q.gap; }
 
-// Item of K_i / V_i of an n-tile segment in the ring order K0, K1, V0, K2, V1, ...
-__device__ __forceinline__ int tree_k_item(int i) { return i == 0 ? 0 : 2 * i - 1; }
-__device__ __forceinline__ int tree_v_item(int i, int n) { return i == n - 1 ? 2 * n - 1 : 2 * i + 2; }
-
-// One K or V tile, page piece by page piece (box of min(page, 128) rows).  Pieces
+// Pool row of page piece `lane` of a tile (box of min(page, 128) rows).  Pieces
 // behind the sequence's end, without a visible key, or behind a bad table
 // entry (an error) read one row past the pool: zeros.
 template <class C>
-__device__ __forceinline__ void tree_load_tile(const TreeParams& p, const TreeSeg& s, int tile,
-                                               const CUtensorMap* map, uint8_t* dst, uint64_t* bar) {
-  const int P = p.page_size, BR = min(P, C::BN);
-  const int32_t* bt = p.block_table + static_cast<int64_t>(s.b) * p.max_pages;
+__device__ __forceinline__ int tree_piece_row(const TreeParams& p, const TreeSeg& s, int tile, int lane) {
+  const int br_log2 = min(p.page_log2, 7);
+  const int key = tile * C::BN + (lane << br_log2);
   const int klo = p.win_left >= 0 ? max(0, s.q.base - p.win_left) : 0;
-  for (int r0 = 0; r0 < C::BN; r0 += BR) {
-    const int key = tile * C::BN + r0;
-    int row = p.num_pages * P;
-    if (key < s.q.L && (key + BR > klo || key < p.sink_tokens)) {
-      const int lp = key / P;
-      const int phys = lp < p.max_pages ? bt[lp] : -1;
-      if (phys >= 0 && phys < p.num_pages)
-        row = phys * P + (key - lp * P);
-      else if (p.err)
-        atomicOr(p.err, 1u << kErrTreeBadPage);
-    }
+  const int none = p.num_pages << p.page_log2;
+  if (lane >= (C::BN >> br_log2) || key >= s.q.L || (key + (1 << br_log2) <= klo && key >= p.sink_tokens))
+    return none;
+  const int lp = key >> p.page_log2;
+  const int phys = lp < p.max_pages ? p.block_table[static_cast<int64_t>(s.b) * p.max_pages + lp] : -1;
+  if (phys >= 0 && phys < p.num_pages) return (phys << p.page_log2) + (key & (p.page_size - 1));
+  if (p.err) atomicOr(p.err, 1u << kErrTreeBadPage);
+  return none;
+}
+
+// 4 x 4 transpose of 16-byte pieces within each quad of lanes: piece i of lane q
+// becomes piece q of lane i.  w: four pieces of four words.  (Selects on both
+// sides, no indexing by lane: that would put the array in local memory.)
+__device__ __forceinline__ void quad_transpose(uint32_t (&w)[16], int lane) {
+  const bool hi2 = lane & 2, hi1 = lane & 1;
 #pragma unroll
-    for (int c = 0; c < C::NCHUNK; ++c)
-      tma_load_3d(dst + c * C::CHUNK_BYTES + r0 * 128, map, bar, c * 64, s.hk, row);
+  for (int e = 0; e < 8; ++e) {  // pieces 0, 1 against 2, 3
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, hi2 ? w[e] : w[e + 8], 2);
+    w[e] = hi2 ? got : w[e];
+    w[e + 8] = hi2 ? w[e + 8] : got;
   }
+#pragma unroll
+  for (int h = 0; h < 16; h += 8)
+#pragma unroll
+    for (int e = h; e < h + 4; ++e) {  // pieces 0 against 1, 2 against 3
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, hi1 ? w[e] : w[e + 4], 1);
+      w[e] = hi1 ? got : w[e];
+      w[e + 4] = hi1 ? w[e + 4] : got;
+    }
 }
 
 // The low n bits (n <= 0: none, n >= 32: all).
@@ -247,22 +330,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
   const int nq = pair ? 2 : 1;               // Q buffers
   const int ns = C::NBUF - nq;               // ring slots
 
-  // This CTA's part of the line.
-  const long long line = tree_total(p, sm.scan) * p.units;
-  const int G = tree_ctas(p, line), cta = blockIdx.x;
-  if (cta >= G) return;
-  TreeWalk walk;
-  {
-    const long long x0 = line * cta / G, x1 = line * (cta + 1) / G;
-    long long cum;
-    tree_locate(p, x0, sm.scan, walk.b, cum);
-    const int slots = tree_seq(p, walk.b).slots;
-    const long long off = x0 - cum * p.units;
-    walk.u = static_cast<int>(off / slots);
-    walk.k = static_cast<int>(off - static_cast<long long>(walk.u) * slots);
-    walk.rem = static_cast<int>(x1 - x0);
-  }
-
+  pdl_launch_dependents();  // the merge kernel may be set up; it waits for this grid's end
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NBUF; ++i) {
       mbar_init(&sm.full[i], 1);
@@ -283,158 +351,261 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
     sm.abort_flag = 0;
     fence_mbar_init();
   }
+  if (warp == 8 && lane == 0) {
+    tma_prefetch_desc(&p.tm_q);
+    tma_prefetch_desc(&p.tm_k);
+    tma_prefetch_desc(&p.tm_v);
+  }
   if (warp == 9) {
     tmem_alloc(&sm.tmem_base, C::TM_COLS);
     tmem_relinquish();
   }
+  // This CTA's part of the line.
   tc_fence_before();
-  __syncthreads();
+  const int cta = blockIdx.x;
+  TreeWalk walk;
+  int cum;
+  const TreeLine line = tree_place(p, sm.scan, walk.b, cum);  // (synchronises the block)
+  const bool deal = tree_unit_mode(p, line, sm.scan, reinterpret_cast<int*>(sm.buf[0]), sm.order);
   tc_fence_after();
+  if (deal) {
+    walk = TreeWalk{-2, 0, 0, 1};
+    if (threadIdx.x == 0) p.cut[cta] = make_int4(-1, 0, 0, 0);
+  } else if (walk.b < 0) {
+    walk.rem = 0;
+    if (threadIdx.x == 0) p.cut[cta] = make_int4(-1, 0, 0, 0);
+  } else {
+    const int slots = tree_seq(p, walk.b).slots, x = line.start(cta);
+    const int off = x - cum * p.units;
+    walk.u = off / slots;
+    walk.k = off - walk.u * slots;
+    walk.rem = line.start(cta + 1) - x;
+    if (threadIdx.x == 0) {
+      // For the merge kernel: this CTA's first tile is inside a unit, and the
+      // CTA before it holds the unit's tile 0.
+      const int x0 = x - walk.k;
+      const bool first_cut = walk.k > p.unit_cost && line.start(cta - 1) <= x0 + p.unit_cost;
+      p.cut[cta] = first_cut ? make_int4(walk.b, walk.u, line.cta_of(x0 + slots - 1), 0)
+                             : make_int4(-1, 0, 0, 0);
+    }
+  }
   const uint32_t tmem = sm.tmem_base;
   const Waiter w{globaltimer_ns() + p.timeout_ns, &sm.abort_flag, p.err};
   TreeSeg s;
-  bool first = true;
 
   if (warp >= 8) {
     setmaxnreg_dec<C::OTHER_REGS>();
-    if (warp == 8 && lane == 0) {
-      // ========================= TMA producer ================================
-      tma_prefetch_desc(&p.tm_q);
-      tma_prefetch_desc(&p.tm_k);
-      tma_prefetch_desc(&p.tm_v);
-      int seg = 0, item = 0;
+    if (warp == 8 || warp == 10) {
+      // ========================= TMA producers (whole warps) =================
+      // Warp 8 loads Q and the K tiles, warp 10 the V tiles, each into its items
+      // of the one ring.  A tile is up to 8 page pieces x 2 column atoms: the
+      // lanes look the pieces' pages up together, a tile ahead, and the warp
+      // issues the boxes with a uniform row (measured at 16-token pages: one
+      // lane doing both in turn needs 3400 cycles per K and V tile, the step
+      // itself 2000).
+      const bool v_warp = warp == 10;
+      const CUtensorMap* map = v_warp ? &p.tm_v : &p.tm_k;
+      const uint32_t lead = elect_one() ? 1u : 0u;
+      const int br_log2 = min(p.page_log2, 7), pieces = C::BN >> br_log2;
+      int seg = 0, armed = 0, slot = 0;  // slot: the ring slot of the segment's next item
+      uint32_t eph = 1;                  // and the parity its release is waited with
       bool ok = true;
-      for (; ok && tree_next(p, walk, s, first); first = false) {
-        if (s.n == 0) continue;
-        // Q goes out behind the segment's first K tile (the CTA's first one
-        // before it): its buffer is free once the previous segment's last S is
-        // done, which that K tile does not have to wait for.
-        const int q_at = seg == 0 ? 0 : 1;
-        for (int i = 0; ok && i < 2 * s.n; ++i, ++item) {
-          if (i == q_at) {
-            if (seg > 0 && !(ok = w.wait(&sm.q_empty, (seg - 1) & 1, kErrTreeWait))) break;
-            const bool second = pair && s.m0 + p.qpt < p.T;
-            mbar_arrive_expect_tx(&sm.q_full, (second ? 2 : 1) * p.qpt * p.g * D * 2);
-            for (int t = 0; t < (second ? 2 : 1); ++t)
+      // Items before this warp's next one that are the other warp's.
+      auto skip = [&](int n) {
+        slot += n;
+        if (slot >= ns) slot -= ns, eph ^= 1;
+      };
+      auto load = [&](int row) {  // one tile into the current slot
+        ok = __all_sync(0xffffffffu, w.wait(&sm.empty[slot], eph, kErrTreeWait));
+        if (!ok) return;
+        if (lead) mbar_arrive_expect_tx(&sm.full[slot], C::TILE_BYTES);
+        __syncwarp();
+        uint8_t* dst = sm.buf[nq + slot];
+        for (int i = 0; i < pieces; ++i) {
+          const int r = __shfl_sync(0xffffffffu, row, i);
 #pragma unroll
-              for (int c = 0; c < C::NCHUNK; ++c)
-                tma_load_5d(sm.buf[t] + c * C::CHUNK_BYTES, &p.tm_q, &sm.q_full, c * 64, 0, s.hk,
-                            s.m0 + t * p.qpt, s.b);
-            ++seg;
-          }
-          // item -> K or V of which tile
-          bool is_v;
-          int tile;
-          if (i == 0) { tile = 0; is_v = false; }
-          else if (i == 2 * s.n - 1) { tile = s.n - 1; is_v = true; }
-          else if (i & 1) { tile = (i + 1) / 2; is_v = false; }
-          else { tile = i / 2 - 1; is_v = true; }
-          const int slot = item % ns;
-          if (!(ok = w.wait(&sm.empty[slot], ((item / ns) & 1) ^ 1, kErrTreeWait))) break;
-          mbar_arrive_expect_tx(&sm.full[slot], C::TILE_BYTES);
-          tree_load_tile<C>(p, s, tree_tile(s.q, s.k0 + tile), is_v ? &p.tm_v : &p.tm_k, sm.buf[nq + slot],
-                            &sm.full[slot]);
+          for (int c = 0; c < C::NCHUNK; ++c)
+            tma_load_3d_warp(dst + c * C::CHUNK_BYTES + (i << (br_log2 + 7)), map, &sm.full[slot], c * 64, s.hk,
+                             r, lead);
         }
+        ++armed;
+        skip(1);
+      };
+      for (; ok && tree_next(p, sm.order, walk, s);) {
+        const int n = __shfl_sync(0xffffffffu, s.n, 0);
+        if (n == 0) continue;
+        int row = tree_piece_row<C>(p, s, tree_tile(s.q, s.k0), lane);
+        for (int i = 0; ok && i < n; ++i) {
+          const int next = i + 1 < n ? tree_piece_row<C>(p, s, tree_tile(s.q, s.k0 + i + 1), lane) : 0;
+          if (!v_warp) {
+            // Q goes out behind the segment's first K tile (the CTA's first one
+            // before it): its buffer is free once the previous segment's last S
+            // is done, which that K tile does not have to wait for.
+            for (int part = 0; ok && part < 2; ++part) {
+              const bool q_part = seg == 0 ? part == 0 : part == 1;
+              if (!q_part) {
+                load(row);
+                // pair: K_i V_i K_i+1; streams: K0 K1 V0 K2 V1 ... V_n-2 V_n-1
+                if (ok) skip(pair ? 1 : i == 0 ? (n == 1 ? 1 : 0) : i == n - 1 ? 2 : 1);
+              } else if (i == 0) {
+                ok = seg == 0 || __all_sync(0xffffffffu, w.wait(&sm.q_empty, (seg - 1) & 1, kErrTreeWait));
+                if (!ok) break;
+                const int nt = pair && s.m0 + p.qpt < p.T ? 2 : 1;
+                if (lead) {
+                  mbar_arrive_expect_tx(&sm.q_full, nt * p.qpt * p.g * D * 2);
+                  for (int t = 0; t < nt; ++t)
+#pragma unroll
+                    for (int c = 0; c < C::NCHUNK; ++c)
+                      tma_load_5d(sm.buf[t] + c * C::CHUNK_BYTES, &p.tm_q, &sm.q_full, c * 64, 0, s.hk,
+                                  s.m0 + t * p.qpt, s.b);
+                }
+                __syncwarp();
+              }
+            }
+          } else {
+            if (i == 0) skip(pair || n == 1 ? 1 : 2);
+            load(row);
+            if (ok) skip(pair ? (i + 1 < n ? 1 : 0) : i + 2 < n ? 1 : 0);
+          }
+          row = next;
+        }
+        ++seg;
       }
       if (w.aborted()) {
-        // Every copy in flight lands before shared memory goes.
+        // Every copy in flight lands before shared memory goes: each slot's
+        // last armed phase completes when its bytes arrive (a slot never armed,
+        // or armed by the other warp, is waited for at most until the limit).
         const uint64_t dl = globaltimer_ns() + 50000000ull;
-        if (seg > 0) wait_raw(&sm.q_full, (seg - 1) & 1, dl);
-        for (int i = max(0, item - ns); i < item; ++i) wait_raw(&sm.full[i % ns], (i / ns) & 1, dl);
+        if (!v_warp && seg > 0) wait_raw(&sm.q_full, (seg - 1) & 1, dl);
+        for (int i = 0; i < ns && armed > 0; ++i) wait_raw(&sm.full[i], i < slot ? eph ^ 1 : eph, dl);
       }
     } else if (warp == 9) {
       // ========================= MMA issuer (whole warp) =====================
+      // The issue rate of this warp bounds the step (16 MMAs and 3 commits per
+      // tile): tiles are compile-time constants here and the ring position is
+      // a cursor, never a division (measured: 1400 cycles per tile's step with
+      // run-time tiles and item % slots).
       const uint32_t lead = elect_one() ? 1u : 0u;
       constexpr uint32_t idesc_s = idesc_f16_f32(BF16, 128, C::BN, false, false);
       constexpr uint32_t idesc_o = idesc_f16_f32(BF16, 128, D, false, true);
-      const uint64_t kdesc0 = sdesc_sw128(smem_u32(sm.buf[0]), 16, 1024);
-      const uint64_t vdesc0 = sdesc_sw128(smem_u32(sm.buf[0]), C::CHUNK_BYTES, 1024);
       constexpr uint32_t kTileDesc = C::TILE_BYTES >> 4;
-      int seg = 0, item0 = 0;
-      uint32_t pph = 0;  // bit t: phase of tile t's next P
-      bool ok = true;
-      auto slot_of = [&](int it) { return (item0 + it) % ns; };
-      auto wait_item = [&](int it) {
-        return w.wait(&sm.full[slot_of(it)], ((item0 + it) / ns) & 1, kErrTreeWait);
+      const uint64_t qdesc0 = sdesc_sw128(smem_u32(sm.buf[0]), 16, 1024);
+      const uint64_t qdesc1 = qdesc0 + (pair ? kTileDesc : 0);
+      const uint64_t kdesc0 = sdesc_sw128(smem_u32(sm.buf[nq]), 16, 1024);
+      const uint64_t vdesc0 = sdesc_sw128(smem_u32(sm.buf[nq]), C::CHUNK_BYTES, 1024);
+      int seg = 0, cur = 0;          // ring slot of the next item
+      uint32_t cph = 0;              // and its phase
+      uint32_t pph0 = 0, pph1 = 0;   // phase of each tile's next P
+      auto advance = [&]() {
+        if (++cur == ns) cur = 0, cph ^= 1;
       };
-      auto issue_s = [&](int t, int i) {  // S_t = Q K_i^T
-        const uint64_t qd = kdesc0 + static_cast<uint64_t>((pair ? t : 0) * kTileDesc);
-        const uint64_t kd = kdesc0 + static_cast<uint64_t>((nq + slot_of(tree_k_item(i))) * kTileDesc);
+      auto issue_s = [&](auto tc, int slot) {  // S_t = Q K^T
+        constexpr int t = decltype(tc)::value;
+        const uint64_t qd = t ? qdesc1 : qdesc0;
+        const uint64_t kd = kdesc0 + static_cast<uint64_t>(slot * kTileDesc);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = ((k >> 2) * C::CHUNK_BYTES + (k & 3) * 32) >> 4;
+          constexpr uint32_t kIn = 32 >> 4;
+          const uint32_t off = (k >> 2) * (C::CHUNK_BYTES >> 4) + (k & 3) * kIn;
           umma_ss_warp(tmem + C::tm_s(t), qd + off, kd + off, idesc_s, k > 0 ? 1u : 0u, lead);
         }
         umma_commit_warp(&sm.s_full[t], lead);
       };
-      auto issue_pv = [&](int t, int slot, bool acc, int k0, int k1) {  // O_t (+)= P_t V
-        const uint64_t vd = vdesc0 + static_cast<uint64_t>((nq + slot) * kTileDesc);
+      // P.V of tile t as its two halves arrive.  fresh: the tile's first of the
+      // segment (O is free once the previous segment's epilogue has read it).
+      auto issue_pv = [&](auto tc, int slot, bool fresh) -> bool {
+        constexpr int t = decltype(tc)::value;
+        uint32_t& ph = t ? pph1 : pph0;
+        const uint64_t vd = vdesc0 + static_cast<uint64_t>(slot * kTileDesc);
+        if (!w.wait(&sm.p_half[t], ph, kErrTreeWait)) return false;
+        if (fresh && seg > 0 && !w.wait(&sm.o_free, (seg - 1) & 1, kErrTreeWait)) return false;
+        tc_fence_after();
 #pragma unroll
-        for (int k = k0; k < k1; ++k)
+        for (int k = 0; k < C::BN / 32; ++k)
           umma_ts_warp(tmem + C::tm_o(t), tmem + C::tm_s(t) + k * 8, vd + ((k * 16 * 128) >> 4), idesc_o,
-                       (acc || k > 0) ? 1u : 0u, lead);
+                       (k > 0 || !fresh) ? 1u : 0u, lead);
+        if (!w.wait(&sm.p_full[t], ph, kErrTreeWait)) return false;
+        ph ^= 1;
+        tc_fence_after();
+#pragma unroll
+        for (int k = C::BN / 32; k < C::BN / 16; ++k)
+          umma_ts_warp(tmem + C::tm_o(t), tmem + C::tm_s(t) + k * 8, vd + ((k * 16 * 128) >> 4), idesc_o, 1u,
+                       lead);
+        return true;
       };
-      for (; ok && tree_next(p, walk, s, first); first = false) {
+      const std::integral_constant<int, 0> t0{};
+      const std::integral_constant<int, 1> t1{};
+      bool ok = true;
+      for (; ok && tree_next(p, sm.order, walk, s);) {
         if (s.n == 0) continue;
-        const int n = s.n;
-        const int live = pair ? (s.m0 + p.qpt < p.T ? 2 : 1) : min(n, 2);  // query tiles / streams in use
+        const int n = __shfl_sync(0xffffffffu, s.n, 0);
+        const bool two = pair ? s.m0 + p.qpt < p.T : n > 1;  // both tiles in use
+        const int tail = s.q.L & (C::BN - 1);  // rows of the sequence's last tile, if not full
+        const int last = s.k0 + n == s.q.tiles && (tail & (p.page_size - 1)) != 0 ? n - 1 : -1;
         if (!(ok = w.wait(&sm.q_full, seg & 1, kErrTreeWait))) break;
-        // First S of each tile (alternate K tiles, or the same one).
-        for (int t = 0; ok && t < live; ++t) {
-          const int i = pair ? 0 : t;
-          if (!(ok = wait_item(tree_k_item(i)))) break;
-          tc_fence_after();
-          issue_s(t, i);
-          if (!pair || t == live - 1) umma_commit_warp(&sm.empty[slot_of(tree_k_item(i))], lead);
+        // First S of each tile: of K0, and of K1 where the tiles are streams.
+        if (!(ok = w.wait(&sm.full[cur], cph, kErrTreeWait))) break;
+        tc_fence_after();
+        issue_s(t0, cur);
+        if (pair) {
+          if (two) issue_s(t1, cur);
+          umma_commit_warp(&sm.empty[cur], lead);
+          advance();
+        } else {
+          umma_commit_warp(&sm.empty[cur], lead);
+          advance();
+          if (two) {
+            if (!(ok = w.wait(&sm.full[cur], cph, kErrTreeWait))) break;
+            tc_fence_after();
+            issue_s(t1, cur);
+            umma_commit_warp(&sm.empty[cur], lead);
+            advance();
+          }
         }
-        if (!ok) break;
         if (pair ? n == 1 : n <= 2) umma_commit_warp(&sm.q_empty, lead);  // no later S
-        for (int i = 0; ok && i < n; ++i) {
-          const int vslot = slot_of(tree_v_item(i, n));
-          if (!(ok = wait_item(tree_v_item(i, n)))) break;
-          {
+        const int step = pair ? 1 : 2;  // K tiles from one S of a tile to its next
+        for (int i = 0; i < n; ++i) {
+          const int vs = cur;
+          if (!(ok = w.wait(&sm.full[vs], cph, kErrTreeWait))) break;
+          advance();
+          if (i == last) {
             // Rows of the last page behind the sequence's end may hold anything,
             // and 0 * NaN in P.V is not 0: zero them.
-            const int rows = s.q.L - tree_tile(s.q, s.k0 + i) * C::BN;
-            if (rows < C::BN && rows % p.page_size != 0) {
-              const int end = min(C::BN, (rows + p.page_size - 1) / p.page_size * p.page_size);
-              for (int e = lane; e < (end - rows) * C::NCHUNK * 8; e += 32) {
-                const int row = rows + e / (C::NCHUNK * 8), c = (e >> 3) % C::NCHUNK;
-                *reinterpret_cast<uint4*>(sm.buf[nq + vslot] + c * C::CHUNK_BYTES + row * 128 + (e & 7) * 16) =
-                    make_uint4(0, 0, 0, 0);
-              }
-              fence_proxy_async_smem();
-              __syncwarp();
+            const int end = min(C::BN, (tail + p.page_size - 1) & ~(p.page_size - 1));
+            for (int e = lane; e < (end - tail) * C::NCHUNK * 8; e += 32) {
+              const int row = tail + e / (C::NCHUNK * 8), c = (e >> 3) % C::NCHUNK;
+              *reinterpret_cast<uint4*>(sm.buf[nq + vs] + c * C::CHUNK_BYTES + row * 128 + (e & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
             }
+            fence_proxy_async_smem();
+            __syncwarp();
           }
-          const int step = pair ? 1 : 2;         // K tiles to this tile's next S
-          const bool more = i + step < n;
-          for (int t = pair ? 0 : (i & 1); ok && t < (pair ? live : (i & 1) + 1); ++t) {
-            if (!(ok = w.wait(&sm.p_half[t], (pph >> t) & 1, kErrTreeWait))) break;
-            const bool fresh = i < step;         // the tile's first P.V of the segment
-            // O is free once the previous segment's epilogue has read it.
-            if (fresh && seg > 0 && !(ok = w.wait(&sm.o_free, (seg - 1) & 1, kErrTreeWait))) break;
-            tc_fence_after();
-            issue_pv(t, vslot, !fresh, 0, C::BN / 32);
-            if (!(ok = w.wait(&sm.p_full[t], (pph >> t) & 1, kErrTreeWait))) break;
-            tc_fence_after();
-            issue_pv(t, vslot, true, C::BN / 32, C::BN / 16);
-            pph ^= 1u << t;
-            if (!more) {
-              umma_commit_warp(&sm.o_final[t], lead);
+          const bool more = i + step < n, fresh = i < step;
+          const int ks = cur;  // K tile of the next S, behind V in the ring
+          const uint32_t kph = cph;
+          // One tile's part of the step: P.V, then its next S.
+          auto part = [&](auto tc) -> bool {
+            constexpr int t = decltype(tc)::value;
+            if (!issue_pv(tc, vs, fresh)) return false;
+            if (more) {
+              if (!w.wait(&sm.full[ks], kph, kErrTreeWait)) return false;
+              tc_fence_after();
+              issue_s(tc, ks);
             } else {
-              if (!(ok = wait_item(tree_k_item(i + step)))) break;
-              issue_s(t, i + step);
+              umma_commit_warp(&sm.o_final[t], lead);
             }
-          }
+            return true;
+          };
+          if (pair) ok = part(t0) && (!two || part(t1));
+          else ok = (i & 1) ? part(t1) : part(t0);
           if (!ok) break;
-          umma_commit_warp(&sm.empty[vslot], lead);
+          umma_commit_warp(&sm.empty[vs], lead);
           if (more) {
-            umma_commit_warp(&sm.empty[slot_of(tree_k_item(i + step))], lead);
+            umma_commit_warp(&sm.empty[ks], lead);
+            advance();
             if (i + step == n - 1) umma_commit_warp(&sm.q_empty, lead);  // the segment's last S
           }
         }
-        item0 += 2 * n;
         ++seg;
       }
       umma_commit_warp(&sm.teardown, lead);
@@ -452,8 +623,21 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
     int pc = 0, seg = 0;
     uint32_t oph = 0;  // bit i: phase of tile i's next final O
     bool ok = true;
-    for (; ok && tree_next(p, walk, s, first); first = false) {
+    // The scores take 128 of the 192 registers: what the loop over the tiles
+    // does not need stays in shared memory or is computed again.
+    if (lane == 0) sm.walk[warp] = make_int4(walk.b, walk.u, walk.k, walk.rem);
+    __syncwarp();
+    while (ok) {
+      {
+        const int4 at = sm.walk[warp];
+        TreeWalk next{at.x, at.y, at.z, at.w};
+        if (!tree_next(p, sm.order, next, s)) break;
+        __syncwarp();
+        if (lane == 0) sm.walk[warp] = make_int4(next.b, next.u, next.k, next.rem);
+        __syncwarp();
+      }
       const int n = s.n;
+      if (n == 0 && !s.whole) continue;
       const int live = pair ? (s.m0 + p.qpt < p.T ? 2 : 1) : min(n, 2);
       const int qi = s.m0 + (pair ? t * p.qpt : 0) + rq;
       const bool row_in = rq < p.qpt && qi < p.T;       // this thread has a row to write
@@ -461,20 +645,37 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       const int hq = s.hk * p.g + hg;
       const int nt = t < live ? (pair ? n : (n + 1 - t) / 2) : 0;
       float m_use = -INFINITY, l = 0.0f;
-      int lo = 0;  // lowest prefix key the window leaves
-      if (p.win_left >= 0 && row_live) {
-        const int depth = p.tree_depth != nullptr ? p.tree_depth[s.b * p.T + qi] : 0;
-        lo = s.q.base + max(0, min(depth, s.q.n - 1)) - p.win_left;
-      }
-      const uint32_t* bits = p.tree_mask + (static_cast<int64_t>(s.b) * p.T + (row_live ? qi : 0)) * p.words;
       for (int j = 0; j < nt; ++j) {
+        const int j0 = tree_tile(s.q, s.k0 + (pair ? j : 2 * j + t)) * C::BN;
+        const bool masked = j0 + C::BN > s.q.base ||
+                            (p.win_left >= 0 && j0 < s.q.base + s.q.n - p.win_left);
+        // Which keys of a masked tile the row sees, worked out (and its mask
+        // words fetched) while the tensor core computes the scores.
+        uint32_t vis[4] = {0u, 0u, 0u, 0u};
+        if (masked && row_live) {
+          const int64_t node_row = static_cast<int64_t>(s.b) * p.T + qi;
+          const uint32_t* bits = p.tree_mask + node_row * p.words;
+          const int sh0 = j0 - s.q.base;  // first column, counted from node 0
+          const int wd = sh0 >> 5, bit = sh0 & 31;
+          uint32_t wds[5];
+#pragma unroll
+          for (int c = 0; c < 5; ++c)
+            wds[c] = wd + c >= 0 && wd + c < p.words ? __ldg(bits + wd + c) : 0u;
+          int lo = 0;  // lowest key before the nodes that the window leaves
+          if (p.win_left >= 0)
+            lo = s.q.base + max(0, min(__ldg(p.tree_depth + node_row), s.q.n - 1)) - p.win_left;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int k0 = j0 + 32 * c;
+            uint32_t pre = low_bits(s.q.base - k0);  // keys before the nodes
+            if (p.win_left >= 0) pre &= ~low_bits(lo - k0) | low_bits(p.sink_tokens - k0);
+            vis[c] = pre | (__funnelshift_r(wds[c], wds[c + 1], bit) & low_bits(s.q.L - k0));
+          }
+        }
         ok = __all_sync(0xffffffffu, w.wait(&sm.s_full[t], pc & 1, kErrTreeWait));
         if (!ok) break;
         ++pc;
         tc_fence_after();
-        const int j0 = tree_tile(s.q, s.k0 + (pair ? j : 2 * j + t)) * C::BN;
-        const bool masked = j0 + C::BN > s.q.base ||
-                            (p.win_left >= 0 && j0 < s.q.base + s.q.n - p.win_left);
         uint32_t sr[C::BN];
         float raw_max = -INFINITY;
         if constexpr (!SOFTCAP) {
@@ -500,21 +701,6 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
         const float a_coef = SOFTCAP ? -2.0f * p.softcap * kLog2e : p.scale_log2;
         const float b_coef = SOFTCAP ? p.softcap * kLog2e : 0.0f;
         if (masked) {
-          uint32_t vis[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int k0 = j0 + 32 * c, sh = k0 - s.q.base;
-            uint32_t pre = low_bits(-sh);  // keys before the drafted nodes
-            if (p.win_left >= 0) pre &= ~low_bits(lo - k0) | low_bits(p.sink_tokens - k0);
-            uint32_t node = 0;
-            if (sh > -32 && sh < s.q.n) {
-              const int wd = sh >> 5, bit = sh & 31;  // word -1 (none) below the first node
-              const uint32_t w0 = wd >= 0 ? bits[wd] : 0u;
-              const uint32_t w1 = bit != 0 && wd + 1 < p.words ? bits[wd + 1] : 0u;
-              node = __funnelshift_r(w0, w1, bit) & low_bits(s.q.L - k0);
-            }
-            vis[c] = row_live ? pre | node : 0u;
-          }
           constexpr float kDrop = SOFTCAP ? INFINITY : -INFINITY;
 #pragma unroll
           for (int c = 0; c < C::BN; ++c) x[c] = (vis[c >> 5] >> (c & 31)) & 1u ? x[c] : kDrop;
@@ -617,39 +803,57 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
         scale1 *= norm;
       }
       const bool zero = !(l > 0.0f);  // nothing seen: O is 0 whatever the accumulator holds
-      const int slot = cta * 2 + (s.first ? 0 : 1);
+      const int slot = cta * 2 + (s.k0 > 0 ? 0 : 1);  // a piece that starts inside its unit is the first
       const int prow = (pair ? t * 128 : 0) + r;                     // row of the piece
       const int prows = pair ? 256 : 128;
       float* part = p.o_part + static_cast<int64_t>(slot) * prows * D;
-      T* out = reinterpret_cast<T*>(p.o) + ((static_cast<int64_t>(s.b) * p.T + qi) * p.Hq + hq) * D;
+      // Rows of this lane's quad in O, from the tile's first query (-1: no row).
+      T* out = reinterpret_cast<T*>(p.o) + ((static_cast<int64_t>(s.b) * p.T + (qi - rq)) * p.Hq + s.hk * p.g) * D;
+      int orow[4], rrq = (r & ~3) / p.g, rhg = (r & ~3) - rrq * p.g;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        orow[i] = rrq < p.qpt && qi - rq + rrq < p.T ? (rrq * p.Hq + rhg) * D : -1;
+        if (++rhg == p.g) rhg = 0, ++rrq;
+      }
       const int c_beg = pair ? 0 : t * (D / 2), c_end = pair ? D : c_beg + D / 2;
       const bool writes = pair ? t < live || n == 0 : true;
       if (writes) {
         for (int c = c_beg; c < c_end; c += 32) {
-          uint32_t o0[32], o1[32];
-          if (use0) {
-            tmem_ld32(tmem + C::tm_o(pair ? t : 0) + lane_base + c, o0);
-            if (use1) tmem_ld32(tmem + C::tm_o(1) + lane_base + c, o1);
-            tmem_ld_wait();
-            reg_fence(o0);
-            if (use1) reg_fence(o1);
-          }
+          // (one accumulator's columns at a time: both at once spill)
           float v[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            v[i] = 0.0f;
-            if (use0 && !zero) v[i] = __uint_as_float(o0[i]) * scale0;
-            if (use1 && !zero) v[i] = fmaf(__uint_as_float(o1[i]), scale1, v[i]);
+          for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+          if (use0) {
+            uint32_t o0[32];
+            tmem_ld32(tmem + C::tm_o(pair ? t : 0) + lane_base + c, o0);
+            tmem_ld_wait();
+            reg_fence(o0);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = zero ? 0.0f : __uint_as_float(o0[i]) * scale0;
           }
-          if (row_in && s.whole) {
+          if (use1) {
+            uint32_t o1[32];
+            tmem_ld32(tmem + C::tm_o(1) + lane_base + c, o1);
+            tmem_ld_wait();
+            reg_fence(o1);
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              uint32_t w4[4];
+            for (int i = 0; i < 32; ++i) v[i] = zero ? 0.0f : fmaf(__uint_as_float(o1[i]), scale1, v[i]);
+          }
+          if (s.whole) {
+            // A thread's 32 columns of its own row would go out 16 bytes to 32
+            // far apart rows at a time: the four lanes of a quad exchange their
+            // 16-byte pieces (a 4 x 4 transpose) and each store of the warp
+            // covers 64 bytes of 8 rows (the unit's epilogue 9000 -> XXXX cycles).
+            uint32_t w16[16];
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w4[e] = BF16 ? pack_bf16(v[i + 2 * e], v[i + 2 * e + 1]) : pack_f16(v[i + 2 * e], v[i + 2 * e + 1]);
-              *reinterpret_cast<uint4*>(out + c + i) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
-            }
+            for (int e = 0; e < 16; ++e)
+              w16[e] = BF16 ? pack_bf16(v[2 * e], v[2 * e + 1]) : pack_f16(v[2 * e], v[2 * e + 1]);
+            quad_transpose(w16, lane);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)  // row (r & ~3) + i, piece lane & 3
+              if (orow[i] >= 0)
+                *reinterpret_cast<uint4*>(out + orow[i] + c + 8 * (lane & 3)) =
+                    make_uint4(w16[4 * i], w16[4 * i + 1], w16[4 * i + 2], w16[4 * i + 3]);
           } else if (row_in) {
             // [D / 4][rows][4]: a warp's 32 rows are one 512-byte line.
 #pragma unroll
@@ -683,29 +887,21 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
   }
 }
 
-// Merges the pieces of every unit that was cut: block x handles the unit that
-// holds the first tile of CTA x's range, if that tile lies inside the unit and
-// no earlier CTA's first tile does; blockIdx.y picks 32 columns.  Thread = row.
+// Merges the pieces of every unit that was cut: block x does it where CTA x of the
+// tree kernel is the first to begin inside a unit (p.cut), blockIdx.y picks 8
+// columns, a thread is a row.
 //   M = max m_i, O = sum 2^(m_i - M) O_i / (sum 2^(m_i - M) l_i [+ 2^(sink - M)])
+// A unit has up to some twenty pieces that one thread reads one after the other:
+// latency bound, hence narrow column slices, four pieces in flight and one pass
+// with a running maximum.  It is launched with programmatic serialisation, so
+// that only its first read waits for the tree kernel.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(256) attn_tree_merge_kernel(const __grid_constant__ TreeParams p) {
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
-  __shared__ long long scan[16];
-  const long long line = tree_total(p, scan) * p.units;
-  const int G = tree_ctas(p, line), c = blockIdx.x;
-  if (c == 0 || c >= G) return;
-  const long long x = line * c / G;
-  int b;
-  long long cum;
-  tree_locate(p, x, scan, b, cum);
-  const TreeSeq q = tree_seq(p, b);
-  const long long off = x - cum * p.units;
-  const int u = static_cast<int>(off / q.slots);
-  const long long x0 = cum * p.units + static_cast<long long>(u) * q.slots, x1 = x0 + q.slots;
-  // The CTAs whose ranges meet the unit; this block acts for the first inside it.
-  const int c0 = static_cast<int>(((x0 + 1) * G - 1) / line), c1 = static_cast<int>((x1 * G - 1) / line);
-  if (x == x0 || c != c0 + 1) return;
-  const int rb = u / p.Hkv, hk = u - rb * p.Hkv;
+  pdl_wait();
+  const int4 cut = p.cut[blockIdx.x];
+  if (cut.x < 0) return;
+  const int b = cut.x, rb = cut.y / p.Hkv, hk = cut.y - rb * p.Hkv;
   const int prows = p.two_tiles ? 256 : 128;
   const int row = threadIdx.x;  // blockDim.x == prows
   const int t = row >> 7, r = row & 127;
@@ -713,46 +909,60 @@ __global__ void __launch_bounds__(256) attn_tree_merge_kernel(const __grid_const
   const int qi = rb * (p.two_tiles ? 2 : 1) * p.qpt + t * p.qpt + rq;
   if (rq >= p.qpt || qi >= p.T) return;
   const int hq = hk * p.g + hg;
-  const float sl = p.sink != nullptr ? p.sink[hq] * kLog2e : -INFINITY;
-  auto piece = [&](int i) {  // workspace piece of CTA i's part
-    return static_cast<int64_t>(i) * 2 + (line * i / G >= x0 ? 0 : 1);
-  };
-  float M = sl;
-  for (int i = c0; i <= c1; ++i) M = fmaxf(M, p.ml_part[piece(i) * prows + row].x);
-  const float ms = M == -INFINITY ? 0.0f : M;
-  float z = p.sink != nullptr ? ex2_approx(sl - ms) : 0.0f;
-  float acc[32];
+  const int c0 = blockIdx.x - 1, n = cut.z - c0 + 1, col = blockIdx.y * 8;
+  auto piece = [&](int i) { return static_cast<int64_t>(2 * (c0 + i) + (i == 0 ? 1 : 0)); };
+  float M = p.sink != nullptr ? p.sink[hq] * kLog2e : -INFINITY;
+  float z = p.sink != nullptr ? 1.0f : 0.0f;
+  float acc[8];
 #pragma unroll
-  for (int i = 0; i < 32; ++i) acc[i] = 0.0f;
-  const int col = blockIdx.y * 32;
-  for (int i = c0; i <= c1; ++i) {
-    const float2 e = p.ml_part[piece(i) * prows + row];
-    const float wgt = ex2_approx(e.x - ms);
-    z = fmaf(e.y, wgt, z);
-    const float* part = p.o_part + piece(i) * prows * D;
+  for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+  for (int i0 = 0; i0 < n; i0 += 4) {
+    float2 e[4];
+    float4 v0[4], v1[4];
 #pragma unroll
-    for (int k = 0; k < 32; k += 4) {
-      const float4 v = *reinterpret_cast<const float4*>(part + (static_cast<int64_t>((col + k) / 4) * prows + row) * 4);
-      acc[k] = fmaf(v.x, wgt, acc[k]);
-      acc[k + 1] = fmaf(v.y, wgt, acc[k + 1]);
-      acc[k + 2] = fmaf(v.z, wgt, acc[k + 2]);
-      acc[k + 3] = fmaf(v.w, wgt, acc[k + 3]);
+    for (int i = 0; i < 4; ++i) {
+      e[i] = make_float2(-INFINITY, 0.0f);
+      v0[i] = v1[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (i0 + i < n) {
+        const int64_t q = piece(i0 + i);
+        const float4* part = reinterpret_cast<const float4*>(p.o_part + q * prows * D) + (col / 4) * prows + row;
+        e[i] = p.ml_part[q * prows + row];
+        v0[i] = part[0];
+        v1[i] = part[prows];
+      }
+    }
+    const float m = fmaxf(fmaxf(M, fmaxf(e[0].x, e[1].x)), fmaxf(e[2].x, e[3].x));
+    const float ms = m == -INFINITY ? 0.0f : m;
+    const float a = ex2_approx(M - ms);
+    M = m;
+    z *= a;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[k] *= a;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float wgt = ex2_approx(e[i].x - ms);
+      z = fmaf(e[i].y, wgt, z);
+      acc[0] = fmaf(v0[i].x, wgt, acc[0]);
+      acc[1] = fmaf(v0[i].y, wgt, acc[1]);
+      acc[2] = fmaf(v0[i].z, wgt, acc[2]);
+      acc[3] = fmaf(v0[i].w, wgt, acc[3]);
+      acc[4] = fmaf(v1[i].x, wgt, acc[4]);
+      acc[5] = fmaf(v1[i].y, wgt, acc[5]);
+      acc[6] = fmaf(v1[i].z, wgt, acc[6]);
+      acc[7] = fmaf(v1[i].w, wgt, acc[7]);
     }
   }
   const float norm = z > 0.0f ? 1.0f / z : 0.0f;
   T* out = reinterpret_cast<T*>(p.o) + ((static_cast<int64_t>(b) * p.T + qi) * p.Hq + hq) * D + col;
+  uint32_t w4[4];
 #pragma unroll
-  for (int i = 0; i < 32; i += 8) {
-    uint32_t w4[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float lo = acc[i + 2 * e] * norm, hi = acc[i + 2 * e + 1] * norm;
-      w4[e] = BF16 ? pack_bf16(lo, hi) : pack_f16(lo, hi);
-    }
-    *reinterpret_cast<uint4*>(out + i) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+  for (int e = 0; e < 4; ++e) {
+    const float lo = acc[2 * e] * norm, hi = acc[2 * e + 1] * norm;
+    w4[e] = BF16 ? pack_bf16(lo, hi) : pack_f16(lo, hi);
   }
+  *reinterpret_cast<uint4*>(out) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
   if (col == 0 && p.lse != nullptr)
-    p.lse[(static_cast<int64_t>(b) * p.Hq + hq) * p.T + qi] = z > 0.0f ? (ms + __log2f(z)) * kLn2 : -INFINITY;
+    p.lse[(static_cast<int64_t>(b) * p.Hq + hq) * p.T + qi] = z > 0.0f ? (M + __log2f(z)) * kLn2 : -INFINITY;
 }
 
 template <int D, bool BF16, bool SOFTCAP>
@@ -772,8 +982,16 @@ static cudaError_t launch_tree_t(const TreeParams& p, cudaStream_t stream) {
   kern<<<p.grid, C::THREADS, smem, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  attn_tree_merge_kernel<D, BF16><<<dim3(p.grid, D / 32), p.two_tiles ? 256 : 128, 0, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.grid, D / 8);
+  cfg.blockDim = dim3(p.two_tiles ? 256 : 128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_tree_merge_kernel<D, BF16>, p);
 }
 
 template <>
