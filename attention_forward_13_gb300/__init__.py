@@ -12,11 +12,16 @@ raised.  Output tensors are allocated with torch when not given.
     o, lse = attn_splitkv_combine(o_part, lse_part)
     mask, depth = attn_tree_mask(parents)                   # drafted tokens' tree
     o, lse = attn_fwd_paged_tree(q, k_pool, v_pool, block_table, seqlens_k, mask)
+    table, lens, refs = attn_cache_reorder(block_table, seqlens, page_refs, index, page)
+    table, lens, refs, free = attn_cache_reserve(k_pool, v_pool, table, lens, refs, add)
+    lens, refs = attn_cache_accept(k_pool, v_pool, table, lens, refs, path, path_lens, tree_lens)
+    table, refs, page_map = attn_cache_compact(k_pool, v_pool, table, lens, refs)
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 
 import torch
 
@@ -26,7 +31,8 @@ __all__ = ["attn_fwd", "attn_fwd_varlen", "attn_fwd_paged", "attn_splitkv_combin
            "attn_paged_workspace_bytes", "attn_paged_auto_splits", "attn_device_error",
            "attn_selftest_timeout", "attn_last_kernel_name", "attn_paged_window_pages",
            "attn_fwd_paged_noalloc", "attn_dense_schedule", "attn_tree_mask",
-           "attn_tree_workspace_bytes", "attn_fwd_paged_tree", "gqa_pack", "AttnError", "library"]
+           "attn_tree_workspace_bytes", "attn_fwd_paged_tree", "attn_cache_reorder",
+           "attn_cache_reserve", "attn_cache_accept", "attn_cache_compact", "gqa_pack", "AttnError", "library"]
 
 
 class AttnError(RuntimeError):
@@ -58,15 +64,27 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# The current stream's handle without building a Stream object (3 us a call on a
+# Grace host, the query itself 0.1 us).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
+    if stream is None and _raw_stream is not None:
+        return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
 
 
+_NO_SWITCH = contextlib.nullcontext()
+
+
 def _device_of(device):
-    """Makes ``device`` current for a call (its streams, its error word); CPU tensors are
-    left to the call's own checks."""
-    return torch.cuda.device(device) if device.type == "cuda" else contextlib.nullcontext()
+    """Makes ``device`` current for a call (its streams, its error word), where it is not;
+    CPU tensors are left to the call's own checks."""
+    if device.type != "cuda" or device.index == torch.cuda.current_device():
+        return _NO_SWITCH
+    return torch.cuda.device(device)
 
 
 def _opts(scale, causal, softcap, sink, window=None, top_left=False, alibi=None, bias=None,
@@ -317,11 +335,22 @@ def attn_fwd_paged_noalloc(q, k_pool, v_pool, block_table, seqlens_k, num_splits
     return o, lse_t
 
 
-def _on_device(device, tensors, dtype, what):
-    """Each given tensor is contiguous, of ``dtype`` and on ``device``."""
-    for t in tensors:
-        if t is not None and (t.dtype != dtype or t.device != device or not t.is_contiguous()):
-            raise ValueError(f"{what} must be contiguous {dtype} on {device}")
+@functools.lru_cache(maxsize=256)
+def attn_tree_workspace_bytes(T, Hq, Hkv, d) -> int:
+    """Bytes of device memory attn_fwd_paged_tree works in."""
+    return int(library().attn_tree_workspace_bytes(T, Hq, Hkv, d))
+
+
+def _ints(device, **tensors):
+    """Each given tensor is contiguous int32 on ``device``."""
+    for name, t in tensors.items():
+        if t is not None and (t.dtype != torch.int32 or t.device != device or not t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous int32 on {device}")
+
+
+def _data(t):
+    """The address of a tensor for the C library (None: NULL)."""
+    return None if t is None else t.data_ptr()
 
 
 def attn_tree_mask(parents, tree_lens=None, mask=None, depth=None, stream=None):
@@ -329,24 +358,21 @@ def attn_tree_mask(parents, tree_lens=None, mask=None, depth=None, stream=None):
     sequence's last token), tree_lens int32 [B] or None.  Returns (mask int32
     [B,T,ceil(T/32)], its 32 bits per word the nodes a node sees, depth int32 [B,T])."""
     B, T = parents.shape
-    dev = parents.device
+    W, dev = (T + 31) // 32, parents.device
     if mask is None:
-        mask = torch.empty((B, T, (T + 31) // 32), dtype=torch.int32, device=dev)
+        mask = torch.empty((B, T, W), dtype=torch.int32, device=dev)
     if depth is None:
         depth = torch.empty((B, T), dtype=torch.int32, device=dev)
-    _on_device(dev, (parents, tree_lens, mask, depth), torch.int32, "parents, tree_lens, mask and depth")
-    if mask.shape != (B, T, (T + 31) // 32) or depth.shape != (B, T) or \
+    _ints(dev, parents=parents, tree_lens=tree_lens, mask=mask, depth=depth)
+    if mask.shape != (B, T, W) or depth.shape != (B, T) or \
             (tree_lens is not None and tree_lens.shape != (B,)):
         raise ValueError("tree_lens is [B], mask [B,T,ceil(T/32)], depth [B,T]")
+    lib = library()
     with _device_of(dev):
-        st = library().attn_tree_mask(_ptr(parents), _ptr(tree_lens), _ptr(mask), _ptr(depth), B, T,
-                                      _stream(stream))
+        st = lib.attn_tree_mask(_data(parents), _data(tree_lens), _data(mask), _data(depth), B, T,
+                                _stream(stream))
     _check(st, "attn_tree_mask")
     return mask, depth
-
-
-def attn_tree_workspace_bytes(T, Hq, Hkv, d) -> int:
-    return int(library().attn_tree_workspace_bytes(T, Hq, Hkv, d))
 
 
 def attn_fwd_paged_tree(q, k_pool, v_pool, block_table, seqlens_k, tree_mask, tree_lens=None,
@@ -358,40 +384,146 @@ def attn_fwd_paged_tree(q, k_pool, v_pool, block_table, seqlens_k, tree_mask, tr
     with tree_depth limits the earlier positions, the first ``sink_tokens`` staying visible.
     Returns (o [B,T,Hq,d], lse fp32 [B,Hq,T] or None)."""
     B, T, Hq, d = q.shape
-    num_pages, page, Hkv, _ = k_pool.shape
+    num_pages, page, Hkv, dk = k_pool.shape
     dev = q.device
-    _on_device(dev, (q, k_pool, v_pool, o), q.dtype, "q, the pools and o")
-    _on_device(dev, (block_table, seqlens_k, tree_mask, tree_lens, tree_depth), torch.int32,
-               "block_table, seqlens_k and the tree tensors")
     if o is None:
         o = torch.empty_like(q)
     lse_t = lse if isinstance(lse, torch.Tensor) else None
     if lse is True:
         lse_t = torch.empty((B, Hq, T), dtype=torch.float32, device=dev)
-    _on_device(dev, (lse_t,), torch.float32, "lse")
-    if k_pool.shape[3] != d or v_pool.shape != k_pool.shape or block_table.dim() != 2 or \
+    for t in (q, k_pool, v_pool, o):
+        if t.dtype != q.dtype or t.device != dev or not t.is_contiguous():
+            raise ValueError("q, the pools and o must be contiguous, of one type and on one device")
+    _ints(dev, block_table=block_table, seqlens_k=seqlens_k, tree_mask=tree_mask, tree_lens=tree_lens,
+          tree_depth=tree_depth)
+    if dk != d or v_pool.shape != k_pool.shape or block_table.dim() != 2 or \
             block_table.shape[0] != B or seqlens_k.shape != (B,) or \
             tree_mask.shape != (B, T, (T + 31) // 32) or o.shape != q.shape or \
             (tree_lens is not None and tree_lens.shape != (B,)) or \
             (tree_depth is not None and tree_depth.shape != (B, T)) or \
-            (lse_t is not None and lse_t.shape != (B, Hq, T)):
+            (lse_t is not None and (lse_t.shape != (B, Hq, T) or lse_t.dtype != torch.float32 or
+                                    lse_t.device != dev or not lse_t.is_contiguous())):
         raise ValueError("shapes: q, o [B,T,Hq,d], pools [pages,page,Hkv,d], block_table [B,max_pages], "
-                         "seqlens_k, tree_lens [B], tree_mask [B,T,ceil(T/32)], tree_depth [B,T], lse [B,Hq,T]")
-    need = attn_tree_workspace_bytes(T, Hq, Hkv, d)
+                         "seqlens_k, tree_lens [B], tree_mask [B,T,ceil(T/32)], tree_depth [B,T], "
+                         "lse fp32 [B,Hq,T]")
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = torch.empty(attn_tree_workspace_bytes(T, Hq, Hkv, d), dtype=torch.uint8, device=dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous on the same device")
-    sink = _check_sink(sink, Hq, dev)
+    if sink is not None:
+        sink = _check_sink(sink, Hq, dev)
     opts = _opts(scale, False, softcap, sink, window, sink_tokens=sink_tokens)
+    lib = library()
     with _device_of(dev):
-        st = library().attn_fwd_paged_tree(
-            _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_table), _ptr(seqlens_k), _ptr(tree_mask),
-            _ptr(tree_lens), _ptr(tree_depth), _ptr(o), _ptr(lse_t), B, T, Hq, Hkv, d, _dtype_code(q),
-            page, num_pages, block_table.shape[1], _ptr(workspace),
+        st = lib.attn_fwd_paged_tree(
+            _data(q), _data(k_pool), _data(v_pool), _data(block_table), _data(seqlens_k), _data(tree_mask),
+            _data(tree_lens), _data(tree_depth), _data(o), _data(lse_t), B, T, Hq, Hkv, d, _dtype_code(q),
+            page, num_pages, block_table.shape[1], _data(workspace),
             workspace.numel() * workspace.element_size(), ctypes.byref(opts), _stream(stream))
     _check(st, "attn_fwd_paged_tree")
     return o, lse_t
+
+
+def _pools(k_pool, v_pool, page_refs):
+    """(layers, num_pages, page, row bytes) of pools [num_pages,page,Hkv,d] or
+    [layers,num_pages,page,Hkv,d]."""
+    if k_pool.shape != v_pool.shape or k_pool.dtype != v_pool.dtype or k_pool.device != v_pool.device or \
+            k_pool.dim() not in (4, 5) or not k_pool.is_contiguous() or not v_pool.is_contiguous():
+        raise ValueError("the pools must be contiguous [num_pages,page,Hkv,d] or "
+                         "[layers,num_pages,page,Hkv,d], alike")
+    *layers, num_pages, page, Hkv, d = k_pool.shape
+    if page_refs.shape != (num_pages,):
+        raise ValueError("page_refs must be [num_pages]")
+    return layers[0] if layers else 1, num_pages, page, Hkv * d * k_pool.element_size()
+
+
+def _cache_state(dev, block_table, seqlens, page_refs, **more):
+    _ints(dev, block_table=block_table, seqlens=seqlens, page_refs=page_refs, **more)
+    B, max_pages = block_table.shape
+    if seqlens.shape != (B,):
+        raise ValueError("seqlens must be [B] for a block_table [B,max_pages]")
+    for name, t in more.items():
+        if t is not None and t.shape[0] != B:
+            raise ValueError(f"{name} must have one entry per sequence")
+    return B, max_pages
+
+
+def attn_cache_reorder(block_table, seqlens, page_refs, index, page_size, stream=None):
+    """New sequence b is old sequence index[b] (int32 [B_out]; -1: an empty one): forks where
+    an index repeats, permutes, frees what nobody takes.  Returns (block_table [B_out,
+    max_pages], seqlens [B_out], page_refs)."""
+    dev = block_table.device
+    B, max_pages = _cache_state(dev, block_table, seqlens, page_refs)
+    _ints(dev, index=index)
+    n = index.shape[0]
+    table_out = torch.empty((n, max_pages), dtype=torch.int32, device=dev)
+    lens_out, refs_out = torch.empty_like(index), torch.empty_like(page_refs)
+    lib = library()
+    with _device_of(dev):
+        st = lib.attn_cache_reorder(_data(block_table), _data(seqlens), _data(page_refs), _data(index),
+                                    _data(table_out), _data(lens_out), _data(refs_out), B, n, max_pages,
+                                    page_refs.shape[0], int(page_size), _stream(stream))
+    _check(st, "attn_cache_reorder")
+    return table_out, lens_out, refs_out
+
+
+def attn_cache_reserve(k_pool, v_pool, block_table, seqlens, page_refs, add, stream=None):
+    """Room for add[b] (int32 [B]) more tokens per sequence; shared partly filled last pages
+    are copied first.  Returns (block_table, seqlens + add, page_refs, free int32 [1]: the
+    free pages left, or minus the pages missing, and then nothing has changed)."""
+    dev = block_table.device
+    B, max_pages = _cache_state(dev, block_table, seqlens, page_refs, add=add)
+    layers, num_pages, page, row = _pools(k_pool, v_pool, page_refs)
+    table_out, lens_out, refs_out = (torch.empty_like(t) for t in (block_table, seqlens, page_refs))
+    free = torch.empty(1, dtype=torch.int32, device=dev)
+    lib = library()
+    with _device_of(dev):
+        st = lib.attn_cache_reserve(_data(k_pool), _data(v_pool), _data(block_table), _data(seqlens),
+                                    _data(page_refs), _data(add), _data(table_out), _data(lens_out),
+                                    _data(refs_out), _data(free), B, max_pages, num_pages, page, layers,
+                                    row, _stream(stream))
+    _check(st, "attn_cache_reserve")
+    return table_out, lens_out, refs_out, free
+
+
+def attn_cache_accept(k_pool, v_pool, block_table, seqlens, page_refs, path, path_lens, tree_lens,
+                      stream=None):
+    """Keeps of each sequence's drafted nodes (the last tree_lens[b] positions) the nodes
+    path[b, :path_lens[b]] (int32 [B,A], rising), moved together behind the tokens before
+    them, and gives the pages past them back.  Returns (seqlens, page_refs); the pools are
+    updated in place, the table stays."""
+    dev = block_table.device
+    B, max_pages = _cache_state(dev, block_table, seqlens, page_refs, path=path, path_lens=path_lens,
+                                tree_lens=tree_lens)
+    layers, num_pages, page, row = _pools(k_pool, v_pool, page_refs)
+    if path.dim() != 2 or tree_lens is None:
+        raise ValueError("path must be [B,A] and tree_lens [B]")
+    lens_out, refs_out = torch.empty_like(seqlens), torch.empty_like(page_refs)
+    lib = library()
+    with _device_of(dev):
+        st = lib.attn_cache_accept(_data(k_pool), _data(v_pool), _data(block_table), _data(seqlens),
+                                   _data(page_refs), _data(path), _data(path_lens), _data(tree_lens),
+                                   _data(lens_out), _data(refs_out), B, path.shape[1], max_pages * page,
+                                   max_pages, num_pages, page, layers, row, _stream(stream))
+    _check(st, "attn_cache_accept")
+    return lens_out, refs_out
+
+
+def attn_cache_compact(k_pool, v_pool, block_table, seqlens, page_refs, stream=None):
+    """Moves the live pages to the pool's front (in place).  Returns (block_table, page_refs,
+    page_map int32 [num_pages]: where each live page is now, -1 for a free one)."""
+    dev = block_table.device
+    B, max_pages = _cache_state(dev, block_table, seqlens, page_refs)
+    layers, num_pages, page, row = _pools(k_pool, v_pool, page_refs)
+    table_out, refs_out, page_map = (torch.empty_like(t) for t in (block_table, page_refs, page_refs))
+    work = torch.empty(num_pages + 1, dtype=torch.int32, device=dev)
+    lib = library()
+    with _device_of(dev):
+        st = lib.attn_cache_compact(_data(k_pool), _data(v_pool), _data(block_table), _data(seqlens),
+                                    _data(page_refs), _data(table_out), _data(refs_out), _data(page_map),
+                                    _data(work), B, max_pages, num_pages, page, layers, row, _stream(stream))
+    _check(st, "attn_cache_compact")
+    return table_out, refs_out, page_map
 
 
 def attn_splitkv_combine(o_partial, lse_partial, sink=None, dtype=torch.bfloat16, o=None,

@@ -46,7 +46,6 @@ enum ErrBits : uint32_t {
   kErrTreeTeardown = 23,
   kErrTreeBadParent = 24,
   kErrCacheBadIndex = 25,
-  kErrCacheFull = 26,
 };
 
 // Element types of a prefill instantiation: fp16 / bf16 end to end, or e4m3

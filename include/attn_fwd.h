@@ -324,6 +324,72 @@ int attn_paged_window_pages(int Lq, int page_size, int max_pages_per_seq, const 
 attn_status attn_dense_schedule(int B, int Hq, int Hkv, int Lq, int Lk, const attn_opts* opts,
                                 int grid, int32_t* off, int32_t* item);
 
+/*
+ * Upkeep of a paged cache on the device.  The state of a cache is
+ *   block_table int32 [B][max_pages], seqlens int32 [B]: sequence b holds the
+ *   first ceil(seqlens[b] / page_size) entries of its row; and page_refs int32
+ *   [num_pages]: how many table entries hold each page (more where something
+ *   else, a prefix store say, holds it too); 0 marks a free page.
+ * The four calls below take that state and write the next one to *_out buffers
+ * (table entries past the held ones are written as -1).  An output may not
+ * overlap an input, except refs_out = page_refs in attn_cache_reorder and
+ * attn_cache_accept.  Pools are [layers][num_pages][page_size][row]: the same
+ * table for every layer, row_bytes = Hkv * d * element size, a multiple of 16
+ * (any element type and head dimension).  page_size as for attn_fwd_paged;
+ * B <= 8192.  An index out of range never faults: the entry is left out, and
+ * the device error word's bit for bad cache indices is set.  All are
+ * deterministic, need no setting of anything beforehand and can be captured.
+ *
+ * attn_cache_reorder -- new sequence b is old sequence index[b] (int32 [B_out];
+ * -1: an empty one).  Forks where an index repeats (the pages are shared),
+ * permutes (beam search), frees what nobody takes.
+ */
+attn_status attn_cache_reorder(const int32_t* block_table, const int32_t* seqlens,
+                               const int32_t* page_refs, const int32_t* index, int32_t* table_out,
+                               int32_t* seqlens_out, int32_t* refs_out, int B_in, int B_out,
+                               int max_pages, int num_pages, int page_size, void* stream);
+
+/* attn_cache_reserve -- room for add[b] >= 0 more tokens per sequence (seqlens_out =
+ * seqlens + add), before their rows are written.  New pages are the free ones
+ * in rising order, dealt to the sequences in order.  A sequence that grows out
+ * of a partly filled last page that others hold gets a copy of it first
+ * (copy-on-write, in order: the last holder keeps the page).  All or nothing:
+ * *free_out (int32) is the number of free pages left, or minus the number
+ * missing, and then nothing has changed.  A sequence that would outgrow its
+ * table row is an error: nothing changes, *free_out = -num_pages - 1. */
+attn_status attn_cache_reserve(void* k_pool, void* v_pool, const int32_t* block_table,
+                               const int32_t* seqlens, const int32_t* page_refs, const int32_t* add,
+                               int32_t* table_out, int32_t* seqlens_out, int32_t* refs_out,
+                               int32_t* free_out, int B, int max_pages, int num_pages, int page_size,
+                               int layers, int64_t row_bytes, void* stream);
+
+/* attn_cache_accept -- after a draft tree has been verified: of the last n_b =
+ * tree_lens[b] (T without tree_lens) positions of each sequence the nodes
+ * path[b][0 .. path_lens[b] - 1] (int32 [B][A], strictly rising, a root-to-leaf
+ * path say) stay, their rows moved together behind the tokens before the tree:
+ * seqlens_out[b] = seqlens[b] - n_b + path_lens[b].  The pages past that are
+ * given back (their counts drop by one; table entries past the held ones are
+ * ignored everywhere, so the table itself does not change).  path_lens[b] = 0
+ * drops the whole tree.  A path that stops rising or leaves the tree is an
+ * error and ends there.  The nodes' rows must not be shared with another
+ * sequence (attn_cache_reserve sees to it). */
+attn_status attn_cache_accept(void* k_pool, void* v_pool, const int32_t* block_table,
+                              const int32_t* seqlens, const int32_t* page_refs, const int32_t* path,
+                              const int32_t* path_lens, const int32_t* tree_lens, int32_t* seqlens_out,
+                              int32_t* refs_out, int B, int A, int T, int max_pages, int num_pages,
+                              int page_size, int layers, int64_t row_bytes, void* stream);
+
+/* attn_cache_compact -- closes the pool's holes: with n live pages, the live pages
+ * numbered n and above move into the free ones below n (the k-th into the
+ * k-th), after which pages n .. num_pages - 1 are free.  page_map int32
+ * [num_pages]: where each live page is now, -1 for a free one (for holders
+ * outside the table).  workspace: int32 [num_pages + 1], nothing to be set. */
+attn_status attn_cache_compact(void* k_pool, void* v_pool, const int32_t* block_table,
+                               const int32_t* seqlens, const int32_t* page_refs, int32_t* table_out,
+                               int32_t* refs_out, int32_t* page_map, int32_t* workspace, int B,
+                               int max_pages, int num_pages, int page_size, int layers,
+                               int64_t row_bytes, void* stream);
+
 /* Human-readable name of a status. */
 const char* attn_status_string(attn_status status);
 

@@ -157,3 +157,55 @@ def test_parity(case):
     check(o, lse, ro, rl, "tree")
     o2, lse2 = A.attn_fwd_paged_tree(*args, **kw)  # the same bits every time
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_refusals_before_a_launch():
+    """Host-side checks of the tree entry points (no GPU needed)."""
+    lib = A.library()
+    p = 1 << 12
+
+    def tree(opts=None, **k):
+        a = dict(q=p, k=p, mask=p, depth=None, o=p, B=2, T=8, Hq=8, Hkv=2, d=128, dt=1, page=64, num=9, w=4,
+                 ws=p, wb=1 << 30)
+        a.update(k)
+        o = _lib.attn_opts()
+        for name, v in (opts or {}).items():
+            setattr(o, name, v)
+        return lib.attn_fwd_paged_tree(a["q"], a["k"], p, p, p, a["mask"], None, a["depth"], a["o"], None, a["B"],
+                                       a["T"], a["Hq"], a["Hkv"], a["d"], a["dt"], a["page"], a["num"], a["w"],
+                                       a["ws"], a["wb"], ctypes.byref(o), None)
+
+    assert tree(B=0) == 0 and tree(T=0) == 0
+    assert tree(Hq=9) == 1 and tree(q=None) == 1 and tree(k=p + 8) == 1 and tree(mask=p + 1) == 1
+    assert tree(dt=2) == 1 and tree(d=96) == 2 and tree(page=8) == 2 and tree(T=1025) == 2
+    assert tree(Hq=258, Hkv=2) == 2
+    assert tree(ws=None) == 1 and tree(ws=p + 4) == 1
+    need = A.attn_tree_workspace_bytes(8, 8, 2, 128)
+    assert need > 0 and tree(wb=need - 1) == 1
+    assert tree({"causal": 1}) == 2 and tree({"top_left": 1}) == 2 and tree({"alibi_slopes": p}) == 2
+    assert tree({"bias": p}) == 2
+    assert tree({"use_window": 1, "window_left": 4, "window_right": 0}, depth=p) == 2
+    assert tree({"use_window": 1, "window_left": 4, "window_right": -1}) == 1     # depths are missing
+    assert tree({"sink_tokens": -1}) == 1
+    assert A.attn_tree_workspace_bytes(40, 8, 2, 128) > need  # two query tiles
+    assert lib.attn_tree_mask(p, None, p, None, 2, 1025, None) == 2
+    assert lib.attn_tree_mask(p, None, None, None, 2, 8, None) == 1
+    assert lib.attn_tree_mask(p + 2, None, p, None, 2, 8, None) == 1
+    assert lib.attn_tree_mask(None, None, None, None, 0, 8, None) == 0
+
+
+def test_python_checks():
+    q = torch.zeros(2, 4, 8, 64, dtype=torch.bfloat16)
+    kp = torch.zeros(3, 16, 2, 64, dtype=torch.bfloat16)
+    bt, sl = torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    mask = torch.zeros(2, 4, 1, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        A.attn_fwd_paged_tree(q, kp.half(), kp.half(), bt, sl, mask)
+    with pytest.raises(ValueError):
+        A.attn_fwd_paged_tree(q, kp, kp, bt, sl.long(), mask)
+    with pytest.raises(ValueError):
+        A.attn_fwd_paged_tree(q, kp, kp, bt, sl, mask[:, :3])
+    with pytest.raises(ValueError):
+        A.attn_fwd_paged_tree(q, kp, kp, bt[:1], sl, mask)
+    with pytest.raises(ValueError):
+        A.attn_tree_mask(torch.zeros(2, 4))
