@@ -19,7 +19,6 @@ raised.  Output tensors are allocated with torch when not given.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 
@@ -29,7 +28,7 @@ from . import _lib
 
 __all__ = ["attn_fwd", "attn_fwd_varlen", "attn_fwd_paged", "attn_splitkv_combine",
            "attn_paged_workspace_bytes", "attn_paged_auto_splits", "attn_device_error",
-           "attn_selftest_timeout", "attn_last_kernel_name", "attn_paged_window_pages",
+           "attn_selftest_timeout", "attn_last_kernel_name", "attn_paged_window_pages", "attn_paged_keep_splits",
            "attn_fwd_paged_noalloc", "attn_dense_schedule", "attn_tree_mask",
            "attn_tree_workspace_bytes", "attn_fwd_paged_tree", "attn_cache_reorder",
            "attn_cache_reserve", "attn_cache_accept", "attn_cache_compact", "gqa_pack", "AttnError", "library"]
@@ -42,7 +41,7 @@ class AttnError(RuntimeError):
 
 
 def library() -> ctypes.CDLL:
-    return _lib.load()
+    return _lib._lib or _lib.load()
 
 
 def _check(status: int, fn: str):
@@ -76,15 +75,17 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-_NO_SWITCH = contextlib.nullcontext()
-
-
-def _device_of(device):
-    """Makes ``device`` current for a call (its streams, its error word), where it is not;
-    CPU tensors are left to the call's own checks."""
-    if device.type != "cuda" or device.index == torch.cuda.current_device():
-        return _NO_SWITCH
-    return torch.cuda.device(device)
+def _call(fn, device, stream, *args):
+    """Calls a library function whose last argument is the stream, with ``device`` current."""
+    here = torch.cuda.current_device()
+    if device.type != "cuda":
+        raise ValueError("the tensors must be on a CUDA device")
+    if device.index != here:
+        with torch.cuda.device(device):
+            return fn(*args, _stream(stream))
+    if stream is None and _raw_stream is not None:
+        return fn(*args, _raw_stream(here))
+    return fn(*args, _stream(stream))
 
 
 def _opts(scale, causal, softcap, sink, window=None, top_left=False, alibi=None, bias=None,
@@ -224,6 +225,11 @@ def attn_paged_auto_splits(B, Hkv, max_pages_per_seq) -> int:
     return int(library().attn_paged_auto_splits(B, Hkv, max_pages_per_seq))
 
 
+def attn_paged_keep_splits(B, Hkv, page_size, window_pages) -> int:
+    """The split count of calls with ``sink_tokens`` over windows of this many pages."""
+    return int(library().attn_paged_keep_splits(B, Hkv, page_size, window_pages))
+
+
 def attn_paged_window_pages(Lq, page_size, max_pages_per_seq, window=None, causal=False,
                             top_left=False, sink_tokens=0) -> int:
     """Pages of one sequence the paged split layout tiles (W of attn_fwd_paged)."""
@@ -274,9 +280,11 @@ def attn_fwd_paged(q, k_pool, v_pool, block_table, seqlens_k, num_splits=0, o=No
     if Lq * (Hq // Hkv) > 16:
         num_splits = 1  # chunked prefill: the prefill kernel, no split-KV scratch
     elif num_splits == 0:
-        num_splits = attn_paged_auto_splits(
-            B, Hkv, attn_paged_window_pages(Lq, page, max_pages, window, causal, top_left,
-                                            sink_tokens))
+        pages = attn_paged_window_pages(Lq, page, max_pages, window, causal, top_left, sink_tokens)
+        if sink_tokens > 0 and window is not None and window[0] >= 0:
+            num_splits = attn_paged_keep_splits(B, Hkv, page, pages)
+        else:
+            num_splits = attn_paged_auto_splits(B, Hkv, pages)
     if o is None:
         o = torch.empty((B, Lq, Hq, d), dtype=q.dtype, device=q.device)
     lse_t = None
@@ -341,11 +349,11 @@ def attn_tree_workspace_bytes(T, Hq, Hkv, d) -> int:
     return int(library().attn_tree_workspace_bytes(T, Hq, Hkv, d))
 
 
-def _ints(device, **tensors):
+def _ints(device, names, *tensors):
     """Each given tensor is contiguous int32 on ``device``."""
-    for name, t in tensors.items():
-        if t is not None and (t.dtype != torch.int32 or t.device != device or not t.is_contiguous()):
-            raise ValueError(f"{name} must be contiguous int32 on {device}")
+    for t in tensors:
+        if t is not None and not (t.dtype is torch.int32 and t.device == device and t.is_contiguous()):
+            raise ValueError(f"{names} must be contiguous int32 on {device}")
 
 
 def _data(t):
@@ -363,15 +371,12 @@ def attn_tree_mask(parents, tree_lens=None, mask=None, depth=None, stream=None):
         mask = torch.empty((B, T, W), dtype=torch.int32, device=dev)
     if depth is None:
         depth = torch.empty((B, T), dtype=torch.int32, device=dev)
-    _ints(dev, parents=parents, tree_lens=tree_lens, mask=mask, depth=depth)
+    _ints(dev, "parents, tree_lens, mask and depth", parents, tree_lens, mask, depth)
     if mask.shape != (B, T, W) or depth.shape != (B, T) or \
             (tree_lens is not None and tree_lens.shape != (B,)):
         raise ValueError("tree_lens is [B], mask [B,T,ceil(T/32)], depth [B,T]")
-    lib = library()
-    with _device_of(dev):
-        st = lib.attn_tree_mask(_data(parents), _data(tree_lens), _data(mask), _data(depth), B, T,
-                                _stream(stream))
-    _check(st, "attn_tree_mask")
+    _check(_call(library().attn_tree_mask, dev, stream, parents.data_ptr(), _data(tree_lens),
+                 mask.data_ptr(), depth.data_ptr(), B, T), "attn_tree_mask")
     return mask, depth
 
 
@@ -394,8 +399,8 @@ def attn_fwd_paged_tree(q, k_pool, v_pool, block_table, seqlens_k, tree_mask, tr
     for t in (q, k_pool, v_pool, o):
         if t.dtype != q.dtype or t.device != dev or not t.is_contiguous():
             raise ValueError("q, the pools and o must be contiguous, of one type and on one device")
-    _ints(dev, block_table=block_table, seqlens_k=seqlens_k, tree_mask=tree_mask, tree_lens=tree_lens,
-          tree_depth=tree_depth)
+    _ints(dev, "block_table, seqlens_k and the tree tensors", block_table, seqlens_k, tree_mask, tree_lens,
+          tree_depth)
     if dk != d or v_pool.shape != k_pool.shape or block_table.dim() != 2 or \
             block_table.shape[0] != B or seqlens_k.shape != (B,) or \
             tree_mask.shape != (B, T, (T + 31) // 32) or o.shape != q.shape or \
@@ -413,13 +418,11 @@ def attn_fwd_paged_tree(q, k_pool, v_pool, block_table, seqlens_k, tree_mask, tr
     if sink is not None:
         sink = _check_sink(sink, Hq, dev)
     opts = _opts(scale, False, softcap, sink, window, sink_tokens=sink_tokens)
-    lib = library()
-    with _device_of(dev):
-        st = lib.attn_fwd_paged_tree(
-            _data(q), _data(k_pool), _data(v_pool), _data(block_table), _data(seqlens_k), _data(tree_mask),
-            _data(tree_lens), _data(tree_depth), _data(o), _data(lse_t), B, T, Hq, Hkv, d, _dtype_code(q),
-            page, num_pages, block_table.shape[1], _data(workspace),
-            workspace.numel() * workspace.element_size(), ctypes.byref(opts), _stream(stream))
+    st = _call(library().attn_fwd_paged_tree, dev, stream, q.data_ptr(), k_pool.data_ptr(),
+               v_pool.data_ptr(), block_table.data_ptr(), seqlens_k.data_ptr(), tree_mask.data_ptr(),
+               _data(tree_lens), _data(tree_depth), o.data_ptr(), _data(lse_t), B, T, Hq, Hkv, d,
+               _dtype_code(q), page, num_pages, block_table.shape[1], workspace.data_ptr(),
+               workspace.numel() * workspace.element_size(), ctypes.byref(opts))
     _check(st, "attn_fwd_paged_tree")
     return o, lse_t
 
@@ -427,43 +430,43 @@ def attn_fwd_paged_tree(q, k_pool, v_pool, block_table, seqlens_k, tree_mask, tr
 def _pools(k_pool, v_pool, page_refs):
     """(layers, num_pages, page, row bytes) of pools [num_pages,page,Hkv,d] or
     [layers,num_pages,page,Hkv,d]."""
-    if k_pool.shape != v_pool.shape or k_pool.dtype != v_pool.dtype or k_pool.device != v_pool.device or \
-            k_pool.dim() not in (4, 5) or not k_pool.is_contiguous() or not v_pool.is_contiguous():
+    shape = k_pool.shape
+    if shape != v_pool.shape or k_pool.dtype is not v_pool.dtype or len(shape) not in (4, 5) or \
+            not k_pool.is_contiguous() or not v_pool.is_contiguous() or \
+            not k_pool.device == v_pool.device == page_refs.device:
         raise ValueError("the pools must be contiguous [num_pages,page,Hkv,d] or "
-                         "[layers,num_pages,page,Hkv,d], alike")
-    *layers, num_pages, page, Hkv, d = k_pool.shape
-    if page_refs.shape != (num_pages,):
+                         "[layers,num_pages,page,Hkv,d], alike, on the tables' device")
+    num_pages, page, Hkv, d = shape[-4:]
+    if page_refs.shape[0] != num_pages:
         raise ValueError("page_refs must be [num_pages]")
-    return layers[0] if layers else 1, num_pages, page, Hkv * d * k_pool.element_size()
+    return shape[0] if len(shape) == 5 else 1, num_pages, page, Hkv * d * k_pool.element_size()
 
 
-def _cache_state(dev, block_table, seqlens, page_refs, **more):
-    _ints(dev, block_table=block_table, seqlens=seqlens, page_refs=page_refs, **more)
+def _cache_state(block_table, seqlens, page_refs, *per_sequence):
+    """(device, B, max_pages) of a cache's tables, checked with further int32 tensors that
+    have one entry per sequence."""
+    dev = block_table.device
+    _ints(dev, "the cache's tables and what goes with them", block_table, seqlens, page_refs, *per_sequence)
     B, max_pages = block_table.shape
-    if seqlens.shape != (B,):
-        raise ValueError("seqlens must be [B] for a block_table [B,max_pages]")
-    for name, t in more.items():
-        if t is not None and t.shape[0] != B:
-            raise ValueError(f"{name} must have one entry per sequence")
-    return B, max_pages
+    for t in (seqlens, *per_sequence):
+        if t.shape[0] != B:
+            raise ValueError("one entry per sequence (row of block_table) is needed")
+    return dev, B, max_pages
 
 
 def attn_cache_reorder(block_table, seqlens, page_refs, index, page_size, stream=None):
     """New sequence b is old sequence index[b] (int32 [B_out]; -1: an empty one): forks where
     an index repeats, permutes, frees what nobody takes.  Returns (block_table [B_out,
     max_pages], seqlens [B_out], page_refs)."""
-    dev = block_table.device
-    B, max_pages = _cache_state(dev, block_table, seqlens, page_refs)
-    _ints(dev, index=index)
+    dev, B, max_pages = _cache_state(block_table, seqlens, page_refs)
+    _ints(dev, "index", index)
     n = index.shape[0]
     table_out = torch.empty((n, max_pages), dtype=torch.int32, device=dev)
     lens_out, refs_out = torch.empty_like(index), torch.empty_like(page_refs)
-    lib = library()
-    with _device_of(dev):
-        st = lib.attn_cache_reorder(_data(block_table), _data(seqlens), _data(page_refs), _data(index),
-                                    _data(table_out), _data(lens_out), _data(refs_out), B, n, max_pages,
-                                    page_refs.shape[0], int(page_size), _stream(stream))
-    _check(st, "attn_cache_reorder")
+    _check(_call(library().attn_cache_reorder, dev, stream, block_table.data_ptr(), seqlens.data_ptr(),
+                 page_refs.data_ptr(), index.data_ptr(), table_out.data_ptr(), lens_out.data_ptr(),
+                 refs_out.data_ptr(), B, n, max_pages, page_refs.shape[0], int(page_size)),
+           "attn_cache_reorder")
     return table_out, lens_out, refs_out
 
 
@@ -471,18 +474,14 @@ def attn_cache_reserve(k_pool, v_pool, block_table, seqlens, page_refs, add, str
     """Room for add[b] (int32 [B]) more tokens per sequence; shared partly filled last pages
     are copied first.  Returns (block_table, seqlens + add, page_refs, free int32 [1]: the
     free pages left, or minus the pages missing, and then nothing has changed)."""
-    dev = block_table.device
-    B, max_pages = _cache_state(dev, block_table, seqlens, page_refs, add=add)
+    dev, B, max_pages = _cache_state(block_table, seqlens, page_refs, add)
     layers, num_pages, page, row = _pools(k_pool, v_pool, page_refs)
-    table_out, lens_out, refs_out = (torch.empty_like(t) for t in (block_table, seqlens, page_refs))
-    free = torch.empty(1, dtype=torch.int32, device=dev)
-    lib = library()
-    with _device_of(dev):
-        st = lib.attn_cache_reserve(_data(k_pool), _data(v_pool), _data(block_table), _data(seqlens),
-                                    _data(page_refs), _data(add), _data(table_out), _data(lens_out),
-                                    _data(refs_out), _data(free), B, max_pages, num_pages, page, layers,
-                                    row, _stream(stream))
-    _check(st, "attn_cache_reserve")
+    table_out, lens_out = torch.empty_like(block_table), torch.empty_like(seqlens)
+    refs_out, free = torch.empty_like(page_refs), torch.empty(1, dtype=torch.int32, device=dev)
+    _check(_call(library().attn_cache_reserve, dev, stream, k_pool.data_ptr(), v_pool.data_ptr(),
+                 block_table.data_ptr(), seqlens.data_ptr(), page_refs.data_ptr(), add.data_ptr(),
+                 table_out.data_ptr(), lens_out.data_ptr(), refs_out.data_ptr(), free.data_ptr(), B,
+                 max_pages, num_pages, page, layers, row), "attn_cache_reserve")
     return table_out, lens_out, refs_out, free
 
 
@@ -492,37 +491,31 @@ def attn_cache_accept(k_pool, v_pool, block_table, seqlens, page_refs, path, pat
     path[b, :path_lens[b]] (int32 [B,A], rising), moved together behind the tokens before
     them, and gives the pages past them back.  Returns (seqlens, page_refs); the pools are
     updated in place, the table stays."""
-    dev = block_table.device
-    B, max_pages = _cache_state(dev, block_table, seqlens, page_refs, path=path, path_lens=path_lens,
-                                tree_lens=tree_lens)
+    dev, B, max_pages = _cache_state(block_table, seqlens, page_refs, path, path_lens, tree_lens)
     layers, num_pages, page, row = _pools(k_pool, v_pool, page_refs)
-    if path.dim() != 2 or tree_lens is None:
-        raise ValueError("path must be [B,A] and tree_lens [B]")
+    if path.dim() != 2:
+        raise ValueError("path must be [B,A]")
     lens_out, refs_out = torch.empty_like(seqlens), torch.empty_like(page_refs)
-    lib = library()
-    with _device_of(dev):
-        st = lib.attn_cache_accept(_data(k_pool), _data(v_pool), _data(block_table), _data(seqlens),
-                                   _data(page_refs), _data(path), _data(path_lens), _data(tree_lens),
-                                   _data(lens_out), _data(refs_out), B, path.shape[1], max_pages * page,
-                                   max_pages, num_pages, page, layers, row, _stream(stream))
-    _check(st, "attn_cache_accept")
+    _check(_call(library().attn_cache_accept, dev, stream, k_pool.data_ptr(), v_pool.data_ptr(),
+                 block_table.data_ptr(), seqlens.data_ptr(), page_refs.data_ptr(), path.data_ptr(),
+                 path_lens.data_ptr(), tree_lens.data_ptr(), lens_out.data_ptr(), refs_out.data_ptr(), B,
+                 path.shape[1], max_pages * page, max_pages, num_pages, page, layers, row),
+           "attn_cache_accept")
     return lens_out, refs_out
 
 
 def attn_cache_compact(k_pool, v_pool, block_table, seqlens, page_refs, stream=None):
     """Moves the live pages to the pool's front (in place).  Returns (block_table, page_refs,
     page_map int32 [num_pages]: where each live page is now, -1 for a free one)."""
-    dev = block_table.device
-    B, max_pages = _cache_state(dev, block_table, seqlens, page_refs)
+    dev, B, max_pages = _cache_state(block_table, seqlens, page_refs)
     layers, num_pages, page, row = _pools(k_pool, v_pool, page_refs)
-    table_out, refs_out, page_map = (torch.empty_like(t) for t in (block_table, page_refs, page_refs))
+    table_out, refs_out = torch.empty_like(block_table), torch.empty_like(page_refs)
+    page_map = torch.empty_like(page_refs)
     work = torch.empty(num_pages + 1, dtype=torch.int32, device=dev)
-    lib = library()
-    with _device_of(dev):
-        st = lib.attn_cache_compact(_data(k_pool), _data(v_pool), _data(block_table), _data(seqlens),
-                                    _data(page_refs), _data(table_out), _data(refs_out), _data(page_map),
-                                    _data(work), B, max_pages, num_pages, page, layers, row, _stream(stream))
-    _check(st, "attn_cache_compact")
+    _check(_call(library().attn_cache_compact, dev, stream, k_pool.data_ptr(), v_pool.data_ptr(),
+                 block_table.data_ptr(), seqlens.data_ptr(), page_refs.data_ptr(), table_out.data_ptr(),
+                 refs_out.data_ptr(), page_map.data_ptr(), work.data_ptr(), B, max_pages, num_pages, page,
+                 layers, row), "attn_cache_compact")
     return table_out, refs_out, page_map
 
 

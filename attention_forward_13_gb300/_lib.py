@@ -35,7 +35,7 @@ EXPORTS = ("attn_fwd", "attn_fwd_varlen", "attn_fwd_paged", "attn_splitkv_combin
            "attn_last_kernel_name", "attn_device_error", "attn_selftest_timeout",
            "attn_fwd_paged_noalloc", "attn_paged_window_pages", "attn_dense_schedule",
            "attn_tree_mask", "attn_tree_workspace_bytes", "attn_fwd_paged_tree", "attn_cache_reorder",
-           "attn_cache_reserve", "attn_cache_accept", "attn_cache_compact")
+           "attn_cache_reserve", "attn_cache_accept", "attn_cache_compact", "attn_paged_keep_splits")
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
 _lock = threading.Lock()
@@ -69,6 +69,8 @@ def _declare(lib):
     lib.attn_tree_workspace_bytes.argtypes = [_I, _I, _I, _I]
     lib.attn_tree_workspace_bytes.restype = ctypes.c_size_t
     lib.attn_fwd_paged_tree.argtypes = [_P] * 10 + [_I] * 9 + [_P, ctypes.c_size_t, O, _P]
+    lib.attn_paged_keep_splits.argtypes = [_I, _I, _I, _I]
+    lib.attn_paged_keep_splits.restype = _I
     lib.attn_cache_reorder.argtypes = [_P] * 7 + [_I] * 5 + [_P]
     lib.attn_cache_reserve.argtypes = [_P] * 10 + [_I] * 5 + [ctypes.c_int64, _P]
     lib.attn_cache_accept.argtypes = [_P] * 10 + [_I] * 7 + [ctypes.c_int64, _P]

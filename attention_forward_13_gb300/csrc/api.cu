@@ -837,6 +837,27 @@ int attn_paged_auto_splits(int B, int Hkv, int max_pages_per_seq) {
   return static_cast<int>(want);
 }
 
+int attn_paged_keep_splits(int B, int Hkv, int page_size, int window_pages) {
+  int sms = 148;
+  device_state(nullptr, &sms);
+  if (B <= 0 || Hkv <= 0 || page_size <= 0 || window_pages <= 0) return 1;
+  // A window reads few pages, so a CTA's start (launch, barriers, first page
+  // look-up and load, final O) weighs as much as 4 of its 128-key blocks, and
+  // the combine as 2 (measured at 64 sequences x 8 kv heads, a window of 1024
+  // keys and 64 first tokens: 75 us with one split, 99 with two, 128 with
+  // four).  Two CTAs are resident per SM; take the cheapest count of waves x
+  // (start + blocks).
+  const int64_t pairs = static_cast<int64_t>(B) * Hkv;
+  int best = 1;
+  int64_t best_cost = INT64_MAX;
+  for (int s = 1; s <= 64 && s <= window_pages; ++s) {
+    const int64_t chunk = (window_pages + s - 1) / s;
+    const int64_t cost = (pairs * s + 2 * sms - 1) / (2 * sms) * (4 + (chunk * page_size + 127) / 128) + (s > 1 ? 2 : 0);
+    if (cost < best_cost) best_cost = cost, best = s;
+  }
+  return best;
+}
+
 attn_status attn_splitkv_combine(const float* o_partial, const float* lse_partial,
                                  int num_splits, int B, int Hq, int Lq, int d,
                                  const float* sink, void* o, attn_dtype dtype, float* lse,
@@ -897,7 +918,9 @@ attn_status attn_fwd_paged(const void* q, const void* k_pool, const void* v_pool
                          dtype == ATTN_BF16, page_size, num_pages, max_pages_per_seq, opts,
                          static_cast<cudaStream_t>(stream));
   const int win_pages = attn_paged_window_pages(Lq, page_size, max_pages_per_seq, opts);
-  if (num_splits == 0) num_splits = attn_paged_auto_splits(B, Hkv, win_pages);
+  if (num_splits == 0)
+    num_splits = resolve_keep(opts) > 0 ? attn_paged_keep_splits(B, Hkv, page_size, win_pages)
+                                        : attn_paged_auto_splits(B, Hkv, win_pages);
   if (num_splits > 1 && (o_partial == nullptr || lse_partial == nullptr ||
                          !aligned16(o_partial) || (reinterpret_cast<uintptr_t>(lse_partial) & 3u)))
     return ATTN_ERR_INVALID;

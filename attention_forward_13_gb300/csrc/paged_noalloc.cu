@@ -76,8 +76,10 @@ extern "C" attn_status attn_fwd_paged_noalloc(const void* q, const void* k_pool,
   // Split count: an explicit count must fit the scratch; the automatic choice
   // is lowered until it fits (one split needs no scratch at all).
   if (num_splits == 0) {
-    num_splits = attn_paged_auto_splits(
-        B, Hkv, attn_paged_window_pages(Lq, page_size, max_pages_per_seq, opts));
+    const int pages = attn_paged_window_pages(Lq, page_size, max_pages_per_seq, opts);
+    const bool keep = opts != nullptr && opts->use_window && opts->window_left >= 0 && opts->sink_tokens > 0;
+    num_splits = keep ? attn_paged_keep_splits(B, Hkv, page_size, pages)
+                      : attn_paged_auto_splits(B, Hkv, pages);
     while (num_splits > 1 &&
            attn_paged_workspace_bytes(B, Lq, Hq, d, num_splits) > ATTN_NOALLOC_SCRATCH_BYTES)
       --num_splits;

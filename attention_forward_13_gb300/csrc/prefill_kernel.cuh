@@ -248,6 +248,7 @@ struct PrefillItem {
   int klo;    // first key of the band any row of the item keeps
   int ub[2];  // query tile t takes part in steps [ub[t], ue[t]) of the item
   int ue[2];
+  int kt[2];  // kMaskBandKeep: and in steps [0, kt[t]), kt[t] <= ub[t]
 };
 
 // K/V tile of step u of an item: the band's tiles in order, with kMaskBandKeep
@@ -256,6 +257,18 @@ template <int MASK>
 __device__ __forceinline__ int kv_tile(const PrefillItem& it, int u) {
   if constexpr (MASK == kMaskBandKeep) return u < it.nkeep ? u : u + it.gap;
   return it.jb + u;
+}
+
+// Whether query tile t takes part in step u, and its first step.
+template <int MASK>
+__device__ __forceinline__ bool takes(const PrefillItem& it, int t, int u) {
+  if constexpr (MASK == kMaskBandKeep) return u < it.kt[t] || (it.ub[t] <= u && u < it.ue[t]);
+  return it.ub[t] <= u && u < it.ue[t];
+}
+template <int MASK>
+__device__ __forceinline__ int first_step(const PrefillItem& it, int t) {
+  if constexpr (MASK == kMaskBandKeep) return it.kt[t] > 0 ? 0 : it.ub[t];
+  return it.ub[t];
 }
 
 // One 128-key K or V tile of sequence it.b gathered from a paged pool
@@ -362,11 +375,10 @@ __device__ __forceinline__ bool decode_pair(const PrefillParams& p, int b, int m
     it.ue[t] = has ? te[t] - it.jb : 0;
   }
   if constexpr (MASK == kMaskBandKeep) {
-    // The tiles of the first sink_tokens keys up to the last row's right
-    // bound (kend of the later tile), then the band's.  A query tile with any
-    // key takes part from step 0 on: a step whose keys are all masked for it
-    // adds nothing, and steps stay one range.
-    int kt[2];  // sink tiles each query tile keeps
+    // The tiles of the first sink_tokens keys, up to the last row's right bound,
+    // before the band's; those of them that the band holds anyway are its own.
+    const int band = it.cnt;  // tiles of the band
+    int kt[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const int mt = it.m0 + t * qpt;
@@ -377,15 +389,21 @@ __device__ __forceinline__ bool decode_pair(const PrefillParams& p, int b, int m
       }
       kt[t] = ks > 0 ? (ks + BN - 1) / BN : 0;
     }
-    const int band = it.cnt;  // tiles of the band
     it.nkeep = max(kt[0], kt[1]);
     if (band > 0) it.nkeep = min(it.nkeep, it.jb);
     it.gap = band > 0 ? it.jb - it.nkeep : 0;
     it.cnt = band + it.nkeep;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      it.ue[t] = te[t] > tb[t] ? it.nkeep + it.ue[t] : min(kt[t], it.cnt);
-      it.ub[t] = 0;
+      // Steps of the band, then what of the sink tiles comes before them (a
+      // tile whose band starts later than the other's still wants sink tiles
+      // that lie in the other's band).
+      const bool has = te[t] > tb[t];
+      it.ub[t] = has ? it.nkeep + it.ub[t] : it.cnt;
+      it.ue[t] = has ? it.nkeep + it.ue[t] : min(kt[t], it.cnt);
+      it.kt[t] = min(kt[t], it.ub[t]);
+      if (!has) it.ub[t] = it.ue[t];  // the sink tiles alone
+      if (it.kt[t] > it.ub[t]) it.kt[t] = it.ub[t];
     }
   }
   return true;
@@ -707,7 +725,7 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
         for (int t = 0; t < 2; ++t) {
           if (!ok || !(ok = w.wait(&sm.q_full[t], qn & 1, kErrPrefillQ))) break;
           tc_fence_after();
-          if (it.ub[t] == 0 && it.ue[t] > 0) issue_s(t, g);
+          if (takes<MASK>(it, t, 0)) issue_s(t, g);
           if (it.ue[t] <= 1) umma_commit_warp(&sm.q_empty[t], lead);  // no later S for tile t
         }
         ++qn;
@@ -744,22 +762,23 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
             break;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            if (it.ub[t] <= u && u < it.ue[t]) {
+            if (takes<MASK>(it, t, u)) {
               if (!(ok = w.wait(HALVES ? &sm.p_half[t] : &sm.p_full[t], pc[t] & 1,
                                 kErrPrefillPFull)))
                 break;
               // O_t is free once the previous item's epilogue has read it.
-              if (u == it.ub[t] && oc[t] > 0 &&
+              const int u0 = first_step<MASK>(it, t);
+              if (u == u0 && oc[t] > 0 &&
                   !(ok = w.wait(&sm.o_free[t], (oc[t] - 1) & 1, kErrPrefillOFinal)))
                 break;
               tc_fence_after();
               if constexpr (HALVES) {
-                issue_pv(t, gu, u > it.ub[t], 0, C::BN / 32);
+                issue_pv(t, gu, u > u0, 0, C::BN / 32);
                 if (!(ok = w.wait(&sm.p_full[t], pc[t] & 1, kErrPrefillPFull))) break;
                 tc_fence_after();
                 issue_pv(t, gu, true, C::BN / 32, C::BN / 16);
               } else {
-                issue_pv(t, gu, u > it.ub[t], 0, C::BN / 16);
+                issue_pv(t, gu, u > u0, 0, C::BN / 16);
               }
               ++pc[t];
               if (u + 1 == it.ue[t]) umma_commit_warp(&sm.o_final[t], lead);
@@ -768,7 +787,7 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
             // p_full wait by the fence above (or, for a tile that starts at
             // u+1, touches no column the softmax still reads), and its K tile
             // by the k_full wait (copy engine to tensor core).
-            if (next && it.ub[t] <= u + 1 && u + 1 < it.ue[t]) {
+            if (next && takes<MASK>(it, t, u + 1)) {
               issue_s(t, gu + 1);
               if (u + 2 == it.ue[t]) umma_commit_warp(&sm.q_empty[t], lead);  // tile t's last S
             }
@@ -779,7 +798,7 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
         }
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-          if (it.ue[t] > it.ub[t]) ++oc[t];
+          if (it.ue[t] > first_step<MASK>(it, t)) ++oc[t];
         g += it.cnt;
       }
       // All MMAs this warp issued must finish before tensor memory is freed.
@@ -838,7 +857,12 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
       if (mt >= it.Lq) continue;                  // this tile has no row
       const int qi = mt + (r & qmask);            // this row's query index within the sequence
       const int hr = it.h + (r >> p.qpt_log2);    // and its query head
-      const int nt = it.ue[t] - it.ub[t];  // K/V steps of this tile
+      // K/V steps of this tile, and the step of its j-th one.
+      const int nt = MASK == kMaskBandKeep ? it.kt[t] + it.ue[t] - it.ub[t] : it.ue[t] - it.ub[t];
+      auto step_of = [&](int j) {
+        if constexpr (MASK == kMaskBandKeep) return j < it.kt[t] ? j : j - it.kt[t] + it.ub[t];
+        return it.ub[t] + j;
+      };
       const int diag = p.top_left ? 0 : it.Lk - it.Lq;  // key on row 0's diagonal
       const int last = min(mt + qmask, it.Lq - 1);      // last query of this tile
       float alibi_raw = 0.0f;      // ALiBi slope / scale (raw-score units)
@@ -856,10 +880,10 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
       // ahead (the valid bytes only).
       uint4 bn[W / 8];
       auto fetch_bias = [&](int jj) {  // registers for step jj, L2 for step jj + 1
-        const int k0 = kv_tile<MASK>(it, it.ub[t] + jj) * C::BN;
+        const int k0 = kv_tile<MASK>(it, step_of(jj)) * C::BN;
         load_bias_regs<W / 8>(bn, bias_row + k0, it.Lk - k0);
         if (jj + 1 < nt) {
-          const int k1 = kv_tile<MASK>(it, it.ub[t] + jj + 1) * C::BN;
+          const int k1 = kv_tile<MASK>(it, step_of(jj + 1)) * C::BN;
           const char* nb = reinterpret_cast<const char*>(bias_row + k1);
           const int bytes = min(it.Lk - k1, W) * static_cast<int>(sizeof(T));
           if (bytes > 0) {
@@ -877,13 +901,31 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
         ++pc;
         tc_fence_after();
         uint32_t sr[W];
-        const int j0 = kv_tile<MASK>(it, it.ub[t] + j) * C::BN;  // first key of this K/V tile
+        const int j0 = kv_tile<MASK>(it, step_of(j)) * C::BN;  // first key of this K/V tile
         // Whether some key of this tile is masked for some row of the tile
         // (the tail past Lk, the causal / window band): the same for every
         // thread of the warpgroup.
         const bool masked = (j0 + W > it.Lk) ||
                             (MASK && p.win_right >= 0 && j0 + W - 1 > mt + diag + p.win_right) ||
                             (MASK && p.win_left >= 0 && j0 < last + diag - p.win_left);
+        // kMaskBandKeep: which quarters of 32 columns some row of the warp sees
+        // (bit q); the others take no special-function work.  A narrow window
+        // leaves most of its tiles' columns to nobody: with a window of 200 keys
+        // and 5 first tokens 9 of a warp's 16 quarters remain (soft-cap, group
+        // mode, 16 sequences up to 2047, H16 d64: 122 -> XXXX us).
+        uint32_t quarters = 0xfu;
+        if constexpr (MASK == kMaskBandKeep) {
+          if (masked) {
+            int hi = it.Lk - 1 - j0;
+            if (p.win_right >= 0) hi = min(hi, qi + diag + p.win_right - j0);
+            const int lo = qi + diag - p.win_left - j0, keep = p.sink_tokens - j0;
+            const int whi = __reduce_max_sync(0xffffffffu, hi), wlo = __reduce_min_sync(0xffffffffu, lo);
+            quarters = 0;
+#pragma unroll
+            for (int qq = 0; qq < W / 32; ++qq)
+              if (32 * qq <= whi && (32 * qq + 31 >= wlo || 32 * qq < keep)) quarters |= 1u << qq;
+          }
+        }
         float raw_max = -INFINITY;  // (HW_MAX) the row maximum of the raw scores
         if constexpr (XF == kXfBias) {
           // A quarter of 32 scores at a time, each taking its bias from
@@ -925,7 +967,13 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
         // (CK MakeKargs FAST_EXP2 fold).
         float* s = reinterpret_cast<float*>(sr);
         if constexpr (XF == kXfSoftcap) {
-          softcap_r_n<W>(s, p.scale * p.softcap_inv);
+          if constexpr (MASK == kMaskBandKeep) {
+#pragma unroll
+            for (int qq = 0; qq < W / 32; ++qq)
+              if ((quarters >> qq) & 1u) softcap_r_n<32>(s + 32 * qq, p.scale * p.softcap_inv);
+          } else {
+            softcap_r_n<W>(s, p.scale * p.softcap_inv);
+          }
         } else if constexpr (XF == kXfAlibi) {
           // CK ALiBi position encoding (slope per (batch, head), aligned like
           // the mask): natural-log score - slope*|diag - j|, in raw-score
@@ -1024,18 +1072,34 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
         uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};  // +0.0f in both lanes
         uint32_t pk[W / 2];
         const uint64_t a2 = f2_pack(a_coef, a_coef), b2 = f2_pack(b_coef - msub, b_coef - msub);
+        auto exp_cols = [&](int c0, auto nc) {  // P of nc columns from c0 on
+          constexpr int N = decltype(nc)::value;
+          if constexpr (MASK == kMaskBandKeep) {
+#pragma unroll
+            for (int qq = 0; qq < N / 32; ++qq) {
+              if ((quarters >> (c0 / 32 + qq)) & 1u) {
+                exp_pack_row<BF16, 16>(s + c0 + 32 * qq, a2, b2, pk + c0 / 2 + 16 * qq, acc2);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) pk[c0 / 2 + 16 * qq + i] = 0u;
+              }
+            }
+          } else {
+            exp_pack_row<BF16, N / 2>(s + c0, a2, b2, pk + c0 / 2, acc2);
+          }
+        };
         if constexpr (HALVES) {
           static_assert(W == 128, "P halves of one 32-column store each");
-          exp_pack_row<BF16, W / 4>(s, a2, b2, pk, acc2);
+          exp_cols(0, std::integral_constant<int, W / 2>{});
           tmem_st32(tS, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
           rescale_o();  // (here, with half of the scores consumed: fewer live registers)
           tmem_st_wait();
           tc_fence_before();
           mbar_arrive(&sm.p_half[t]);
-          exp_pack_row<BF16, W / 4>(s + W / 2, a2, b2, pk + W / 4, acc2);
+          exp_cols(W / 2, std::integral_constant<int, W / 2>{});
           tmem_st32(tS + W / 4, *reinterpret_cast<uint32_t(*)[32]>(&pk[W / 4]));
         } else {
-          exp_pack_row<BF16, W / 2>(s, a2, b2, pk, acc2);
+          exp_cols(0, std::integral_constant<int, W>{});
           // P over the first W/2 columns of S.
 #pragma unroll
           for (int qq = 0; qq < W / 64; ++qq)

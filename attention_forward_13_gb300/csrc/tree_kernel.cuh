@@ -43,6 +43,7 @@
 #include "ptx.cuh"
 #include "softmax.cuh"
 
+#include <atomic>
 #include <type_traits>
 
 namespace attn {
@@ -973,12 +974,20 @@ static cudaError_t launch_tree_t(const TreeParams& p, cudaStream_t stream) {
   static_assert(sizeof(TreeSmem<C>) <= 227 * 1024, "shared memory per block");
   // setmaxnreg.inc draws on what the block was launched with: refuse to launch
   // a build whose launch count is not the one the split assumes.
-  cudaFuncAttributes fa;
-  cudaError_t e = cudaFuncGetAttributes(&fa, kern);
+  static std::atomic<uint64_t> configured{0};  // bit per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (fa.numRegs != C::LAUNCH_REGS) return cudaErrorInvalidConfiguration;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(configured.load(std::memory_order_relaxed) & bit)) {
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, kern);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs != C::LAUNCH_REGS) return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(bit, std::memory_order_relaxed);
+  }
   kern<<<p.grid, C::THREADS, smem, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;

@@ -290,6 +290,10 @@ size_t attn_paged_workspace_bytes(int B, int Lq, int Hq, int d, int num_splits);
  * (pass W of attn_paged_window_pages as max_pages_per_seq). */
 int attn_paged_auto_splits(int B, int Hkv, int max_pages_per_seq);
 
+/* The same for calls with sink_tokens (pass W as window_pages): a window's few
+ * pages want fewer splits than a whole cache. */
+int attn_paged_keep_splits(int B, int Hkv, int page_size, int window_pages);
+
 /* W of the paged split layout: the most logical pages of one sequence that
  * hold a key some query row keeps.  max_pages_per_seq without a left window,
  * else min(max_pages_per_seq, ceil((Lq + window_left) / page_size) + 1 +
