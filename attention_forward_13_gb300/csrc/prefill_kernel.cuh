@@ -857,12 +857,13 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
       if (mt >= it.Lq) continue;                  // this tile has no row
       const int qi = mt + (r & qmask);            // this row's query index within the sequence
       const int hr = it.h + (r >> p.qpt_log2);    // and its query head
-      // K/V steps of this tile, and the step of its j-th one.
-      const int nt = MASK == kMaskBandKeep ? it.kt[t] + it.ue[t] - it.ub[t] : it.ue[t] - it.ub[t];
-      auto step_of = [&](int j) {
-        if constexpr (MASK == kMaskBandKeep) return j < it.kt[t] ? j : j - it.kt[t] + it.ub[t];
-        return it.ub[t] + j;
-      };
+      // K/V steps of this tile, and the step of its j-th one.  (Selects, not
+      // it.ub[t]: an index known only at run time would put the item in local
+      // memory.)
+      const int ub = t ? it.ub[1] : it.ub[0], ue = t ? it.ue[1] : it.ue[0];
+      const int kt = MASK == kMaskBandKeep ? (t ? it.kt[1] : it.kt[0]) : 0;
+      const int nt = kt + ue - ub;
+      auto step_of = [&](int j) { return j < kt ? j : j - kt + ub; };
       const int diag = p.top_left ? 0 : it.Lk - it.Lq;  // key on row 0's diagonal
       const int last = min(mt + qmask, it.Lq - 1);      // last query of this tile
       float alibi_raw = 0.0f;      // ALiBi slope / scale (raw-score units)
@@ -914,11 +915,15 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
         // and 5 first tokens 9 of a warp's 16 quarters remain (soft-cap, group
         // mode, 16 sequences up to 2047, H16 d64: 122 -> XXXX us).
         uint32_t quarters = 0xfu;
+        int col_lo = 0, col_hi = W, col_keep = 0;  // the row sees [lo, hi) and [0, min(keep, hi))
         if constexpr (MASK == kMaskBandKeep) {
           if (masked) {
             int hi = it.Lk - 1 - j0;
             if (p.win_right >= 0) hi = min(hi, qi + diag + p.win_right - j0);
             const int lo = qi + diag - p.win_left - j0, keep = p.sink_tokens - j0;
+            col_lo = lo;
+            col_hi = hi + 1;
+            col_keep = min(keep, hi + 1);
             const int whi = __reduce_max_sync(0xffffffffu, hi), wlo = __reduce_min_sync(0xffffffffu, lo);
             quarters = 0;
 #pragma unroll
@@ -1022,6 +1027,26 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
             m_cand = raw_max * a_coef;  // a_coef > 0: order kept
           }
         } else {
+          if (MASK == kMaskBandKeep) {
+            // From a word of visible columns per quarter: a test and a select
+            // per score, and none in quarters that nobody sees (two compares
+            // per score cost the softmax 2600 cycles per masked tile).
+            constexpr float kDrop = XF == kXfSoftcap ? INFINITY : -INFINITY;
+            float part = kDrop;
+#pragma unroll
+            for (int qq = 0; qq < W / 32; ++qq) {
+              if (!((quarters >> qq) & 1u)) continue;
+              float* sq = s + 32 * qq;
+              if (masked) {
+                const uint32_t vis = (low_bits(col_hi - 32 * qq) & ~low_bits(col_lo - 32 * qq)) |
+                                     low_bits(col_keep - 32 * qq);
+#pragma unroll
+                for (int c = 0; c < 32; ++c) sq[c] = (vis >> c) & 1u ? sq[c] : kDrop;
+              }
+              part = XF == kXfSoftcap ? fminf(part, min_n<32>(sq)) : fmaxf(part, max_n<32>(sq));
+            }
+            m_cand = XF == kXfSoftcap ? fmaf(part, a_coef, b_coef) : part * a_coef;
+          } else {
           if (masked) {
             int hi = it.Lk - 1 - j0, lo = 0;  // kept columns [lo, hi] of this row
             if (MASK && p.win_right >= 0) hi = min(hi, qi + diag + p.win_right - j0);
@@ -1030,10 +1055,6 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
             if (lo <= 0) {  // no left bound inside the columns (plain causal or the tail)
 #pragma unroll
               for (int c = 0; c < W; ++c) s[c] = c <= hi ? s[c] : kDrop;
-            } else if constexpr (MASK == kMaskBandKeep) {
-              const int keep = p.sink_tokens - j0;  // columns below it are first tokens
-#pragma unroll
-              for (int c = 0; c < W; ++c) s[c] = (c <= hi && (c >= lo || c < keep)) ? s[c] : kDrop;
             } else {
 #pragma unroll
               for (int c = 0; c < W; ++c) s[c] = (c <= hi && c >= lo) ? s[c] : kDrop;
@@ -1043,6 +1064,7 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
             m_cand = fmaf(min_n<W>(s), a_coef, b_coef);  // c (1 - 2 min r); -inf if all masked
           else
             m_cand = max_n<W>(s) * a_coef;  // a_coef > 0: order kept
+          }
         }
         const float m_new = fmaxf(m_use, m_cand);
         float alpha = 1.0f;

@@ -307,11 +307,6 @@ __device__ __forceinline__ void quad_transpose(uint32_t (&w)[16], int lane) {
     }
 }
 
-// The low n bits (n <= 0: none, n >= 32: all).
-__device__ __forceinline__ uint32_t low_bits(int n) {
-  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
-}
-
 template <int D, bool BF16, bool SOFTCAP>
 __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
     attn_tree_kernel(const __grid_constant__ TreeParams p) {
