@@ -89,6 +89,8 @@ struct ReorderParams {
 
 __global__ void __launch_bounds__(512) reorder_kernel(const ReorderParams p) {
   extern __shared__ int sh[];
+  pdl_launch_dependents();
+  pdl_wait();
   int* cnt = sh;             // [kRange]
   int* times = sh + kRange;  // [B_in]: how often an old sequence is taken
   for (int b = threadIdx.x; b < p.B_in; b += blockDim.x) times[b] = 0;
@@ -170,6 +172,7 @@ __global__ void __launch_bounds__(1024) reserve_plan_kernel(const ReserveParams 
   __shared__ int scratch[33];
   const int tid = threadIdx.x, n_thr = blockDim.x;
   pdl_launch_dependents();
+  pdl_wait();
   for (int b = tid; b < p.B; b += n_thr) {
     const int len = max(p.seqlens[b], 0), add = p.add[b];
     const int has = held_pages(len, p.page_log2, p.max_pages);
@@ -326,6 +329,7 @@ __global__ void __launch_bounds__(128) reserve_copy_kernel(const ReserveParams p
   extern __shared__ int sh[];  // [B] sequences that copy
   __shared__ int count;
   if (threadIdx.x == 0) count = 0;
+  pdl_launch_dependents();
   pdl_wait();
   __syncthreads();
   for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
@@ -400,6 +404,8 @@ __device__ __forceinline__ int accept_count(const AcceptParams& p, int b, int n)
 // out ahead of the stores.
 __global__ void __launch_bounds__(128) accept_kernel(const AcceptParams p, const PoolParams q) {
   extern __shared__ int sh[];
+  pdl_launch_dependents();
+  pdl_wait();
   if (static_cast<int>(blockIdx.x) < p.ref_ctas) {
     int* cnt = sh;
     int* keep = sh + kRange;  // [B] new length
@@ -483,6 +489,7 @@ __global__ void __launch_bounds__(1024) compact_plan_kernel(const CompactParams 
   __shared__ int scratch[33];
   const int tid = threadIdx.x, n_thr = blockDim.x;
   pdl_launch_dependents();
+  pdl_wait();
   int live = 0;
   for (int p0 = 0; p0 < p.num_pages; p0 += n_thr * 8) {
     int v[8];
@@ -548,6 +555,7 @@ __global__ void __launch_bounds__(1024) compact_plan_kernel(const CompactParams 
 }
 
 __global__ void __launch_bounds__(128) compact_move_kernel(const CompactParams p, const PoolParams q, int chunks) {
+  pdl_launch_dependents();
   pdl_wait();
   const int64_t entries = static_cast<int64_t>(p.B) * p.max_pages;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < entries;
@@ -611,24 +619,14 @@ int chunks_of(const PoolParams& q) { return static_cast<int>((q.page_bytes + kCh
 // CTAs that count references: one per 1024 pages.
 int ref_ctas(int num_pages) { return std::min(kMaxCtas, (num_pages + 1023) / 1024); }
 
-template <class... A>
-cudaError_t launch(void (*kern)(A...), dim3 grid, int threads, size_t smem, cudaStream_t s, bool after, A... args) {
+template <class... P, class... A>
+cudaError_t launch(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
   if (smem > 48 * 1024) {
     const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = after ? 1 : 0;  // after: the kernel waits for its predecessor itself
-  return cudaLaunchKernelEx(&cfg, kern, args...);
+  return launch_pdl(kern, grid, threads, smem, s, args...);
 }
 
 }  // namespace
@@ -653,7 +651,7 @@ attn_status attn_cache_reorder(const int32_t* block_table, const int32_t* seqlen
                   B_in, B_out, max_pages, num_pages, log2_of(page_size), nullptr};
   if (host_device_state(&p.err, nullptr) != ATTN_OK) return ATTN_ERR_CUDA;
   return host_finish(launch(reorder_kernel, dim3(ref_ctas(num_pages)), 512, (kRange + (size_t)B_in) * 4,
-                            static_cast<cudaStream_t>(stream), false, p),
+                            static_cast<cudaStream_t>(stream), p),
                      "attn_cache_reorder");
 }
 
@@ -675,12 +673,12 @@ attn_status attn_cache_reserve(void* k_pool, void* v_pool, const int32_t* block_
   if (host_device_state(&p.err, &sms) != ATTN_OK) return ATTN_ERR_CUDA;
   const PoolParams q = pool_params(k_pool, v_pool, layers, row_bytes, page_size, num_pages);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch(reserve_plan_kernel, dim3(1), 1024, (3 * (size_t)B + 1) * 4, s, false, p);
+  cudaError_t e = launch(reserve_plan_kernel, dim3(1), 1024, (3 * (size_t)B + 1) * 4, s, p);
   if (e == cudaSuccess) {
     const int chunks = chunks_of(q);
     const int64_t tasks = static_cast<int64_t>(B) * chunks * 2 * layers;
     const int grid = static_cast<int>(std::min<int64_t>(tasks, 8 * static_cast<int64_t>(sms)));
-    e = launch(reserve_copy_kernel, dim3(grid), 128, (size_t)B * 4, s, true, p, q, chunks);
+    e = launch(reserve_copy_kernel, dim3(grid), 128, (size_t)B * 4, s, p, q, chunks);
   }
   return host_finish(e, "attn_cache_reserve_plan+attn_cache_reserve_copy");
 }
@@ -708,7 +706,7 @@ attn_status attn_cache_accept(void* k_pool, void* v_pool, const int32_t* block_t
   const int64_t blocks = p.ref_ctas + static_cast<int64_t>(B) * 2 * layers * p.row_ctas;
   if (blocks > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
   return host_finish(launch(accept_kernel, dim3(static_cast<unsigned>(blocks)), 128, (kRange + (size_t)B) * 4,
-                            static_cast<cudaStream_t>(stream), false, p, q),
+                            static_cast<cudaStream_t>(stream), p, q),
                      "attn_cache_accept");
 }
 
@@ -729,9 +727,9 @@ attn_status attn_cache_compact(void* k_pool, void* v_pool, const int32_t* block_
   if (host_device_state(&p.err, &sms) != ATTN_OK) return ATTN_ERR_CUDA;
   const PoolParams q = pool_params(k_pool, v_pool, layers, row_bytes, page_size, num_pages);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch(compact_plan_kernel, dim3(1), 1024, 0, s, false, p);
+  cudaError_t e = launch(compact_plan_kernel, dim3(1), 1024, 0, s, p);
   if (e == cudaSuccess)
-    e = launch(compact_move_kernel, dim3(8 * sms), 128, 0, s, true, p, q, chunks_of(q));
+    e = launch(compact_move_kernel, dim3(8 * sms), 128, 0, s, p, q, chunks_of(q));
   return host_finish(e, "attn_cache_compact_plan+attn_cache_compact_move");
 }
 

@@ -39,6 +39,25 @@ cudaError_t launch_tree_d(const TreeParams& p, bool bf16, bool softcap, cudaStre
 cudaError_t launch_combine(const CombineParams& p, bool bf16, cudaStream_t stream, char* name,
                            size_t name_len);
 
+// Launch with programmatic serialisation: the kernel may be set up while its
+// predecessor in the stream still runs, and calls pdl_wait() before it touches
+// global memory.
+template <class... P, class... A>
+cudaError_t launch_pdl(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                       const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 cudaError_t launch_selftest_timeout(unsigned int* err, unsigned long long timeout_ns,
                                     cudaStream_t stream);
 

@@ -913,8 +913,9 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
         // (bit q); the others take no special-function work.  A narrow window
         // leaves most of its tiles' columns to nobody: with a window of 200 keys
         // and 5 first tokens 9 of a warp's 16 quarters remain (soft-cap, group
-        // mode, 16 sequences up to 2047, H16 d64: 122 -> XXXX us).
+        // mode, 16 sequences up to 2047, H16 d64: 122 -> 117 us).
         uint32_t quarters = 0xfu;
+        constexpr bool QUARTERS = MASK == kMaskBandKeep && HALVES;  // (the others would spill)
         int col_lo = 0, col_hi = W, col_keep = 0;  // the row sees [lo, hi) and [0, min(keep, hi))
         if constexpr (MASK == kMaskBandKeep) {
           if (masked) {
@@ -925,7 +926,7 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
             col_hi = hi + 1;
             col_keep = min(keep, hi + 1);
             const int whi = __reduce_max_sync(0xffffffffu, hi), wlo = __reduce_min_sync(0xffffffffu, lo);
-            quarters = 0;
+            if constexpr (QUARTERS) quarters = 0;
 #pragma unroll
             for (int qq = 0; qq < W / 32; ++qq)
               if (32 * qq <= whi && (32 * qq + 31 >= wlo || 32 * qq < keep)) quarters |= 1u << qq;
@@ -1035,7 +1036,7 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
             float part = kDrop;
 #pragma unroll
             for (int qq = 0; qq < W / 32; ++qq) {
-              if (!((quarters >> qq) & 1u)) continue;
+              if (QUARTERS && !((quarters >> qq) & 1u)) continue;
               float* sq = s + 32 * qq;
               if (masked) {
                 const uint32_t vis = (low_bits(col_hi - 32 * qq) & ~low_bits(col_lo - 32 * qq)) |
@@ -1096,7 +1097,7 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
         const uint64_t a2 = f2_pack(a_coef, a_coef), b2 = f2_pack(b_coef - msub, b_coef - msub);
         auto exp_cols = [&](int c0, auto nc) {  // P of nc columns from c0 on
           constexpr int N = decltype(nc)::value;
-          if constexpr (MASK == kMaskBandKeep) {
+          if constexpr (QUARTERS) {
 #pragma unroll
             for (int qq = 0; qq < N / 32; ++qq) {
               if ((quarters >> (c0 / 32 + qq)) & 1u) {

@@ -3,6 +3,7 @@
 // kernels of tree_kernel.cuh.
 #include "host.h"
 #include "launch.h"
+#include "ptx.cuh"
 
 #include <cstdio>
 #include <cstring>
@@ -25,6 +26,8 @@ __global__ void __launch_bounds__(1024)
   uint32_t* m = sh;                                    // [T][W]
   int* jump = reinterpret_cast<int*>(sh + T * W);      // [T]
   const int b = blockIdx.x;
+  pdl_launch_dependents();
+  pdl_wait();
   const int n = tree_lens != nullptr ? max(0, min(tree_lens[b], T)) : T;
   const int i = threadIdx.x;                           // node of this thread (blockDim >= T)
   for (int e = threadIdx.x; e < T * W; e += blockDim.x) {
@@ -93,11 +96,9 @@ attn_status attn_tree_mask(const int32_t* parents, const int32_t* tree_lens, uin
   cudaError_t e = cudaSuccess;
   if (smem > 48 * 1024)
     e = cudaFuncSetAttribute(tree_mask_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess) {
-    tree_mask_kernel<<<B, threads, smem, static_cast<cudaStream_t>(stream)>>>(parents, tree_lens, mask,
-                                                                              depth, T, W, err);
-    e = cudaGetLastError();
-  }
+  if (e == cudaSuccess)
+    e = launch_pdl(tree_mask_kernel, dim3(B), threads, smem, static_cast<cudaStream_t>(stream), parents,
+                   tree_lens, mask, depth, T, W, err);
   return host_finish(e, "attn_tree_mask");
 }
 

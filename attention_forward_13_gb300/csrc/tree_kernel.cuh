@@ -356,7 +356,9 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
     tmem_alloc(&sm.tmem_base, C::TM_COLS);
     tmem_relinquish();
   }
-  // This CTA's part of the line.
+  // This CTA's part of the line.  (Up to here nothing was read that an earlier
+  // kernel of the stream may still be writing.)
+  pdl_wait();
   tc_fence_before();
   const int cta = blockIdx.x;
   TreeWalk walk;
@@ -839,7 +841,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
             // A thread's 32 columns of its own row would go out 16 bytes to 32
             // far apart rows at a time: the four lanes of a quad exchange their
             // 16-byte pieces (a 4 x 4 transpose) and each store of the warp
-            // covers 64 bytes of 8 rows (the unit's epilogue 9000 -> XXXX cycles).
+            // covers 64 bytes of 8 rows.
             uint32_t w16[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e)
@@ -983,19 +985,9 @@ static cudaError_t launch_tree_t(const TreeParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit, std::memory_order_relaxed);
   }
-  kern<<<p.grid, C::THREADS, smem, stream>>>(p);
-  e = cudaGetLastError();
+  e = launch_pdl(kern, dim3(p.grid), C::THREADS, smem, stream, p);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.grid, D / 8);
-  cfg.blockDim = dim3(p.two_tiles ? 256 : 128);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_tree_merge_kernel<D, BF16>, p);
+  return launch_pdl(attn_tree_merge_kernel<D, BF16>, dim3(p.grid, D / 8), p.two_tiles ? 256 : 128, 0, stream, p);
 }
 
 template <>
