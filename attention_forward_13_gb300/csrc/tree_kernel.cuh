@@ -73,7 +73,7 @@ struct TreeSmem {
   alignas(1024) uint8_t buf[C::NBUF][C::TILE_BYTES];
   uint64_t full[C::NBUF], empty[C::NBUF];
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_half[2], p_full[2], o_final[2], o_free, xch, xread;
+  uint64_t s_full[2], p_half[2], p_full[2], o_final[2], o_free[2], xch, xread;
   uint64_t teardown;
   float2 x[2][128];     // (m, l) of a row, per warpgroup
   int scan[16];
@@ -339,8 +339,8 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       mbar_init(&sm.p_half[t], 128);
       mbar_init(&sm.p_full[t], 128);
       mbar_init(&sm.o_final[t], 1);
+      mbar_init(&sm.o_free[t], pair ? 128 : 256);  // the threads that read the tile's O
     }
-    mbar_init(&sm.o_free, 256);
     mbar_init(&sm.xch, 256);
     mbar_init(&sm.xread, 256);
     mbar_init(&sm.teardown, 1);
@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
         uint32_t& ph = t ? pph1 : pph0;
         const uint64_t vd = vdesc0 + static_cast<uint64_t>(slot * kTileDesc);
         if (!w.wait(&sm.p_half[t], ph, kErrTreeWait)) return false;
-        if (fresh && seg > 0 && !w.wait(&sm.o_free, (seg - 1) & 1, kErrTreeWait)) return false;
+        if (fresh && seg > 0 && !w.wait(&sm.o_free[t], (seg - 1) & 1, kErrTreeWait)) return false;
         tc_fence_after();
 #pragma unroll
         for (int k = 0; k < C::BN / 32; ++k)
@@ -767,19 +767,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
         a1 = ex2_approx(e1.x - ms);
         l = e0.y * a0 + e1.y * a1;
       }
-      const bool use0 = pair ? (t < live && n > 0) : n > 0, use1 = !pair && n > 1;
-      if (use0) {
-        const int tt = pair ? t : 0;
-        ok = __all_sync(0xffffffffu, w.wait(&sm.o_final[tt], (oph >> tt) & 1, kErrTreeWait));
-        if (!ok) break;
-      }
-      if (use1) {
-        ok = __all_sync(0xffffffffu, w.wait(&sm.o_final[1], oph >> 1, kErrTreeWait));
-        if (!ok) break;
-      }
-      if (n > 0) oph ^= live == 2 ? 3u : 1u;
-      tc_fence_after();
-
+      // Everything that does not need O comes before the wait for it.
       float scale0 = a0, scale1 = a1, lse = -INFINITY;
       if (s.whole) {
         const float ms = m == -INFINITY ? 0.0f : m;
@@ -802,9 +790,9 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       }
       const bool zero = !(l > 0.0f);  // nothing seen: O is 0 whatever the accumulator holds
       const int slot = cta * 2 + (s.k0 > 0 ? 0 : 1);  // a piece that starts inside its unit is the first
-      const int prow = (pair ? t * 128 : 0) + r;                     // row of the piece
+      const int prow = (pair ? t * 128 : 0) + r;      // row of the piece
       const int prows = pair ? 256 : 128;
-      float* part = p.o_part + static_cast<int64_t>(slot) * prows * D;
+      float4* part = reinterpret_cast<float4*>(p.o_part + static_cast<int64_t>(slot) * prows * D) + prow;
       // Rows of this lane's quad in O, from the tile's first query (-1: no row).
       T* out = reinterpret_cast<T*>(p.o) + ((static_cast<int64_t>(s.b) * p.T + (qi - rq)) * p.Hq + s.hk * p.g) * D;
       int orow[4], rrq = (r & ~3) / p.g, rhg = (r & ~3) - rrq * p.g;
@@ -813,66 +801,101 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
         orow[i] = rrq < p.qpt && qi - rq + rrq < p.T ? (rrq * p.Hq + rhg) * D : -1;
         if (++rhg == p.g) rhg = 0, ++rrq;
       }
-      const int c_beg = pair ? 0 : t * (D / 2), c_end = pair ? D : c_beg + D / 2;
-      const bool writes = pair ? t < live || n == 0 : true;
-      if (writes) {
-        for (int c = c_beg; c < c_end; c += 32) {
-          // (one accumulator's columns at a time: both at once spill)
+      const bool mine = t < live;  // two tiles: this warpgroup's tile is in use
+      if (n > 0 && (!pair || mine)) {
+        const int tt = pair ? t : 0;
+        ok = __all_sync(0xffffffffu, w.wait(&sm.o_final[tt], (oph >> tt) & 1, kErrTreeWait)) &&
+             (pair || n == 1 || __all_sync(0xffffffffu, w.wait(&sm.o_final[1], oph >> 1, kErrTreeWait)));
+        if (!ok) break;
+      }
+      if (n > 0) oph ^= live == 2 ? 3u : 1u;
+      tc_fence_after();
+      // 32 columns from column c on, in registers, to O or to the piece.
+      auto put = [&](int c, const float* v) {
+        if (s.whole) {
+          // A thread's 32 columns of its own row would go out 16 bytes to 32
+          // far apart rows at a time: the four lanes of a quad exchange their
+          // 16-byte pieces (a 4 x 4 transpose) and each store of the warp
+          // covers 64 bytes of 8 rows.
+          uint32_t w16[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            w16[e] = BF16 ? pack_bf16(v[2 * e], v[2 * e + 1]) : pack_f16(v[2 * e], v[2 * e + 1]);
+          quad_transpose(w16, lane);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)  // row (r & ~3) + i, piece lane & 3
+            if (orow[i] >= 0)
+              *reinterpret_cast<uint4*>(out + orow[i] + c + 8 * (lane & 3)) =
+                  make_uint4(w16[4 * i], w16[4 * i + 1], w16[4 * i + 2], w16[4 * i + 3]);
+          __syncwarp();
+        } else if (row_in) {
+          // [D / 4][rows][4]: a warp's 32 rows are one 512-byte line.
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            part[(c + i) / 4 * prows] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        }
+      };
+      // O is read whole, in one wait, and handed back before it is packed.
+      if (n == 0) {
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+#pragma unroll 1
+        for (int c = pair ? 0 : t * (D / 2); c < (pair ? D : (t + 1) * (D / 2)); c += 32) put(c, v);
+      } else if (pair) {
+        if (mine) {
+          uint32_t ov[D];
+#pragma unroll
+          for (int c = 0; c < D; c += 32)
+            tmem_ld32(tmem + C::tm_o(t) + lane_base + c, *reinterpret_cast<uint32_t(*)[32]>(&ov[c]));
+          tmem_ld_wait();
+          reg_fence(ov);
+          tc_fence_before();
+          mbar_arrive(&sm.o_free[t]);
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            float v[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = zero ? 0.0f : __uint_as_float(ov[c + i]) * scale0;
+            put(c, v);
+          }
+        } else {
+          mbar_arrive(&sm.o_free[t]);
+        }
+        ++seg;
+      } else {
+        // Half the columns of both streams' accumulators.
+        const int c0 = t * (D / 2);
+        const bool one = n == 1;  // the second stream had no tile
+        uint32_t ov[D];
+#pragma unroll
+        for (int c = 0; c < D / 2; c += 32) {
+          tmem_ld32(tmem + C::tm_o(0) + lane_base + c0 + c, *reinterpret_cast<uint32_t(*)[32]>(&ov[c]));
+          tmem_ld32(tmem + C::tm_o(1) + lane_base + c0 + c, *reinterpret_cast<uint32_t(*)[32]>(&ov[D / 2 + c]));
+        }
+        tmem_ld_wait();
+        reg_fence(ov);
+        tc_fence_before();
+        mbar_arrive(&sm.o_free[0]);
+        mbar_arrive(&sm.o_free[1]);
+#pragma unroll
+        for (int c = 0; c < D / 2; c += 32) {
           float v[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-          if (use0) {
-            uint32_t o0[32];
-            tmem_ld32(tmem + C::tm_o(pair ? t : 0) + lane_base + c, o0);
-            tmem_ld_wait();
-            reg_fence(o0);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = zero ? 0.0f : __uint_as_float(o0[i]) * scale0;
+          for (int i = 0; i < 32; ++i) {
+            const float x = __uint_as_float(ov[c + i]) * scale0;
+            v[i] = zero ? 0.0f : one ? x : fmaf(__uint_as_float(ov[D / 2 + c + i]), scale1, x);
           }
-          if (use1) {
-            uint32_t o1[32];
-            tmem_ld32(tmem + C::tm_o(1) + lane_base + c, o1);
-            tmem_ld_wait();
-            reg_fence(o1);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = zero ? 0.0f : fmaf(__uint_as_float(o1[i]), scale1, v[i]);
-          }
-          if (s.whole) {
-            // A thread's 32 columns of its own row would go out 16 bytes to 32
-            // far apart rows at a time: the four lanes of a quad exchange their
-            // 16-byte pieces (a 4 x 4 transpose) and each store of the warp
-            // covers 64 bytes of 8 rows.
-            uint32_t w16[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              w16[e] = BF16 ? pack_bf16(v[2 * e], v[2 * e + 1]) : pack_f16(v[2 * e], v[2 * e + 1]);
-            quad_transpose(w16, lane);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)  // row (r & ~3) + i, piece lane & 3
-              if (orow[i] >= 0)
-                *reinterpret_cast<uint4*>(out + orow[i] + c + 8 * (lane & 3)) =
-                    make_uint4(w16[4 * i], w16[4 * i + 1], w16[4 * i + 2], w16[4 * i + 3]);
-          } else if (row_in) {
-            // [D / 4][rows][4]: a warp's 32 rows are one 512-byte line.
-#pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<float4*>(part + (static_cast<int64_t>((c + i) / 4) * prows + prow) * 4) =
-                  make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-          }
-          __syncwarp();
+          put(c0 + c, v);
         }
-        if (row_in && c_beg == 0) {
-          if (s.whole) {
-            if (p.lse != nullptr) p.lse[(static_cast<int64_t>(s.b) * p.Hq + hq) * p.T + qi] = lse;
-          } else {
-            p.ml_part[static_cast<int64_t>(slot) * prows + prow] = make_float2(zero ? -INFINITY : m, l);
-          }
-        }
-      }
-      if (n > 0) {
-        tc_fence_before();
-        mbar_arrive(&sm.o_free);
         ++seg;
+      }
+      if (row_in && (pair ? mine || n == 0 : t == 0)) {
+        if (s.whole) {
+          if (p.lse != nullptr) p.lse[(static_cast<int64_t>(s.b) * p.Hq + hq) * p.T + qi] = lse;
+        } else {
+          p.ml_part[static_cast<int64_t>(slot) * prows + prow] = make_float2(zero ? -INFINITY : m, l);
+        }
       }
     }
   }
