@@ -116,6 +116,17 @@ bool make_map(CUtensorMap* m, const void* base, int dt, int rank, const uint64_t
   return r == CUDA_SUCCESS;
 }
 
+// The two parts of a folded first tile (PrefillKeepParams): the same map as K or
+// V with boxes of fold and of 128 - fold rows.
+bool make_fold_maps(CUtensorMap* first, CUtensorMap* rest, const void* base, int dt, const uint64_t* dims,
+                    const uint64_t* strides_bytes, const uint32_t* box, int fold) {
+  if (fold == 0) return true;
+  uint32_t b[4] = {box[0], static_cast<uint32_t>(fold), 1, 1};
+  if (!make_map(first, base, dt, 4, dims, strides_bytes, b)) return false;
+  b[1] = 128 - static_cast<uint32_t>(fold);
+  return make_map(rest, base, dt, 4, dims, strides_bytes, b);
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 // Element strides: positive and a whole number of 16-byte units.
 bool stride_ok(int64_t s, int eb = 2) { return s > 0 && (s * eb) % 16 == 0; }
@@ -140,6 +151,16 @@ void resolve_window(const attn_opts* opts, int* wl, int* wr) {
 // every earlier key is visible anyway.
 int resolve_keep(const attn_opts* opts) {
   return (opts != nullptr && opts->use_window && opts->window_left >= 0) ? opts->sink_tokens : 0;
+}
+
+// Rows of the first tokens in the band's first tile (PrefillKeepParams), 0 where
+// they keep tiles of their own: no first tokens, too many to be worth it (more
+// than 64 leave the band less than half of the tile), or a score transform
+// that needs every column's key (ALiBi, elementwise bias).
+int fold_of(const attn_opts* opts) {
+  const int keep = resolve_keep(opts);
+  if (keep <= 0 || keep > 64 || opts->alibi_slopes != nullptr || opts->bias != nullptr) return 0;
+  return (keep + 7) / 8 * 8;
 }
 
 int prefill_mask(const PrefillParams& p) {
@@ -245,7 +266,7 @@ cudaError_t launch_decode(const DecodeParams& p, int d, bool bf16, bool softcap,
   return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_prefill(const PrefillParams& p, int grid, int d, int dt, int mask,
+cudaError_t launch_prefill(const PrefillKeepParams& p, int grid, int d, int dt, int mask,
                            int xf, cudaStream_t stream, char* name, size_t name_len) {
   const char* mask_name = mask == kMaskNone                        ? "nomask"
                           : mask == kMaskBandKeep                  ? "window_keep"
@@ -348,7 +369,7 @@ int dense_block_steps(const PrefillParams& p, int mb) {
   const int qpt = 1 << p.qpt_log2;  // queries per tile
   const int m0 = mb * 2 * qpt;
   const int diag = p.top_left ? 0 : p.Lk - p.Lq;
-  int jb = INT_MAX, je = 0, keep = 0;
+  int jb = INT_MAX, je = 0, keep = 0, khi = 0;
   for (int t = 0; t < 2; ++t) {
     const int mt = m0 + t * qpt;
     if (mt >= p.Lq) continue;
@@ -359,18 +380,21 @@ int dense_block_steps(const PrefillParams& p, int mb) {
     if (kend > kbeg) {
       jb = std::min(jb, kbeg / BN);
       je = std::max(je, (kend + BN - 1) / BN);
+      khi = std::max(khi, kend);
     }
     keep = std::max(keep, (std::min(p.sink_tokens, kend) + BN - 1) / BN);
   }
   if (je <= jb) return std::max(keep, 0);
+  const int first = p.win_left >= 0 ? std::max(0, m0 + diag - p.win_left) : 0;
+  if (p.fold > 0 && first >= p.fold) return (khi - (first - p.fold) + BN - 1) / BN;
   return je - jb + std::max(0, std::min(keep, jb));
 }
 
 std::shared_ptr<const Schedule> dense_schedule(const PrefillParams& p, int grid) {
   static std::mutex mu;
-  static std::map<std::array<int, 10>, std::shared_ptr<const Schedule>> cache;
-  const std::array<int, 10> key = {p.B, p.units, p.Lq, p.Lk, p.win_left, p.win_right, p.top_left,
-                                   p.qpt_log2, grid, p.sink_tokens};
+  static std::map<std::array<int, 11>, std::shared_ptr<const Schedule>> cache;
+  const std::array<int, 11> key = {p.B, p.units, p.Lq, p.Lk, p.win_left, p.win_right, p.top_left,
+                                   p.qpt_log2, grid, p.sink_tokens, p.fold};
   {
     std::lock_guard<std::mutex> lock(mu);
     const auto f = cache.find(key);
@@ -542,7 +566,7 @@ attn_status attn_fwd(const void* q, const void* k, const void* v, void* o, float
       0x7fffffffLL)
     return ATTN_ERR_UNSUPPORTED;
 
-  PrefillParams p;
+  PrefillKeepParams p;
   memset(&p, 0, sizeof(p));
   unsigned int* err = nullptr;
   int num_sms = 0;
@@ -556,18 +580,23 @@ attn_status attn_fwd(const void* q, const void* k, const void* v, void* o, float
     const uint64_t st[3] = {(uint64_t)sq.row * eb, (uint64_t)sq.head * eb, (uint64_t)sq.batch * eb};
     if (!make_map(&p.tm_q, q, dtype, 4, dims, st, qbox)) return ATTN_ERR_INVALID;
   }
+  p.fold = fold_of(opts);
   if (Lk > 0) {  // Lk = 0: no key tile is ever loaded, the maps stay unused
     {
       const uint64_t dims[4] = {(uint64_t)d, (uint64_t)Lk, (uint64_t)Hkv, (uint64_t)B};
       const uint64_t st[3] = {(uint64_t)sk.row * eb, (uint64_t)sk.head * eb,
                               (uint64_t)sk.batch * eb};
-      if (!make_map(&p.tm_k, k, dtype, 4, dims, st, box)) return ATTN_ERR_INVALID;
+      if (!make_map(&p.tm_k, k, dtype, 4, dims, st, box) ||
+          !make_fold_maps(&p.tm_k_first, &p.tm_k_rest, k, dtype, dims, st, box, p.fold))
+        return ATTN_ERR_INVALID;
     }
     {
       const uint64_t dims[4] = {(uint64_t)d, (uint64_t)Lk, (uint64_t)Hkv, (uint64_t)B};
       const uint64_t st[3] = {(uint64_t)sv.row * eb, (uint64_t)sv.head * eb,
                               (uint64_t)sv.batch * eb};
-      if (!make_map(&p.tm_v, v, dtype, 4, dims, st, box)) return ATTN_ERR_INVALID;
+      if (!make_map(&p.tm_v, v, dtype, 4, dims, st, box) ||
+          !make_fold_maps(&p.tm_v_first, &p.tm_v_rest, v, dtype, dims, st, box, p.fold))
+        return ATTN_ERR_INVALID;
     }
   }
   p.o = o;
@@ -651,7 +680,7 @@ attn_status attn_fwd_varlen(const void* q, const void* k, const void* v, void* o
     if (so_ != ATTN_OK) return so_;
   }
 
-  PrefillParams p;
+  PrefillKeepParams p;
   memset(&p, 0, sizeof(p));
   unsigned int* err = nullptr;
   int num_sms = 0;
@@ -666,19 +695,24 @@ attn_status attn_fwd_varlen(const void* q, const void* k, const void* v, void* o
                             (uint64_t)sq.row * eb * (uint64_t)total_q};
     if (!make_map(&p.tm_q, q, dtype, 4, dims, st, qbox)) return ATTN_ERR_INVALID;
   }
+  p.fold = fold_of(opts);
   if (total_k > 0) {  // no keys at all: the maps stay unused
     const int tk = total_k;
     {
       const uint64_t dims[4] = {(uint64_t)d, (uint64_t)tk, (uint64_t)Hkv, 1};
       const uint64_t st[3] = {(uint64_t)sk.row * eb, (uint64_t)sk.head * eb,
                               (uint64_t)sk.row * eb * (uint64_t)tk};
-      if (!make_map(&p.tm_k, k, dtype, 4, dims, st, box)) return ATTN_ERR_INVALID;
+      if (!make_map(&p.tm_k, k, dtype, 4, dims, st, box) ||
+          !make_fold_maps(&p.tm_k_first, &p.tm_k_rest, k, dtype, dims, st, box, p.fold))
+        return ATTN_ERR_INVALID;
     }
     {
       const uint64_t dims[4] = {(uint64_t)d, (uint64_t)tk, (uint64_t)Hkv, 1};
       const uint64_t st[3] = {(uint64_t)sv.row * eb, (uint64_t)sv.head * eb,
                               (uint64_t)sv.row * eb * (uint64_t)tk};
-      if (!make_map(&p.tm_v, v, dtype, 4, dims, st, box)) return ATTN_ERR_INVALID;
+      if (!make_map(&p.tm_v, v, dtype, 4, dims, st, box) ||
+          !make_fold_maps(&p.tm_v_first, &p.tm_v_rest, v, dtype, dims, st, box, p.fold))
+        return ATTN_ERR_INVALID;
     }
   }
   p.o = o;
@@ -722,7 +756,7 @@ attn_status paged_prefill(const void* q, const void* k_pool, const void* v_pool,
   if (static_cast<int64_t>(B) * (Hq / pack_of(Hq, Hkv)) * m_blocks(Lq, pack_of(Hq, Hkv)) >
       0x7fffffffLL)
     return ATTN_ERR_UNSUPPORTED;
-  PrefillParams p;
+  PrefillKeepParams p;
   memset(&p, 0, sizeof(p));
   unsigned int* err = nullptr;
   int num_sms = 0;
@@ -796,6 +830,7 @@ attn_status attn_dense_schedule(int B, int Hq, int Hkv, int Lq, int Lk, const at
   p.top_left = (opts != nullptr && opts->top_left) ? 1 : 0;
   p.num_m_blocks = m_blocks(Lq, p.pack);
   p.num_items = static_cast<int>(n);
+  p.fold = fold_of(opts);
   if (!schedule_applies(p, grid)) return ATTN_ERR_UNSUPPORTED;
   const auto s = dense_schedule(p, grid);
   if (s == nullptr) return ATTN_ERR_INVALID;

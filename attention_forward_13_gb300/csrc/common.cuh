@@ -109,6 +109,7 @@ struct PrefillParams {
   // masking is win_right = 0.  Only read by the masked instantiations.
   int win_left, win_right;
   int sink_tokens;                 // keys j < sink_tokens stay visible left of the band (win_left >= 0)
+  int fold;                        // > 0: first tokens share the band's first tile (see below)
   int top_left;                    // masks and ALiBi aligned top-left (row i on key i)
   float o_scale;                   // FP8 static quantisation: scale_p * scale_o on O
   float inv_scale;                 // 1 / scale (bias and ALiBi go to raw-score units)
@@ -133,6 +134,15 @@ struct PrefillParams {
   uint16_t sched_item[kSchedMaxItems];
 };
 static_assert(sizeof(PrefillParams) <= 4096, "prefill launch parameters exceed 4 KB");
+
+// Launch parameters of the windows whose first tokens stay visible.  With
+// fold > 0 (sink_tokens rounded up to 8, at most 64; dense and group mode) the
+// tiles of an item start at fold keys before its band, and rows 0 .. fold - 1
+// of its first tile are keys 0 .. fold - 1 in place of those: one box of fold
+// rows and one of 128 - fold.  (Eight rows are one swizzle period.)
+struct PrefillKeepParams : PrefillParams {
+  CUtensorMap tm_k_first, tm_k_rest, tm_v_first, tm_v_rest;
+};
 
 // Paged split-KV decode parameters.
 struct DecodeParams {

@@ -10,7 +10,7 @@ namespace attn {
 // grid = number of CTAs; name receives the kernel's trait string.  xf is a
 // ScoreXf value.  Dispatches to launch_prefill_d<64 / 128>.
 // mask is a PrefillMask value.
-cudaError_t launch_prefill(const PrefillParams& p, int grid, int d, int dt, int mask,
+cudaError_t launch_prefill(const PrefillKeepParams& p, int grid, int d, int dt, int mask,
                            int xf, cudaStream_t stream, char* name, size_t name_len);
 // One per head dimension, each in its own translation unit (prefill_d64.cu,
 // prefill_d128.cu) so the two compile in parallel.
@@ -21,7 +21,7 @@ cudaError_t launch_prefill_d(const PrefillParams& p, int grid, int dt, bool mask
 // The same for a window whose first tokens stay visible (prefill_keep_d64.cu,
 // prefill_keep_d128.cu).
 template <int D>
-cudaError_t launch_prefill_keep_d(const PrefillParams& p, int grid, int dt, int xf,
+cudaError_t launch_prefill_keep_d(const PrefillKeepParams& p, int grid, int dt, int xf,
                                   cudaStream_t stream);
 
 cudaError_t launch_decode(const DecodeParams& p, int d, bool bf16, bool softcap, int rows,

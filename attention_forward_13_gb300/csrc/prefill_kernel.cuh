@@ -246,6 +246,8 @@ struct PrefillItem {
   int nkeep;  // kMaskBandKeep: the first nkeep steps are K/V tiles 0 .. nkeep-1
   int gap;    // ... and step u >= nkeep is tile u + gap
   int klo;    // first key of the band any row of the item keeps
+  int kstart; // kMaskBandKeep: key of the first row of tile 0
+  bool fold;  // ... and that tile begins with the first tokens (PrefillKeepParams)
   int ub[2];  // query tile t takes part in steps [ub[t], ue[t]) of the item
   int ue[2];
   int kt[2];  // kMaskBandKeep: and in steps [0, kt[t]), kt[t] <= ub[t]
@@ -257,6 +259,13 @@ template <int MASK>
 __device__ __forceinline__ int kv_tile(const PrefillItem& it, int u) {
   if constexpr (MASK == kMaskBandKeep) return u < it.nkeep ? u : u + it.gap;
   return it.jb + u;
+}
+
+// Key of the first row of step u's tile.
+template <int MASK, int BN = 128>
+__device__ __forceinline__ int kv_key(const PrefillItem& it, int u) {
+  if constexpr (MASK == kMaskBandKeep) return it.kstart + kv_tile<MASK>(it, u) * BN;
+  return kv_tile<MASK>(it, u) * BN;
 }
 
 // Whether query tile t takes part in step u, and its first step.
@@ -311,6 +320,20 @@ __device__ __forceinline__ void load_paged_tile(const PrefillParams& p, const Pr
   }
 }
 
+// The first tile of an item whose first tokens are folded in: rows 0 .. fold - 1
+// are keys 0 .. fold - 1, the others the band from its first key on.
+template <class C>
+__device__ __forceinline__ void load_folded_tile(const PrefillParams& p, const PrefillItem& it,
+                                                 const CUtensorMap* first, const CUtensorMap* rest,
+                                                 uint8_t* dst, uint64_t* bar, uint64_t pol) {
+#pragma unroll
+  for (int c = 0; c < C::NCHUNK; ++c) {
+    uint8_t* d = dst + c * C::CHUNK_BYTES;
+    tma_load_4d_hint(d, first, bar, c * C::ATOM, it.rk0, it.hk, it.bcoord, pol);
+    tma_load_4d_hint(d + p.fold * 128, rest, bar, c * C::ATOM, it.rk0 + it.klo, it.hk, it.bcoord, pol);
+  }
+}
+
 // Item index -> coordinates.  Masked problems list the heaviest query blocks
 // first (Composable Kernel GetTileIndex reverses the m-tile order when
 // masking).  Returns false when the block starts past the sequence end.
@@ -347,10 +370,11 @@ __device__ __forceinline__ bool decode_pair(const PrefillParams& p, int b, int m
   if (it.m0 >= it.Lq) return false;
   const int diag = p.top_left ? 0 : it.Lk - it.Lq;  // key on row 0's diagonal
   int tb[2], te[2];  // K/V tile range [tb, te) of each query tile
+  int kb[2], ke[2];  // and its key range
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int mt = it.m0 + t * qpt;
-    tb[t] = te[t] = 0;
+    tb[t] = te[t] = kb[t] = ke[t] = 0;
     if (mt < it.Lq) {
       const int last = min(mt + qpt - 1, it.Lq - 1);
       int kend = it.Lk, kbeg = 0;  // keys [kbeg, kend) some row of the tile keeps
@@ -359,6 +383,8 @@ __device__ __forceinline__ bool decode_pair(const PrefillParams& p, int b, int m
       if (kend > kbeg) {
         tb[t] = kbeg / BN;
         te[t] = (kend + BN - 1) / BN;
+        kb[t] = kbeg;
+        ke[t] = kend;
       }
     }
   }
@@ -388,6 +414,26 @@ __device__ __forceinline__ bool decode_pair(const PrefillParams& p, int b, int m
         if (p.win_right >= 0) ks = min(ks, min(mt + qpt - 1, it.Lq - 1) + diag + p.win_right + 1);
       }
       kt[t] = ks > 0 ? (ks + BN - 1) / BN : 0;
+    }
+    it.kstart = 0;
+    it.fold = p.fold > 0 && band > 0 && it.klo >= p.fold;
+    if (it.fold) {
+      // One tile for the first tokens and the band's beginning: narrow windows
+      // have few tiles, and one that serves a handful of keys costs as much as
+      // any (window 1024 and 4 first tokens, 64 queries per block: 9 steps
+      // instead of 10).
+      it.kstart = it.klo - p.fold;
+      it.cnt = 0;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const bool has = te[t] > tb[t];
+        const int sees = kt[t] > 0 ? 1 : 0;
+        it.ub[t] = has ? (kb[t] - it.kstart) / BN : sees;
+        it.ue[t] = has ? (ke[t] - it.kstart + BN - 1) / BN : sees;
+        it.kt[t] = min(sees, it.ub[t]);
+        it.cnt = max(it.cnt, it.ue[t]);
+      }
+      return true;
     }
     it.nkeep = max(kt[0], kt[1]);
     if (band > 0) it.nkeep = min(it.nkeep, it.jb);
@@ -513,9 +559,13 @@ __device__ __forceinline__ int item_of_round(const PrefillParams& p, int r) {
 // XF: score transform before masking (ScoreXf): none, soft-cap, ALiBi or an
 // elementwise bias (the last two are mutually exclusive with the soft-cap).
 // ORD: group mode or paged cache, work items in the sorted order (order_items).
+template <int MASK>
+using PrefillArgs =
+    typename std::conditional<MASK == kMaskBandKeep, PrefillKeepParams, PrefillParams>::type;
+
 template <int D, int DT, int MASK, int XF, bool ORD>
 __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
-    attn_prefill_kernel(const __grid_constant__ PrefillParams p) {
+    attn_prefill_kernel(const __grid_constant__ PrefillArgs<MASK> p) {
   using C = PrefillCfg<D, DT>;
   constexpr bool FP8 = C::FP8;
   constexpr bool BF16 = DT == kDtBF16;  // P / V type of the P.V MMA (FP8: fp16)
@@ -619,36 +669,42 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
           if (!(ok = w.wait(&sm.k_empty[s], ph ^ 1, kErrPrefillKEmpty))) break;
           mbar_arrive_expect_tx(&sm.k_full[s], C::TILE_BYTES);
           if (p.block_table != nullptr) {
-            load_paged_tile<C, MASK>(p, it, kv_tile<MASK>(it, j) * C::BN, &p.tm_k, sm.k[s], &sm.k_full[s],
+            load_paged_tile<C, MASK>(p, it, kv_key<MASK>(it, j), &p.tm_k, sm.k[s], &sm.k_full[s],
                                pol_kv);
+          } else if (MASK == kMaskBandKeep && it.fold && j == 0) {
+            if constexpr (MASK == kMaskBandKeep)
+              load_folded_tile<C>(p, it, &p.tm_k_first, &p.tm_k_rest, sm.k[s], &sm.k_full[s], pol_kv);
           } else {
 #pragma unroll
             for (int c = 0; c < C::NCHUNK; ++c) {
               if constexpr (ATTN_L2_HINTS)
                 tma_load_4d_hint(sm.k[s] + c * C::CHUNK_BYTES, &p.tm_k, &sm.k_full[s],
-                                 c * C::ATOM, it.rk0 + kv_tile<MASK>(it, j) * C::BN, it.hk, it.bcoord,
+                                 c * C::ATOM, it.rk0 + kv_key<MASK>(it, j), it.hk, it.bcoord,
                                  pol_kv);
               else
                 tma_load_4d(sm.k[s] + c * C::CHUNK_BYTES, &p.tm_k, &sm.k_full[s],
-                            c * C::ATOM, it.rk0 + kv_tile<MASK>(it, j) * C::BN, it.hk, it.bcoord);
+                            c * C::ATOM, it.rk0 + kv_key<MASK>(it, j), it.hk, it.bcoord);
             }
           }
           ++k_armed;
           if (!(ok = w.wait(&sm.v_empty[s], ph ^ 1, kErrPrefillVEmpty))) break;
           mbar_arrive_expect_tx(&sm.v_full[s], C::TILE_BYTES);
           if (p.block_table != nullptr) {
-            load_paged_tile<C, MASK>(p, it, kv_tile<MASK>(it, j) * C::BN, &p.tm_v, sm.v[s], &sm.v_full[s],
+            load_paged_tile<C, MASK>(p, it, kv_key<MASK>(it, j), &p.tm_v, sm.v[s], &sm.v_full[s],
                                pol_kv);
+          } else if (MASK == kMaskBandKeep && it.fold && j == 0) {
+            if constexpr (MASK == kMaskBandKeep)
+              load_folded_tile<C>(p, it, &p.tm_v_first, &p.tm_v_rest, sm.v[s], &sm.v_full[s], pol_kv);
           } else {
 #pragma unroll
             for (int c = 0; c < C::NCHUNK; ++c) {
               if constexpr (ATTN_L2_HINTS)
                 tma_load_4d_hint(sm.v[s] + c * C::CHUNK_BYTES, &p.tm_v, &sm.v_full[s],
-                                 c * C::ATOM, it.rk0 + kv_tile<MASK>(it, j) * C::BN, it.hk, it.bcoord,
+                                 c * C::ATOM, it.rk0 + kv_key<MASK>(it, j), it.hk, it.bcoord,
                                  pol_kv);
               else
                 tma_load_4d(sm.v[s] + c * C::CHUNK_BYTES, &p.tm_v, &sm.v_full[s],
-                            c * C::ATOM, it.rk0 + kv_tile<MASK>(it, j) * C::BN, it.hk, it.bcoord);
+                            c * C::ATOM, it.rk0 + kv_key<MASK>(it, j), it.hk, it.bcoord);
             }
           }
           ++v_armed;
@@ -744,7 +800,7 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
           if constexpr (ORD && !FP8) {
             // Paged cache: rows of the last page behind the sequence's end
             // may hold anything, and 0 * NaN in P.V is not 0: zero them.
-            const int live = it.Lk - kv_tile<MASK>(it, u) * C::BN;
+            const int live = it.Lk - kv_key<MASK>(it, u);
             if (p.block_table != nullptr && live > 0 && live < C::BN && live % p.page_size != 0) {
               const int end = min(C::BN, (live + p.page_size - 1) / p.page_size * p.page_size);
               for (int i = lane; i < (end - live) * C::NCHUNK * 8; i += 32) {
@@ -881,10 +937,10 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
       // ahead (the valid bytes only).
       uint4 bn[W / 8];
       auto fetch_bias = [&](int jj) {  // registers for step jj, L2 for step jj + 1
-        const int k0 = kv_tile<MASK>(it, step_of(jj)) * C::BN;
+        const int k0 = kv_key<MASK>(it, step_of(jj));
         load_bias_regs<W / 8>(bn, bias_row + k0, it.Lk - k0);
         if (jj + 1 < nt) {
-          const int k1 = kv_tile<MASK>(it, step_of(jj + 1)) * C::BN;
+          const int k1 = kv_key<MASK>(it, step_of(jj + 1));
           const char* nb = reinterpret_cast<const char*>(bias_row + k1);
           const int bytes = min(it.Lk - k1, W) * static_cast<int>(sizeof(T));
           if (bytes > 0) {
@@ -902,7 +958,7 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
         ++pc;
         tc_fence_after();
         uint32_t sr[W];
-        const int j0 = kv_tile<MASK>(it, step_of(j)) * C::BN;  // first key of this K/V tile
+        const int j0 = kv_key<MASK>(it, step_of(j));  // first key of this K/V tile
         // Whether some key of this tile is masked for some row of the tile
         // (the tail past Lk, the causal / window band): the same for every
         // thread of the warpgroup.
@@ -921,15 +977,18 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
           if (masked) {
             int hi = it.Lk - 1 - j0;
             if (p.win_right >= 0) hi = min(hi, qi + diag + p.win_right - j0);
-            const int lo = qi + diag - p.win_left - j0, keep = p.sink_tokens - j0;
+            const int lo = qi + diag - p.win_left - j0;
+            // (a folded tile's first columns are keys 0, 1, ...)
+            const bool folded = it.fold && step_of(j) == 0;
             col_lo = lo;
             col_hi = hi + 1;
-            col_keep = min(keep, hi + 1);
+            col_keep = folded ? min(p.sink_tokens, hi + 1 + j0) : min(p.sink_tokens - j0, hi + 1);
             const int whi = __reduce_max_sync(0xffffffffu, hi), wlo = __reduce_min_sync(0xffffffffu, lo);
+            const int wkeep = __reduce_max_sync(0xffffffffu, col_keep);
             if constexpr (QUARTERS) quarters = 0;
 #pragma unroll
             for (int qq = 0; qq < W / 32; ++qq)
-              if (32 * qq <= whi && (32 * qq + 31 >= wlo || 32 * qq < keep)) quarters |= 1u << qq;
+              if ((32 * qq <= whi && 32 * qq + 31 >= wlo) || 32 * qq < wkeep) quarters |= 1u << qq;
           }
         }
         float raw_max = -INFINITY;  // (HW_MAX) the row maximum of the raw scores
@@ -1321,7 +1380,7 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
 }
 
 template <int D, int DT, int MASK, int XF, bool ORD = false>
-static cudaError_t launch_prefill_t(const PrefillParams& p, int grid, cudaStream_t stream) {
+static cudaError_t launch_prefill_t(const PrefillArgs<MASK>& p, int grid, cudaStream_t stream) {
   using C = PrefillCfg<D, DT>;
   auto kern = attn_prefill_kernel<D, DT, MASK, XF, ORD>;
   const int smem = static_cast<int>(sizeof(PrefillSmem<C, ORD>)) + 1024;
@@ -1345,7 +1404,7 @@ static cudaError_t launch_prefill_t(const PrefillParams& p, int grid, cudaStream
 }
 
 template <int DT, int MASK>
-static cudaError_t launch_prefill_x(const PrefillParams& p, int grid, int xf,
+static cudaError_t launch_prefill_x(const PrefillArgs<MASK>& p, int grid, int xf,
                                    cudaStream_t stream) {
   // Group mode and paged caches take the sorted work order (no bias there).
   if (p.cu_q != nullptr || p.seqlens_k != nullptr) {
@@ -1368,7 +1427,7 @@ static cudaError_t launch_prefill_x(const PrefillParams& p, int grid, int xf,
 
 // All types of one mask.
 template <int MASK>
-static cudaError_t launch_prefill_m(const PrefillParams& p, int grid, int dt, int xf,
+static cudaError_t launch_prefill_m(const PrefillArgs<MASK>& p, int grid, int dt, int xf,
                                    cudaStream_t stream) {
   if (dt == kDtBF16) return launch_prefill_x<kDtBF16, MASK>(p, grid, xf, stream);
   if (dt == kDtF16) return launch_prefill_x<kDtF16, MASK>(p, grid, xf, stream);
@@ -1383,7 +1442,7 @@ static cudaError_t launch_prefill_m(const PrefillParams& p, int grid, int dt, in
 
 #ifdef ATTN_PREFILL_KEEP
 template <>
-cudaError_t launch_prefill_keep_d<ATTN_PREFILL_D>(const PrefillParams& p, int grid, int dt, int xf,
+cudaError_t launch_prefill_keep_d<ATTN_PREFILL_D>(const PrefillKeepParams& p, int grid, int dt, int xf,
                                                   cudaStream_t stream) {
   return launch_prefill_m<kMaskBandKeep>(p, grid, dt, xf, stream);
 }

@@ -324,7 +324,8 @@ int attn_paged_window_pages(int Lq, int page_size, int max_pages_per_seq, const 
  *   order (no mask, more than 1408 items or 160 CTAs, or no more items than
  *   CTAs), ATTN_ERR_INVALID for non-positive sizes, Hq % Hkv != 0 or NULL
  *   buffers.  Host only: needs no device.  opts as for attn_fwd (only the
- *   mask fields are read); may be NULL. */
+ *   mask fields are read, and with sink_tokens whether there is ALiBi or a
+ *   bias); may be NULL. */
 attn_status attn_dense_schedule(int B, int Hq, int Hkv, int Lq, int Lk, const attn_opts* opts,
                                 int grid, int32_t* off, int32_t* item);
 

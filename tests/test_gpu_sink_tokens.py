@@ -39,6 +39,14 @@ DENSE = [
     (1, 2, 2, 500, 400, 128, "bf16", False, (50, 10), 7, 0.0, False, True),    # top-left, rows past the keys
     (1, 16, 1, 200, 200, 128, "bf16", True, (16, -1), 2, 0.0, False, False),   # 16 heads per tile
     (1, 1, 1, 1, 1, 64, "f16", True, (0, -1), 1, 0.0, False, False),
+    # first tokens in the band's first tile: whole multiples of 8 and not, the most and one more
+    (1, 2, 2, 1000, 1000, 128, "bf16", True, (150, -1), 8, 0.0, False, False),
+    (1, 8, 2, 1111, 1111, 64, "f16", True, (255, -1), 63, 30.0, True, False),
+    (2, 4, 4, 777, 1500, 128, "bf16", True, (301, -1), 64, 0.0, True, False),
+    (1, 2, 1, 900, 900, 128, "bf16", True, (200, -1), 65, 0.0, False, False),
+    (1, 2, 2, 640, 640, 64, "bf16", False, (100, 200), 17, 0.0, False, False),
+    (1, 2, 2, 500, 900, 128, "f16", False, (40, 3), 33, 0.0, False, True),
+    (1, 1, 1, 2000, 2000, 64, "bf16", True, (0, -1), 1, 0.0, False, False),
 ]
 
 
@@ -90,6 +98,7 @@ VARLEN = [
     ([1, 0, 130, 257, 500], None, 4, 2, 128, "bf16", True, (64, -1), 4),
     ([5, 100, 64], [300, 100, 1], 2, 2, 64, "f16", False, (32, 16), 140),
     ([513, 1, 129], [513, 1000, 0], 8, 2, 128, "bf16", False, (200, 0), 1),
+    ([700, 3, 1025], [900, 400, 1025], 4, 4, 64, "f16", True, (130, -1), 60),
 ]
 
 
