@@ -185,6 +185,7 @@ struct TreeParams {
   float2* ml_part;            // [2 * grid][rows]
   int4* cut;                  // [grid] for the merge kernel: the unit to merge there
   int B, T, Hq, Hkv, g, words;
+  int g_magic;                // ceil(2^16 / g)
   int qpt;                    // queries per 128-row tile
   int two_tiles;              // units of two query tiles
   int units;                  // (query block, kv head) pairs per sequence

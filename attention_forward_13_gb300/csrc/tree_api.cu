@@ -157,6 +157,7 @@ attn_status attn_fwd_paged_tree(const void* q, const void* k_pool, const void* v
   if (host_device_state(&p.err, &num_sms) != ATTN_OK) return ATTN_ERR_CUDA;
   const bool bf16 = dtype == ATTN_BF16;
   p.g = g;
+  p.g_magic = (65536 + g - 1) / g;
   p.qpt = queries_per_tile(g);
   p.two_tiles = T > p.qpt ? 1 : 0;
   const int per = p.qpt * (p.two_tiles ? 2 : 1);

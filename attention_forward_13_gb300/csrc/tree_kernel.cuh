@@ -77,7 +77,8 @@ struct TreeSmem {
   uint64_t teardown;
   float2 x[2][128];     // (m, l) of a row, per warpgroup
   int scan[16];
-  int4 walk[8];         // each softmax warp's place (TreeWalk)
+  int4 desc[4][3];      // segments on their way from the producer to the other roles
+  uint64_t desc_full[4], desc_empty[4];
   uint8_t order[256];   // unit mode: the sequences, most tiles first
   uint32_t tmem_base;
   int abort_flag;
@@ -266,6 +267,42 @@ __device__ __forceinline__ bool tree_next(const TreeParams& p, const uint8_t* or
   return true;
 }
 
+// Segments are worked out once, by the K producer, which runs ahead of the
+// others, and handed on through shared memory (three 16-byte words): the
+// softmax warps' time between two segments is all dependent scalar code, and
+// the walk was a third of it.  n = -1 ends the walk.
+__device__ __forceinline__ void tree_pack(const TreeSeg& s, int4 (&w)[3]) {
+  w[0] = make_int4(s.b, s.hk, s.m0, s.n);
+  w[1] = make_int4(s.k0, s.q.L, s.q.base, s.q.n);
+  w[2] = make_int4(s.q.nkeep, s.q.gap, s.q.tiles, s.whole ? 1 : 0);
+}
+template <class C>
+__device__ __forceinline__ void tree_read(const TreeSmem<C>& sm, int slot, TreeSeg& s) {
+  const int4 a = sm.desc[slot][0], b = sm.desc[slot][1], c = sm.desc[slot][2];
+  s.b = a.x, s.hk = a.y, s.m0 = a.z, s.n = a.w;
+  s.k0 = b.x, s.q.L = b.y, s.q.base = b.z, s.q.n = b.w;
+  s.q.nkeep = c.x, s.q.gap = c.y, s.q.tiles = c.z, s.whole = c.w != 0;
+}
+// The k-th segment is in its slot (false: a wait gave up).  Released when the
+// warp needs it no more.
+template <class C>
+__device__ __forceinline__ bool tree_wait(TreeSmem<C>& sm, const Waiter& w, int k) {
+  return __all_sync(0xffffffffu, w.wait(&sm.desc_full[k & 3], (k >> 2) & 1, kErrTreeWait));
+}
+template <class C>
+__device__ __forceinline__ void tree_release(TreeSmem<C>& sm, int k) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.desc_empty[k & 3]);
+}
+template <class C>
+__device__ __forceinline__ bool tree_take(TreeSmem<C>& sm, const Waiter& w, int& k, TreeSeg& s) {
+  if (!tree_wait(sm, w, k)) return false;
+  tree_read(sm, k & 3, s);
+  tree_release(sm, k);
+  ++k;
+  return s.n >= 0;
+}
+
 __device__ __forceinline__ int tree_tile(const TreeSeq& q, int k) { return k < q.nkeep ? k : k + q.gap; }
 
 // Pool row of page piece `lane` of a tile (box of min(page, 128) rows).  Pieces
@@ -307,7 +344,9 @@ __device__ __forceinline__ void quad_transpose(uint32_t (&w)[16], int lane) {
     }
 }
 
-template <int D, bool BF16, bool SOFTCAP>
+// pair: units of two query tiles, one per softmax warpgroup; else one tile and two
+// streams of K/V tiles (see the top of the file).
+template <int D, bool BF16, bool SOFTCAP, bool pair>
 __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
     attn_tree_kernel(const __grid_constant__ TreeParams p) {
   using C = TreeCfg<D>;
@@ -322,9 +361,8 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
   }
   TreeSmem<C>& sm = *reinterpret_cast<TreeSmem<C>*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool pair = p.two_tiles != 0;        // one query tile per warpgroup
-  const int nq = pair ? 2 : 1;               // Q buffers
-  const int ns = C::NBUF - nq;               // ring slots
+  constexpr int nq = pair ? 2 : 1;           // Q buffers
+  constexpr int ns = C::NBUF - nq;           // ring slots
 
   pdl_launch_dependents();  // the merge kernel may be set up; it waits for this grid's end
   if (threadIdx.x == 0) {
@@ -343,6 +381,10 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
     }
     mbar_init(&sm.xch, 256);
     mbar_init(&sm.xread, 256);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sm.desc_full[i], 1);
+      mbar_init(&sm.desc_empty[i], 10);  // 8 softmax warps, the V producer, the MMA issuer
+    }
     mbar_init(&sm.teardown, 1);
     sm.abort_flag = 0;
     fence_mbar_init();
@@ -429,7 +471,28 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
         ++armed;
         skip(1);
       };
-      for (; ok && tree_next(p, sm.order, walk, s);) {
+      int dk = 0;  // segments handed on or taken
+      while (ok) {
+        if (!v_warp) {
+          s.n = -1;
+          bool more;
+          while ((more = tree_next(p, sm.order, walk, s)) && s.n == 0 && !s.whole) {
+          }
+          if (!more) s.n = -1;
+          ok = __all_sync(0xffffffffu, w.wait(&sm.desc_empty[dk & 3], ((dk >> 2) & 1) ^ 1, kErrTreeWait));
+          if (!ok) break;
+          if (lane == 0) {
+            int4 d[3];
+            tree_pack(s, d);
+            for (int i = 0; i < 3; ++i) sm.desc[dk & 3][i] = d[i];
+            mbar_arrive(&sm.desc_full[dk & 3]);
+          }
+          __syncwarp();
+          ++dk;
+          if (!more) break;
+        } else if (!tree_take(sm, w, dk, s)) {
+          break;
+        }
         const int n = __shfl_sync(0xffffffffu, s.n, 0);
         if (n == 0) continue;
         int row = tree_piece_row<C>(p, s, tree_tile(s.q, s.k0), lane);
@@ -534,7 +597,8 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       const std::integral_constant<int, 0> t0{};
       const std::integral_constant<int, 1> t1{};
       bool ok = true;
-      for (; ok && tree_next(p, sm.order, walk, s);) {
+      int dk = 0;
+      while (ok && tree_take(sm, w, dk, s)) {
         if (s.n == 0) continue;
         const int n = __shfl_sync(0xffffffffu, s.n, 0);
         const bool two = pair ? s.m0 + p.qpt < p.T : n > 1;  // both tiles in use
@@ -617,30 +681,27 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
     const int r = (warp & 3) * 32 + lane;       // row == tensor-memory lane
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + C::tm_s(t) + lane_base;
-    const int rq = r / p.g, hg = r - rq * p.g;  // query within the tile, head within the group
+    // Division of a row by the group size, in two instructions (exact below
+    // 128): the registers are better spent on scores than on keeping quotients.
+    auto div_g = [&](int x) { return (x * p.g_magic) >> 16; };
     int pc = 0, seg = 0;
     uint32_t oph = 0;  // bit i: phase of tile i's next final O
     bool ok = true;
-    // The scores take 128 of the 192 registers: what the loop over the tiles
-    // does not need stays in shared memory or is computed again.
-    if (lane == 0) sm.walk[warp] = make_int4(walk.b, walk.u, walk.k, walk.rem);
-    __syncwarp();
-    while (ok) {
-      {
-        const int4 at = sm.walk[warp];
-        TreeWalk next{at.x, at.y, at.z, at.w};
-        if (!tree_next(p, sm.order, next, s)) break;
-        __syncwarp();
-        if (lane == 0) sm.walk[warp] = make_int4(next.b, next.u, next.k, next.rem);
-        __syncwarp();
-      }
+    // The scores take 128 of the 192 registers: of the segment only what the loop
+    // over its tiles needs stays in registers, the rest is read again from shared
+    // memory where a masked tile or the epilogue asks for it.
+    auto rows_of = [&](const TreeSeg& e, int& qi, int& hq, bool& in) {  // this thread's row
+      const int rq = div_g(r);
+      qi = e.m0 + (pair ? t * p.qpt : 0) + rq;
+      hq = e.hk * p.g + (r - rq * p.g);
+      in = rq < p.qpt && qi < p.T;
+    };
+    for (int dk = 0; ok; ++dk) {
+      if (!(ok = tree_wait(sm, w, dk))) break;
+      tree_read(sm, dk & 3, s);
       const int n = s.n;
-      if (n == 0 && !s.whole) continue;
+      if (n < 0) break;
       const int live = pair ? (s.m0 + p.qpt < p.T ? 2 : 1) : min(n, 2);
-      const int qi = s.m0 + (pair ? t * p.qpt : 0) + rq;
-      const bool row_in = rq < p.qpt && qi < p.T;       // this thread has a row to write
-      const bool row_live = row_in && qi < s.q.n;       // ... that sees anything
-      const int hq = s.hk * p.g + hg;
       const int nt = t < live ? (pair ? n : (n + 1 - t) / 2) : 0;
       float m_use = -INFINITY, l = 0.0f;
       for (int j = 0; j < nt; ++j) {
@@ -650,10 +711,18 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
         // Which keys of a masked tile the row sees, worked out (and its mask
         // words fetched) while the tensor core computes the scores.
         uint32_t vis[4] = {0u, 0u, 0u, 0u};
-        if (masked && row_live) {
-          const int64_t node_row = static_cast<int64_t>(s.b) * p.T + qi;
+        TreeSeg e;
+        int qi, hq;
+        bool row_live = false;
+        if (masked) {
+          tree_read(sm, dk & 3, e);
+          rows_of(e, qi, hq, row_live);
+          row_live = row_live && qi < e.q.n;  // a row that sees anything
+        }
+        if (row_live) {
+          const int64_t node_row = static_cast<int64_t>(e.b) * p.T + qi;
           const uint32_t* bits = p.tree_mask + node_row * p.words;
-          const int sh0 = j0 - s.q.base;  // first column, counted from node 0
+          const int sh0 = j0 - e.q.base;  // first column, counted from node 0
           const int wd = sh0 >> 5, bit = sh0 & 31;
           uint32_t wds[5];
 #pragma unroll
@@ -661,13 +730,13 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
             wds[c] = wd + c >= 0 && wd + c < p.words ? __ldg(bits + wd + c) : 0u;
           int lo = 0;  // lowest key before the nodes that the window leaves
           if (p.win_left >= 0)
-            lo = s.q.base + max(0, min(__ldg(p.tree_depth + node_row), s.q.n - 1)) - p.win_left;
+            lo = e.q.base + max(0, min(__ldg(p.tree_depth + node_row), e.q.n - 1)) - p.win_left;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const int k0 = j0 + 32 * c;
-            uint32_t pre = low_bits(s.q.base - k0);  // keys before the nodes
+            uint32_t pre = low_bits(e.q.base - k0);  // keys before the nodes
             if (p.win_left >= 0) pre &= ~low_bits(lo - k0) | low_bits(p.sink_tokens - k0);
-            vis[c] = pre | (__funnelshift_r(wds[c], wds[c + 1], bit) & low_bits(s.q.L - k0));
+            vis[c] = pre | (__funnelshift_r(wds[c], wds[c + 1], bit) & low_bits(e.q.L - k0));
           }
         }
         ok = __all_sync(0xffffffffu, w.wait(&sm.s_full[t], pc & 1, kErrTreeWait));
@@ -749,6 +818,11 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       // ---- epilogue.  With two query tiles each warpgroup owns its rows; with
       // two streams both hold parts of the same rows: they exchange (m, l) and
       // each merges half of the columns.
+      tree_read(sm, dk & 3, s);
+      int qi, hq;
+      bool row_in;  // this thread has a row to write
+      rows_of(s, qi, hq, row_in);
+      const bool row_live = row_in && qi < s.q.n;  // ... that saw anything
       float a0 = 1.0f, a1 = 0.0f, m = m_use;  // weights of the two streams' O
       if (!row_live) l = 0.0f, m = -INFINITY;
       if (!pair && n > 0) {
@@ -771,14 +845,14 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       float scale0 = a0, scale1 = a1, lse = -INFINITY;
       if (s.whole) {
         const float ms = m == -INFINITY ? 0.0f : m;
-        float mfin = ms, ltot = l, norm = l > 0.0f ? 1.0f / l : 0.0f;
+        float mfin = ms, ltot = l, norm = l > 0.0f ? rcp_approx(l) : 0.0f;
         if (p.sink != nullptr && row_in) {
           const float sl = p.sink[hq] * kLog2e;
           if (l > 0.0f) {
             mfin = fmaxf(ms, sl);
             const float a = ex2_approx(ms - mfin);
             ltot = l * a + ex2_approx(sl - mfin);
-            norm = a / ltot;
+            norm = a * rcp_approx(ltot);
           } else {
             mfin = sl;
             ltot = 1.0f;
@@ -794,11 +868,11 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       const int prows = pair ? 256 : 128;
       float4* part = reinterpret_cast<float4*>(p.o_part + static_cast<int64_t>(slot) * prows * D) + prow;
       // Rows of this lane's quad in O, from the tile's first query (-1: no row).
-      T* out = reinterpret_cast<T*>(p.o) + ((static_cast<int64_t>(s.b) * p.T + (qi - rq)) * p.Hq + s.hk * p.g) * D;
-      int orow[4], rrq = (r & ~3) / p.g, rhg = (r & ~3) - rrq * p.g;
+      T* out = reinterpret_cast<T*>(p.o) + ((static_cast<int64_t>(s.b) * p.T + (qi - div_g(r))) * p.Hq + s.hk * p.g) * D;
+      int orow[4], rrq = div_g(r & ~3), rhg = (r & ~3) - rrq * p.g;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        orow[i] = rrq < p.qpt && qi - rq + rrq < p.T ? (rrq * p.Hq + rhg) * D : -1;
+        orow[i] = rrq < p.qpt && qi - div_g(r) + rrq < p.T ? (rrq * p.Hq + rhg) * D : -1;
         if (++rhg == p.g) rhg = 0, ++rrq;
       }
       const bool mine = t < live;  // two tiles: this warpgroup's tile is in use
@@ -897,6 +971,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
           p.ml_part[static_cast<int64_t>(slot) * prows + prow] = make_float2(zero ? -INFINITY : m, l);
         }
       }
+      tree_release(sm, dk);
     }
   }
 
@@ -986,10 +1061,10 @@ __global__ void __launch_bounds__(256) attn_tree_merge_kernel(const __grid_const
     p.lse[(static_cast<int64_t>(b) * p.Hq + hq) * p.T + qi] = z > 0.0f ? (M + __log2f(z)) * kLn2 : -INFINITY;
 }
 
-template <int D, bool BF16, bool SOFTCAP>
+template <int D, bool BF16, bool SOFTCAP, bool pair>
 static cudaError_t launch_tree_t(const TreeParams& p, cudaStream_t stream) {
   using C = TreeCfg<D>;
-  auto kern = attn_tree_kernel<D, BF16, SOFTCAP>;
+  auto kern = attn_tree_kernel<D, BF16, SOFTCAP, pair>;
   const int smem = static_cast<int>(sizeof(TreeSmem<C>));
   static_assert(sizeof(TreeSmem<C>) <= 227 * 1024, "shared memory per block");
   // setmaxnreg.inc draws on what the block was launched with: refuse to launch
@@ -1013,12 +1088,16 @@ static cudaError_t launch_tree_t(const TreeParams& p, cudaStream_t stream) {
   return launch_pdl(attn_tree_merge_kernel<D, BF16>, dim3(p.grid, D / 8), p.two_tiles ? 256 : 128, 0, stream, p);
 }
 
+template <bool BF16, bool SOFTCAP>
+static cudaError_t launch_tree_p(const TreeParams& p, cudaStream_t stream) {
+  return p.two_tiles ? launch_tree_t<ATTN_TREE_D, BF16, SOFTCAP, true>(p, stream)
+                     : launch_tree_t<ATTN_TREE_D, BF16, SOFTCAP, false>(p, stream);
+}
+
 template <>
 cudaError_t launch_tree_d<ATTN_TREE_D>(const TreeParams& p, bool bf16, bool softcap, cudaStream_t stream) {
-  if (bf16) return softcap ? launch_tree_t<ATTN_TREE_D, true, true>(p, stream)
-                           : launch_tree_t<ATTN_TREE_D, true, false>(p, stream);
-  return softcap ? launch_tree_t<ATTN_TREE_D, false, true>(p, stream)
-                 : launch_tree_t<ATTN_TREE_D, false, false>(p, stream);
+  if (bf16) return softcap ? launch_tree_p<true, true>(p, stream) : launch_tree_p<true, false>(p, stream);
+  return softcap ? launch_tree_p<false, true>(p, stream) : launch_tree_p<false, false>(p, stream);
 }
 
 }  // namespace attn
