@@ -18,6 +18,15 @@ uint64_t host_timeout_ns();
 // result into a status.
 attn_status host_finish(cudaError_t e, const char* name);
 
+// Decode over a window with first tokens on the tree kernel (tree_api.cu): whether
+// it has enough units to balance without cutting any, and the launch.  The
+// arguments have been checked.
+bool host_chain_applies(int B, int Lq, int Hq, int Hkv, int page_size, int max_pages, const attn_opts* opts);
+attn_status host_chain(const void* q, const void* k_pool, const void* v_pool, const int32_t* block_table,
+                       const int32_t* seqlens_k, void* o, float* lse, int B, int Lq, int Hq, int Hkv, int d,
+                       bool bf16, int page_size, int num_pages, int max_pages, const attn_opts* opts,
+                       cudaStream_t stream);
+
 inline bool host_aligned(const void* p, unsigned bytes) {
   return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
 }

@@ -75,6 +75,79 @@ __global__ void __launch_bounds__(1024)
 // one does not hold all T nodes.
 int queries_per_tile(int g) { return 128 / g; }
 
+// Tile slots of the whole call, at most: the kernels count them in 32 bits.
+bool line_fits(int B, int units, int page_size, int max_pages) {
+  return static_cast<double>(B) * units * ((static_cast<double>(max_pages) * page_size + 127) / 128 + 8) <
+         2147483647.0;
+}
+
+// What the launches share: everything but the masks and the workspace.
+attn_status tree_params(TreeParams* out, const void* q, const void* k_pool, const void* v_pool,
+                        const int32_t* block_table, const int32_t* seqlens_k, void* o, float* lse, int B,
+                        int T, int Hq, int Hkv, int d, bool bf16, int page_size, int num_pages, int max_pages,
+                        const attn_opts* opts) {
+  memset(out, 0, sizeof(*out));
+  TreeParams& p = *out;
+  int num_sms = 0;
+  if (host_device_state(&p.err, &num_sms) != ATTN_OK) return ATTN_ERR_CUDA;
+  const int g = Hq / Hkv;
+  p.g = g;
+  p.g_magic = (65536 + g - 1) / g;
+  p.qpt = queries_per_tile(g);
+  p.two_tiles = T > p.qpt ? 1 : 0;
+  const int per = p.qpt * (p.two_tiles ? 2 : 1);
+  p.units = Hkv * ((T + per - 1) / per);
+  if (!line_fits(B, p.units, page_size, max_pages)) return ATTN_ERR_UNSUPPORTED;
+  {
+    const uint64_t eb = 2, row = static_cast<uint64_t>(d) * eb;
+    const uint64_t dims[5] = {(uint64_t)d, (uint64_t)g, (uint64_t)Hkv, (uint64_t)T, (uint64_t)B};
+    const uint64_t st[4] = {row, row * g, row * Hq, row * Hq * T};
+    const uint32_t box[5] = {64, (uint32_t)g, 1, (uint32_t)p.qpt, 1};
+    if (!host_make_map(&p.tm_q, q, bf16, 5, dims, st, box)) return ATTN_ERR_INVALID;
+  }
+  {
+    const uint32_t box[3] = {64, 1, (uint32_t)(page_size < 128 ? page_size : 128)};
+    const uint64_t dims[3] = {(uint64_t)d, (uint64_t)Hkv, (uint64_t)num_pages * page_size};
+    const uint64_t st[2] = {(uint64_t)d * 2, (uint64_t)Hkv * d * 2};
+    if (!host_make_map(&p.tm_k, k_pool, bf16, 3, dims, st, box)) return ATTN_ERR_INVALID;
+    if (!host_make_map(&p.tm_v, v_pool, bf16, 3, dims, st, box)) return ATTN_ERR_INVALID;
+  }
+  p.block_table = block_table;
+  p.seqlens_k = seqlens_k;
+  p.o = o;
+  p.lse = lse;
+  p.sink = opts != nullptr ? opts->sink : nullptr;
+  p.B = B;
+  p.T = T;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.words = (T + 31) / 32;
+  p.grid = num_sms < kTreeMaxCtas ? num_sms : kTreeMaxCtas;
+  p.min_share = 4;
+  p.unit_cost = 2;
+  p.page_size = page_size;
+  while ((1 << p.page_log2) < page_size) ++p.page_log2;
+  p.num_pages = num_pages;
+  p.max_pages = max_pages;
+  p.win_left = opts != nullptr && opts->use_window && opts->window_left >= 0 ? opts->window_left : -1;
+  p.sink_tokens = p.win_left >= 0 ? opts->sink_tokens : 0;
+  p.scale = host_scale(opts, d);
+  p.scale_log2 = p.scale * kLog2e;
+  p.softcap = opts != nullptr && opts->softcap > 0.0f ? opts->softcap : 0.0f;
+  p.softcap_inv = p.softcap > 0.0f ? 1.0f / p.softcap : 0.0f;
+  p.timeout_ns = host_timeout_ns();
+  return ATTN_OK;
+}
+
+attn_status tree_launch(const TreeParams& p, int d, bool bf16, const char* what, cudaStream_t s) {
+  const bool cap = p.softcap > 0.0f;
+  char name[128];
+  const int n = snprintf(name, sizeof(name), "attn_tree%s_paged_tcgen05_d%d_%s_%s_%s", what, d,
+                         bf16 ? "bf16" : "f16", cap ? "softcap" : "nocap", p.two_tiles ? "m256" : "m128");
+  if (p.o_part != nullptr) snprintf(name + n, sizeof(name) - n, "+attn_tree_merge_d%d", d);
+  return host_finish(d == 64 ? launch_tree_d<64>(p, bf16, cap, s) : launch_tree_d<128>(p, bf16, cap, s), name);
+}
+
 }  // namespace
 
 extern "C" {
@@ -152,71 +225,42 @@ attn_status attn_fwd_paged_tree(const void* q, const void* k_pool, const void* v
   if (left >= 0 && tree_depth == nullptr) return ATTN_ERR_INVALID;
 
   TreeParams p;
-  memset(&p, 0, sizeof(p));
-  int num_sms = 0;
-  if (host_device_state(&p.err, &num_sms) != ATTN_OK) return ATTN_ERR_CUDA;
-  const bool bf16 = dtype == ATTN_BF16;
-  p.g = g;
-  p.g_magic = (65536 + g - 1) / g;
-  p.qpt = queries_per_tile(g);
-  p.two_tiles = T > p.qpt ? 1 : 0;
-  const int per = p.qpt * (p.two_tiles ? 2 : 1);
-  p.units = Hkv * ((T + per - 1) / per);
-  // Tile slots of the whole call, at most: the kernels count them in 32 bits.
-  if (static_cast<int64_t>(B) * p.units * ((static_cast<int64_t>(max_pages_per_seq) * page_size + 127) / 128 + 8) >
-      0x7fffffffLL)
-    return ATTN_ERR_UNSUPPORTED;
-  {
-    const uint64_t eb = 2, row = static_cast<uint64_t>(d) * eb;
-    const uint64_t dims[5] = {(uint64_t)d, (uint64_t)g, (uint64_t)Hkv, (uint64_t)T, (uint64_t)B};
-    const uint64_t st[4] = {row, row * g, row * Hq, row * Hq * T};
-    const uint32_t box[5] = {64, (uint32_t)g, 1, (uint32_t)p.qpt, 1};
-    if (!host_make_map(&p.tm_q, q, bf16, 5, dims, st, box)) return ATTN_ERR_INVALID;
-  }
-  {
-    const uint32_t box[3] = {64, 1, (uint32_t)(page_size < 128 ? page_size : 128)};
-    const uint64_t dims[3] = {(uint64_t)d, (uint64_t)Hkv, (uint64_t)num_pages * page_size};
-    const uint64_t st[2] = {(uint64_t)d * 2, (uint64_t)Hkv * d * 2};
-    if (!host_make_map(&p.tm_k, k_pool, bf16, 3, dims, st, box)) return ATTN_ERR_INVALID;
-    if (!host_make_map(&p.tm_v, v_pool, bf16, 3, dims, st, box)) return ATTN_ERR_INVALID;
-  }
-  p.block_table = block_table;
-  p.seqlens_k = seqlens_k;
+  const attn_status st = tree_params(&p, q, k_pool, v_pool, block_table, seqlens_k, o, lse, B, T, Hq, Hkv, d,
+                                     dtype == ATTN_BF16, page_size, num_pages, max_pages_per_seq, opts);
+  if (st != ATTN_OK) return st;
   p.tree_lens = tree_lens;
   p.tree_mask = tree_mask;
   p.tree_depth = tree_depth;
-  p.o = o;
-  p.lse = lse;
-  p.sink = opts != nullptr ? opts->sink : nullptr;
-  p.B = B;
-  p.T = T;
-  p.Hq = Hq;
-  p.Hkv = Hkv;
-  p.words = (T + 31) / 32;
-  p.grid = num_sms < kTreeMaxCtas ? num_sms : kTreeMaxCtas;
-  p.min_share = 4;
-  p.unit_cost = 2;
-  p.page_size = page_size;
-  while ((1 << p.page_log2) < page_size) ++p.page_log2;
-  p.num_pages = num_pages;
-  p.max_pages = max_pages_per_seq;
-  p.win_left = left;
-  p.sink_tokens = left >= 0 ? opts->sink_tokens : 0;
-  p.scale = host_scale(opts, d);
-  p.scale_log2 = p.scale * kLog2e;
-  p.softcap = opts != nullptr && opts->softcap > 0.0f ? opts->softcap : 0.0f;
-  p.softcap_inv = p.softcap > 0.0f ? 1.0f / p.softcap : 0.0f;
-  p.timeout_ns = host_timeout_ns();
   const size_t pieces = 2 * static_cast<size_t>(p.grid), rows = p.two_tiles ? 256 : 128;
   p.o_part = static_cast<float*>(workspace);
   p.ml_part = reinterpret_cast<float2*>(p.o_part + pieces * rows * d);
   p.cut = reinterpret_cast<int4*>(p.ml_part + pieces * rows);
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool cap = p.softcap > 0.0f;
-  char name[128];
-  snprintf(name, sizeof(name), "attn_tree_paged_tcgen05_d%d_%s_%s_%s+attn_tree_merge_d%d", d,
-           bf16 ? "bf16" : "f16", cap ? "softcap" : "nocap", p.two_tiles ? "m256" : "m128", d);
-  return host_finish(d == 64 ? launch_tree_d<64>(p, bf16, cap, s) : launch_tree_d<128>(p, bf16, cap, s), name);
+  return tree_launch(p, d, dtype == ATTN_BF16, "", static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
+
+namespace attn {
+
+bool host_chain_applies(int B, int Lq, int Hq, int Hkv, int page_size, int max_pages, const attn_opts* opts) {
+  const int g = Hq / Hkv;
+  int sms = 0;
+  if (opts == nullptr || host_device_state(nullptr, &sms) != ATTN_OK) return false;
+  const int grid = sms < kTreeMaxCtas ? sms : kTreeMaxCtas;
+  return opts->use_window && opts->window_left >= 0 && opts->sink_tokens > 0 && !opts->top_left &&
+         opts->alibi_slopes == nullptr && (opts->causal || opts->window_right == 0 || Lq == 1) &&
+         Lq <= queries_per_tile(g) && Hq <= 65535 && B <= 256 && static_cast<int64_t>(B) * Hkv >= 2 * grid &&
+         line_fits(B, Hkv, page_size, max_pages);
+}
+
+attn_status host_chain(const void* q, const void* k_pool, const void* v_pool, const int32_t* block_table,
+                       const int32_t* seqlens_k, void* o, float* lse, int B, int Lq, int Hq, int Hkv, int d,
+                       bool bf16, int page_size, int num_pages, int max_pages, const attn_opts* opts,
+                       cudaStream_t stream) {
+  TreeParams p;
+  const attn_status st = tree_params(&p, q, k_pool, v_pool, block_table, seqlens_k, o, lse, B, Lq, Hq, Hkv, d,
+                                     bf16, page_size, num_pages, max_pages, opts);
+  return st != ATTN_OK ? st : tree_launch(p, d, bf16, "_chain", stream);
+}
+
+}  // namespace attn

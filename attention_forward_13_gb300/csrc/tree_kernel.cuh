@@ -35,6 +35,9 @@
 //    order (K0, K1, V0, K2, V1, ... for two streams, K0, V0, K1, V1, ... for two
 //    query tiles); what Q does not take of shared memory is ring (d = 128: 6
 //    slots of 32 KB, or 5 beside two query tiles).
+//  * without masks (tree_mask NULL) the T queries are the sequence's last tokens, a
+//    plain causal chunk: single-token decode with a window and first tokens runs
+//    here where there are enough units (attn_fwd_paged).
 //  * only the tiles that hold drafted nodes, the sequence's end or a window's
 //    edge are masked, from a 128-bit visibility word per row.
 #pragma once
@@ -194,7 +197,8 @@ __device__ __forceinline__ int tree_item(int G, int c, int round) {
 __device__ inline bool tree_unit_mode(const TreeParams& p, const TreeLine& line, int* scratch, int* cost,
                                       uint8_t* order) {
   const int N = p.B * p.units, G = gridDim.x, warp = threadIdx.x >> 5;
-  if (p.B > 256 || N < 2 * G || N > 16 * G) return false;
+  const bool always = p.o_part == nullptr;  // no workspace for pieces: the host has checked the counts
+  if (p.B > 256 || N < 2 * G || (N > 16 * G && !always)) return always;
   const int b = threadIdx.x;
   if (b < p.B) cost[b] = tree_seq(p, b).slots;
   __syncthreads();
@@ -213,7 +217,7 @@ __device__ inline bool tree_unit_mode(const TreeParams& p, const TreeLine& line,
   __syncthreads();
   for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) hand = max(hand, scratch[i]);
   __syncthreads();
-  return hand <= line.q + line.q / 16 + 2 * p.unit_cost + 8;
+  return always || hand <= line.q + line.q / 16 + 2 * p.unit_cost + 8;
 }
 
 // A CTA's walk along the line, one segment (a run of tiles of one unit) at a time.
@@ -410,7 +414,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
   tc_fence_after();
   if (deal) {
     walk = TreeWalk{-2, 0, 0, 1};
-    if (threadIdx.x == 0) p.cut[cta] = make_int4(-1, 0, 0, 0);
+    if (threadIdx.x == 0 && p.o_part != nullptr) p.cut[cta] = make_int4(-1, 0, 0, 0);
   } else if (walk.b < 0) {
     walk.rem = 0;
     if (threadIdx.x == 0) p.cut[cta] = make_int4(-1, 0, 0, 0);
@@ -696,6 +700,10 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       hq = e.hk * p.g + (r - rq * p.g);
       in = rq < p.qpt && qi < p.T;
     };
+    // Whether the row may see anything: a node in use; in a chain, a position.
+    auto sees = [&](const TreeSeg& e, int qi) {
+      return p.tree_mask != nullptr ? qi < e.q.n : e.q.L - p.T + qi >= 0;
+    };
     for (int dk = 0; ok; ++dk) {
       if (!(ok = tree_wait(sm, w, dk))) break;
       tree_read(sm, dk & 3, s);
@@ -717,9 +725,17 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
         if (masked) {
           tree_read(sm, dk & 3, e);
           rows_of(e, qi, hq, row_live);
-          row_live = row_live && qi < e.q.n;  // a row that sees anything
+          row_live = row_live && sees(e, qi);
         }
-        if (row_live) {
+        if (row_live && p.tree_mask == nullptr) {
+          // A chain: keys up to the query's own position, within the window.
+          const int pos = e.q.L - p.T + qi, lo = p.win_left >= 0 ? pos - p.win_left : 0;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int k0 = j0 + 32 * c;
+            vis[c] = low_bits(pos + 1 - k0) & (~low_bits(lo - k0) | low_bits(p.sink_tokens - k0));
+          }
+        } else if (row_live) {
           const int64_t node_row = static_cast<int64_t>(e.b) * p.T + qi;
           const uint32_t* bits = p.tree_mask + node_row * p.words;
           const int sh0 = j0 - e.q.base;  // first column, counted from node 0
@@ -822,7 +838,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
       int qi, hq;
       bool row_in;  // this thread has a row to write
       rows_of(s, qi, hq, row_in);
-      const bool row_live = row_in && qi < s.q.n;  // ... that saw anything
+      const bool row_live = row_in && sees(s, qi);
       float a0 = 1.0f, a1 = 0.0f, m = m_use;  // weights of the two streams' O
       if (!row_live) l = 0.0f, m = -INFINITY;
       if (!pair && n > 0) {
@@ -1084,7 +1100,7 @@ static cudaError_t launch_tree_t(const TreeParams& p, cudaStream_t stream) {
     configured.fetch_or(bit, std::memory_order_relaxed);
   }
   e = launch_pdl(kern, dim3(p.grid), C::THREADS, smem, stream, p);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.o_part == nullptr) return e;
   return launch_pdl(attn_tree_merge_kernel<D, BF16>, dim3(p.grid, D / 8), p.two_tiles ? 256 : 128, 0, stream, p);
 }
 

@@ -183,6 +183,49 @@ def test_paged_with_the_hole_freed(case):
     no_device_error()
 
 
+MANY = [
+    # B, longest, Lq, Hq, Hkv, d, page, dtype, window, keep, cap, sink: enough (sequence, kv head)
+    # pairs for whole ones to be dealt to the SMs
+    (40, 700, 1, 16, 8, 64, 16, "f16", 100, 40, 0.0, False),
+    (64, 900, 1, 24, 8, 128, 64, "bf16", 256, 4, 0.0, True),
+    (160, 300, 4, 8, 2, 64, 32, "bf16", 33, 1, 30.0, True),     # four queries, shorter sequences too
+    (256, 200, 2, 16, 2, 64, 128, "f16", 0, 130, 0.0, False),   # 8 heads a pair, the most sequences
+    (320, 90, 1, 2, 1, 64, 16, "bf16", 20, 3, 0.0, False),      # more: the other kernel
+]
+
+
+@gpu
+@pytest.mark.parametrize("case", MANY, ids=[str(i) for i in range(len(MANY))])
+def test_paged_with_many_sequences(case):
+    B, most, Lq, Hq, Hkv, d, page, dt, win, keep, cap, sink = case
+    rng = np.random.default_rng(B)
+    lens = [0, 1, Lq, max(0, Lq - 1), most] + [int(x) for x in rng.integers(0, most + 1, B - 5)]
+    npages = sum(-(-L // page) for L in lens) + 5
+    inp = inputs.paged(lens, Lq, Hq, Hkv, d, page, npages, dtype=dt, seed=B + page, softcap=cap, with_sink=sink)
+    ro, rl = _paged_ref(inp, win, keep, cap, d)
+    bt, kp, vp = inp.block_table.clone(), inp.k_pool.clone(), inp.v_pool.clone()
+    for b, L in enumerate(lens):
+        held = -(-L // page)
+        if L % page:
+            kp[bt[b, held - 1], L % page:] = float("nan")
+            vp[bt[b, held - 1], L % page:] = float("nan")
+        bt[b, -(-keep // page):max(0, L - Lq - win) // page] = -1
+        bt[b, held:] = -1
+    args = (cuda(inp.q), cuda(kp), cuda(vp), cuda(bt), cuda(inp.seqlens_k))
+    kw = dict(causal=True, softcap=cap, sink=cuda(inp.sink), window=(win, -1), sink_tokens=keep)
+    o, lse = A.attn_fwd_paged(*args, **kw)
+    assert ("chain" in A.attn_last_kernel_name()) == (B <= 256)
+    torch.cuda.synchronize()
+    no_device_error()
+    check(o, lse, ro, rl, "many")
+    o2, lse2 = A.attn_fwd_paged_noalloc(*args, **kw)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    o3, lse3 = A.attn_fwd_paged(*args, num_splits=2, **kw)  # the splitting kernel
+    assert "decode" in A.attn_last_kernel_name()
+    check(o3, lse3, ro, rl, "split")
+    no_device_error()
+
+
 @gpu
 def test_zero_and_unbounded_are_what_they_were():
     """sink_tokens without a left bound, and 0 with one, give the bits of the call without it."""
