@@ -75,17 +75,15 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _call(fn, device, stream, *args):
-    """Calls a library function whose last argument is the stream, with ``device`` current."""
-    here = torch.cuda.current_device()
+def _call(fn, device, *args):
+    """Calls a library function whose last argument is the stream: ``device``'s current one."""
     if device.type != "cuda":
         raise ValueError("the tensors must be on a CUDA device")
+    here = torch.cuda.current_device()
     if device.index != here:
         with torch.cuda.device(device):
-            return fn(*args, _stream(stream))
-    if stream is None and _raw_stream is not None:
-        return fn(*args, _raw_stream(here))
-    return fn(*args, _stream(stream))
+            return fn(*args, _stream(None))
+    return fn(*args, _raw_stream(here) if _raw_stream is not None else _stream(None))
 
 
 def _opts(scale, causal, softcap, sink, window=None, top_left=False, alibi=None, bias=None,
@@ -356,12 +354,25 @@ def _ints(device, names, *tensors):
             raise ValueError(f"{names} must be contiguous int32 on {device}")
 
 
+def _on_stream(fn):
+    """With ``stream`` given, the call runs with that stream current: what it allocates (and
+    frees again) then belongs to the stream that uses it."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kwargs):
+        if stream is None:
+            return fn(*args, **kwargs)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kwargs)
+    return call
+
+
 def _data(t):
     """The address of a tensor for the C library (None: NULL)."""
     return None if t is None else t.data_ptr()
 
 
-def attn_tree_mask(parents, tree_lens=None, mask=None, depth=None, stream=None):
+@_on_stream
+def attn_tree_mask(parents, tree_lens=None, mask=None, depth=None):
     """Visibility masks and depths of draft trees.  parents int32 [B,T] (-1: follows the
     sequence's last token), tree_lens int32 [B] or None.  Returns (mask int32
     [B,T,ceil(T/32)], its 32 bits per word the nodes a node sees, depth int32 [B,T])."""
@@ -375,14 +386,15 @@ def attn_tree_mask(parents, tree_lens=None, mask=None, depth=None, stream=None):
     if mask.shape != (B, T, W) or depth.shape != (B, T) or \
             (tree_lens is not None and tree_lens.shape != (B,)):
         raise ValueError("tree_lens is [B], mask [B,T,ceil(T/32)], depth [B,T]")
-    _check(_call(library().attn_tree_mask, dev, stream, parents.data_ptr(), _data(tree_lens),
+    _check(_call(library().attn_tree_mask, dev, parents.data_ptr(), _data(tree_lens),
                  mask.data_ptr(), depth.data_ptr(), B, T), "attn_tree_mask")
     return mask, depth
 
 
+@_on_stream
 def attn_fwd_paged_tree(q, k_pool, v_pool, block_table, seqlens_k, tree_mask, tree_lens=None,
                         tree_depth=None, o=None, lse=True, scale=None, softcap=0.0, sink=None,
-                        workspace=None, stream=None, window=None, sink_tokens=0):
+                        workspace=None, window=None, sink_tokens=0):
     """Attention of drafted nodes over a paged cache.  q [B,T,Hq,d]; the nodes' K/V are the
     last T (or tree_lens[b]) of the seqlens_k[b] positions; node i sees every earlier
     position and the nodes of its tree_mask row (attn_tree_mask).  ``window`` = (left, -1)
@@ -418,7 +430,7 @@ def attn_fwd_paged_tree(q, k_pool, v_pool, block_table, seqlens_k, tree_mask, tr
     if sink is not None:
         sink = _check_sink(sink, Hq, dev)
     opts = _opts(scale, False, softcap, sink, window, sink_tokens=sink_tokens)
-    st = _call(library().attn_fwd_paged_tree, dev, stream, q.data_ptr(), k_pool.data_ptr(),
+    st = _call(library().attn_fwd_paged_tree, dev, q.data_ptr(), k_pool.data_ptr(),
                v_pool.data_ptr(), block_table.data_ptr(), seqlens_k.data_ptr(), tree_mask.data_ptr(),
                _data(tree_lens), _data(tree_depth), o.data_ptr(), _data(lse_t), B, T, Hq, Hkv, d,
                _dtype_code(q), page, num_pages, block_table.shape[1], workspace.data_ptr(),
@@ -454,7 +466,8 @@ def _cache_state(block_table, seqlens, page_refs, *per_sequence):
     return dev, B, max_pages
 
 
-def attn_cache_reorder(block_table, seqlens, page_refs, index, page_size, stream=None):
+@_on_stream
+def attn_cache_reorder(block_table, seqlens, page_refs, index, page_size):
     """New sequence b is old sequence index[b] (int32 [B_out]; -1: an empty one): forks where
     an index repeats, permutes, frees what nobody takes.  Returns (block_table [B_out,
     max_pages], seqlens [B_out], page_refs)."""
@@ -463,14 +476,15 @@ def attn_cache_reorder(block_table, seqlens, page_refs, index, page_size, stream
     n = index.shape[0]
     table_out = torch.empty((n, max_pages), dtype=torch.int32, device=dev)
     lens_out, refs_out = torch.empty_like(index), torch.empty_like(page_refs)
-    _check(_call(library().attn_cache_reorder, dev, stream, block_table.data_ptr(), seqlens.data_ptr(),
+    _check(_call(library().attn_cache_reorder, dev, block_table.data_ptr(), seqlens.data_ptr(),
                  page_refs.data_ptr(), index.data_ptr(), table_out.data_ptr(), lens_out.data_ptr(),
                  refs_out.data_ptr(), B, n, max_pages, page_refs.shape[0], int(page_size)),
            "attn_cache_reorder")
     return table_out, lens_out, refs_out
 
 
-def attn_cache_reserve(k_pool, v_pool, block_table, seqlens, page_refs, add, stream=None):
+@_on_stream
+def attn_cache_reserve(k_pool, v_pool, block_table, seqlens, page_refs, add):
     """Room for add[b] (int32 [B]) more tokens per sequence; shared partly filled last pages
     are copied first.  Returns (block_table, seqlens + add, page_refs, free int32 [1]: the
     free pages left, or minus the pages missing, and then nothing has changed)."""
@@ -478,15 +492,15 @@ def attn_cache_reserve(k_pool, v_pool, block_table, seqlens, page_refs, add, str
     layers, num_pages, page, row = _pools(k_pool, v_pool, page_refs)
     table_out, lens_out = torch.empty_like(block_table), torch.empty_like(seqlens)
     refs_out, free = torch.empty_like(page_refs), torch.empty(1, dtype=torch.int32, device=dev)
-    _check(_call(library().attn_cache_reserve, dev, stream, k_pool.data_ptr(), v_pool.data_ptr(),
+    _check(_call(library().attn_cache_reserve, dev, k_pool.data_ptr(), v_pool.data_ptr(),
                  block_table.data_ptr(), seqlens.data_ptr(), page_refs.data_ptr(), add.data_ptr(),
                  table_out.data_ptr(), lens_out.data_ptr(), refs_out.data_ptr(), free.data_ptr(), B,
                  max_pages, num_pages, page, layers, row), "attn_cache_reserve")
     return table_out, lens_out, refs_out, free
 
 
-def attn_cache_accept(k_pool, v_pool, block_table, seqlens, page_refs, path, path_lens, tree_lens,
-                      stream=None):
+@_on_stream
+def attn_cache_accept(k_pool, v_pool, block_table, seqlens, page_refs, path, path_lens, tree_lens):
     """Keeps of each sequence's drafted nodes (the last tree_lens[b] positions) the nodes
     path[b, :path_lens[b]] (int32 [B,A], rising), moved together behind the tokens before
     them, and gives the pages past them back.  Returns (seqlens, page_refs); the pools are
@@ -496,7 +510,7 @@ def attn_cache_accept(k_pool, v_pool, block_table, seqlens, page_refs, path, pat
     if path.dim() != 2:
         raise ValueError("path must be [B,A]")
     lens_out, refs_out = torch.empty_like(seqlens), torch.empty_like(page_refs)
-    _check(_call(library().attn_cache_accept, dev, stream, k_pool.data_ptr(), v_pool.data_ptr(),
+    _check(_call(library().attn_cache_accept, dev, k_pool.data_ptr(), v_pool.data_ptr(),
                  block_table.data_ptr(), seqlens.data_ptr(), page_refs.data_ptr(), path.data_ptr(),
                  path_lens.data_ptr(), tree_lens.data_ptr(), lens_out.data_ptr(), refs_out.data_ptr(), B,
                  path.shape[1], max_pages * page, max_pages, num_pages, page, layers, row),
@@ -504,7 +518,8 @@ def attn_cache_accept(k_pool, v_pool, block_table, seqlens, page_refs, path, pat
     return lens_out, refs_out
 
 
-def attn_cache_compact(k_pool, v_pool, block_table, seqlens, page_refs, stream=None):
+@_on_stream
+def attn_cache_compact(k_pool, v_pool, block_table, seqlens, page_refs):
     """Moves the live pages to the pool's front (in place).  Returns (block_table, page_refs,
     page_map int32 [num_pages]: where each live page is now, -1 for a free one)."""
     dev, B, max_pages = _cache_state(block_table, seqlens, page_refs)
@@ -512,7 +527,7 @@ def attn_cache_compact(k_pool, v_pool, block_table, seqlens, page_refs, stream=N
     table_out, refs_out = torch.empty_like(block_table), torch.empty_like(page_refs)
     page_map = torch.empty_like(page_refs)
     work = torch.empty(num_pages + 1, dtype=torch.int32, device=dev)
-    _check(_call(library().attn_cache_compact, dev, stream, k_pool.data_ptr(), v_pool.data_ptr(),
+    _check(_call(library().attn_cache_compact, dev, k_pool.data_ptr(), v_pool.data_ptr(),
                  block_table.data_ptr(), seqlens.data_ptr(), page_refs.data_ptr(), table_out.data_ptr(),
                  refs_out.data_ptr(), page_map.data_ptr(), work.data_ptr(), B, max_pages, num_pages, page,
                  layers, row), "attn_cache_compact")

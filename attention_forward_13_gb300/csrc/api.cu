@@ -150,7 +150,8 @@ void resolve_window(const attn_opts* opts, int* wl, int* wr) {
 // First tokens that stay visible left of the window; without a left bound
 // every earlier key is visible anyway.
 int resolve_keep(const attn_opts* opts) {
-  return (opts != nullptr && opts->use_window && opts->window_left >= 0) ? opts->sink_tokens : 0;
+  if (opts == nullptr || !opts->use_window || opts->window_left < 0) return 0;
+  return std::min(opts->sink_tokens, 1 << 30);  // (more than any sequence holds; the kernels round it up)
 }
 
 // Rows of the first tokens in the band's first tile (PrefillKeepParams), 0 where

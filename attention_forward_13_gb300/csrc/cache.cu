@@ -123,22 +123,23 @@ __global__ void __launch_bounds__(512) reorder_kernel(const ReorderParams p) {
 }
 
 // ---------------------------------------------------------------------------
-// Block-wide exclusive sum of v; total in `all`.  scratch: 33 ints.
-__device__ __forceinline__ int block_scan(int v, int* scratch, int& all) {
+// Block-wide exclusive sum of v; total in `all`.  scratch: 32 values.
+template <class T>
+__device__ __forceinline__ T block_scan(T v, T* scratch, T& all) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  int inc = v;
+  T inc = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, inc, o);
+    const T y = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += y;
   }
   __syncthreads();
   if (lane == 31) scratch[warp] = inc;
   __syncthreads();
-  int pre = 0;
+  T pre = 0;
   all = 0;
   for (int i = 0; i < warps; ++i) {
-    const int x = scratch[i];
+    const T x = scratch[i];
     pre += i < warp ? x : 0;
     all += x;
   }
@@ -152,7 +153,7 @@ __device__ __forceinline__ void load8(const int32_t* refs, int p, int n, int (&v
 }
 
 // ---------------------------------------------------------------------------
-// Reserve: one CTA plans, a second kernel copies the shared last pages.
+// Reserve: a plan, then a second kernel copies the shared last pages.
 struct ReserveParams {
   const int32_t *table, *seqlens, *refs, *add;
   int32_t *table_out, *seqlens_out, *refs_out, *free_out;
@@ -163,13 +164,16 @@ struct ReserveParams {
 // Sequences are taken in order.  One that grows out of a partly filled last
 // page with other holders left copies it (the first `refs - 1` growers of a
 // page do, the last holder keeps it).  New pages are the free pages in rising
-// order, dealt to the sequences in order.  All or nothing.
+// order, dealt to the sequences in order.  All or nothing.  Every CTA works the
+// plan out (it is short), CTA 0 deals the pages and writes the counts, and all
+// share the rows of the table (one CTA alone writes a 2 MB table in 50 us).
 __global__ void __launch_bounds__(1024) reserve_plan_kernel(const ReserveParams p) {
   extern __shared__ int sh[];
   int* last = sh;              // [B] page that the sequence would share, or -1
   int* start = sh + p.B;       // [B] first new page's number; then one past the end
   int* first = sh + 2 * p.B + 1;  // [B] first new column
-  __shared__ int scratch[33];
+  __shared__ int scratch[32];
+  __shared__ long long wide[32];
   const int tid = threadIdx.x, n_thr = blockDim.x;
   pdl_launch_dependents();
   pdl_wait();
@@ -187,11 +191,12 @@ __global__ void __launch_bounds__(1024) reserve_plan_kernel(const ReserveParams 
     last[b] = page;
   }
   __syncthreads();
-  int total = 0;
+  long long total = 0;  // (thousands of long rows pass 32 bits; no pool holds them, but the answer says so)
   bool bad = false;  // a sequence outgrows its row of the table: nothing is reserved
   for (int b0 = 0; b0 < p.B; b0 += n_thr) {
     const int b = b0 + tid;
-    int need = 0, col = 0;
+    long long need = 0;
+    int col = 0;
     if (b < p.B) {
       const int len = max(p.seqlens[b], 0), add = max(p.add[b], 0);
       const int has = held_pages(len, p.page_log2, p.max_pages);
@@ -205,20 +210,19 @@ __global__ void __launch_bounds__(1024) reserve_plan_kernel(const ReserveParams 
       if (p.add[b] < 0) report(p.err);
       col = has - copied;
       if (want > p.max_pages) bad = true;
-      need = want > p.max_pages ? 0 : static_cast<int>(want) - col;
-      if (need < 0) need = 0;
+      need = want > p.max_pages || want < col ? 0 : want - col;
     }
-    int all;
-    const int pre = block_scan(need, scratch, all);
+    long long all;
+    const long long pre = block_scan(need, wide, all);
     if (b < p.B) {
-      start[b] = total + pre;
+      start[b] = static_cast<int>(total + pre);  // (read only where the total fits the pool)
       first[b] = col;
     }
     total += all;
   }
-  if (tid == 0) start[p.B] = total;
+  if (tid == 0) start[p.B] = static_cast<int>(total);
   bad = __syncthreads_or(bad);
-  if (bad && tid == 0) report(p.err);
+  if (bad && tid == 0 && blockIdx.x == 0) report(p.err);
   // Free pages there are.
   int free_pages = 0;
   for (int p0 = 0; p0 < p.num_pages; p0 += n_thr * 8) {
@@ -234,10 +238,13 @@ __global__ void __launch_bounds__(1024) reserve_plan_kernel(const ReserveParams 
     free_pages = all;
   }
   const bool fits = !bad && total <= free_pages;
-  if (tid == 0) *p.free_out = bad ? -p.num_pages - 1 : free_pages - total;
+  if (tid == 0 && blockIdx.x == 0) {
+    const long long left = free_pages - total;
+    *p.free_out = bad ? -p.num_pages - 1 : static_cast<int>(left > -0x7fffffffLL ? left : -0x7fffffffLL);
+  }
   // Tables as they were, without the columns that get new pages.
   const int warp = tid >> 5, lane = tid & 31, warps = n_thr >> 5;
-  for (int b = warp; b < p.B; b += warps) {
+  for (int b = blockIdx.x * warps + warp; b < p.B; b += gridDim.x * warps) {
     const int len = max(p.seqlens[b], 0);
     const int has = held_pages(len, p.page_log2, p.max_pages);
     const int keep = fits ? min(has, first[b]) : has;
@@ -248,6 +255,7 @@ __global__ void __launch_bounds__(1024) reserve_plan_kernel(const ReserveParams 
             j < keep ? p.table[static_cast<int64_t>(b) * p.max_pages + j] : -1;
     if (lane == 0) p.seqlens_out[b] = len + (fits ? max(p.add[b], 0) : 0);
   }
+  if (blockIdx.x > 0) return;
   // Deal the free pages out and write the counts.
   int rank0 = 0;
   for (int p0 = 0; p0 < p.num_pages; p0 += n_thr * 8) {
@@ -486,7 +494,7 @@ struct CompactParams {
 };
 
 __global__ void __launch_bounds__(1024) compact_plan_kernel(const CompactParams p) {
-  __shared__ int scratch[33];
+  __shared__ int scratch[32];
   const int tid = threadIdx.x, n_thr = blockDim.x;
   pdl_launch_dependents();
   pdl_wait();
@@ -586,15 +594,20 @@ int log2_of(int s) {
   return l;
 }
 
-attn_status check_cache(int B, int max_pages, int num_pages, int page_size, std::initializer_list<const void*> ints) {
+// Sizes, and the tables that must be there: `ints` always, `rows` where there are
+// sequences.
+attn_status check_cache(int B, int max_pages, int num_pages, int page_size, std::initializer_list<const void*> ints,
+                        std::initializer_list<const void*> rows) {
   if (B < 0 || max_pages <= 0 || num_pages <= 0) return ATTN_ERR_INVALID;
   if (!page_size_ok(page_size) || B > kMaxSeqs) return ATTN_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(num_pages) * page_size > 0x7fffffffLL ||
       static_cast<int64_t>(max_pages) * page_size > 0x7fffffffLL)
     return ATTN_ERR_UNSUPPORTED;
-  if (B == 0) return ATTN_OK;
   for (const void* p : ints)
     if (p == nullptr || !host_aligned(p, 4)) return ATTN_ERR_INVALID;
+  if (B > 0)
+    for (const void* p : rows)
+      if (p == nullptr || !host_aligned(p, 4)) return ATTN_ERR_INVALID;
   return ATTN_OK;
 }
 
@@ -618,6 +631,11 @@ int chunks_of(const PoolParams& q) { return static_cast<int>((q.page_bytes + kCh
 
 // CTAs that count references: one per 1024 pages.
 int ref_ctas(int num_pages) { return std::min(kMaxCtas, (num_pages + 1023) / 1024); }
+// The same where they also write a table: at least one per 32768 entries.
+int table_ctas(int B, int max_pages, int least) {
+  const int64_t n = (static_cast<int64_t>(B) * max_pages + 32767) / 32768;
+  return static_cast<int>(std::max<int64_t>(least, std::min<int64_t>(n, kMaxCtas)));
+}
 
 template <class... P, class... A>
 cudaError_t launch(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
@@ -638,19 +656,14 @@ attn_status attn_cache_reorder(const int32_t* block_table, const int32_t* seqlen
                                int32_t* refs_out, int B_in, int B_out, int max_pages, int num_pages,
                                int page_size, void* stream) {
   if (B_in < 0 || B_out < 0) return ATTN_ERR_INVALID;
-  attn_status st = check_cache(std::max(B_in, B_out), max_pages, num_pages, page_size,
-                               {page_refs, refs_out});
+  attn_status st = check_cache(B_in, max_pages, num_pages, page_size, {page_refs, refs_out}, {block_table, seqlens});
+  if (st == ATTN_OK) st = check_cache(B_out, max_pages, num_pages, page_size, {}, {index, table_out, seqlens_out});
   if (st != ATTN_OK) return st;
-  if (B_in == 0 && B_out == 0) return ATTN_OK;
-  if (B_in > 0) st = check_cache(B_in, max_pages, num_pages, page_size, {block_table, seqlens});
-  if (st == ATTN_OK && B_out > 0)
-    st = check_cache(B_out, max_pages, num_pages, page_size, {index, table_out, seqlens_out});
-  if (st != ATTN_OK) return st;
-  if (table_out == block_table || (seqlens_out == seqlens && seqlens != nullptr)) return ATTN_ERR_INVALID;
+  if (B_in > 0 && B_out > 0 && (table_out == block_table || seqlens_out == seqlens)) return ATTN_ERR_INVALID;
   ReorderParams p{block_table, seqlens, page_refs, index, table_out, seqlens_out, refs_out,
                   B_in, B_out, max_pages, num_pages, log2_of(page_size), nullptr};
   if (host_device_state(&p.err, nullptr) != ATTN_OK) return ATTN_ERR_CUDA;
-  return host_finish(launch(reorder_kernel, dim3(ref_ctas(num_pages)), 512, (kRange + (size_t)B_in) * 4,
+  return host_finish(launch(reorder_kernel, dim3(table_ctas(B_out, max_pages, ref_ctas(num_pages))), 512, (kRange + (size_t)B_in) * 4,
                             static_cast<cudaStream_t>(stream), p),
                      "attn_cache_reorder");
 }
@@ -661,20 +674,21 @@ attn_status attn_cache_reserve(void* k_pool, void* v_pool, const int32_t* block_
                                int max_pages, int num_pages, int page_size, int layers, int64_t row_bytes,
                                void* stream) {
   attn_status st = check_cache(B, max_pages, num_pages, page_size,
-                               {block_table, seqlens, page_refs, add, table_out, seqlens_out, refs_out, free_out});
+                               {page_refs, refs_out, free_out},
+                               {block_table, seqlens, add, table_out, seqlens_out});
   if (st != ATTN_OK) return st;
-  if (B == 0) return ATTN_OK;
   st = check_pool(k_pool, v_pool, layers, row_bytes);
   if (st != ATTN_OK) return st;
-  if (table_out == block_table || seqlens_out == seqlens || refs_out == page_refs) return ATTN_ERR_INVALID;
+  if ((B > 0 && (table_out == block_table || seqlens_out == seqlens)) || refs_out == page_refs)
+    return ATTN_ERR_INVALID;
   ReserveParams p{block_table, seqlens, page_refs, add, table_out, seqlens_out, refs_out, free_out,
                   B, max_pages, num_pages, log2_of(page_size), nullptr};
   int sms = 0;
   if (host_device_state(&p.err, &sms) != ATTN_OK) return ATTN_ERR_CUDA;
   const PoolParams q = pool_params(k_pool, v_pool, layers, row_bytes, page_size, num_pages);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch(reserve_plan_kernel, dim3(1), 1024, (3 * (size_t)B + 1) * 4, s, p);
-  if (e == cudaSuccess) {
+  cudaError_t e = launch(reserve_plan_kernel, dim3(table_ctas(B, max_pages, 1)), 1024, (3 * (size_t)B + 1) * 4, s, p);
+  if (e == cudaSuccess && B > 0) {
     const int chunks = chunks_of(q);
     const int64_t tasks = static_cast<int64_t>(B) * chunks * 2 * layers;
     const int grid = static_cast<int>(std::min<int64_t>(tasks, 8 * static_cast<int64_t>(sms)));
@@ -690,13 +704,12 @@ attn_status attn_cache_accept(void* k_pool, void* v_pool, const int32_t* block_t
                               int64_t row_bytes, void* stream) {
   if (A < 0 || T < 0) return ATTN_ERR_INVALID;
   attn_status st = check_cache(B, max_pages, num_pages, page_size,
-                               {block_table, seqlens, page_refs, path_lens, seqlens_out, refs_out});
+                               {page_refs, refs_out}, {block_table, seqlens, path_lens, seqlens_out});
   if (st != ATTN_OK) return st;
-  if (B == 0) return ATTN_OK;
   st = check_pool(k_pool, v_pool, layers, row_bytes);
   if (st != ATTN_OK) return st;
-  if ((A > 0 && (path == nullptr || !host_aligned(path, 4))) || !host_aligned(tree_lens, 4) ||
-      seqlens_out == seqlens)
+  if ((A > 0 && B > 0 && (path == nullptr || !host_aligned(path, 4))) || !host_aligned(tree_lens, 4) ||
+      (B > 0 && seqlens_out == seqlens))
     return ATTN_ERR_INVALID;
   AcceptParams p{block_table, seqlens, page_refs, path, path_lens, tree_lens, seqlens_out, refs_out, B, A, T,
                  max_pages, num_pages, log2_of(page_size), ref_ctas(num_pages),
@@ -715,12 +728,11 @@ attn_status attn_cache_compact(void* k_pool, void* v_pool, const int32_t* block_
                                int32_t* page_map, int32_t* workspace, int B, int max_pages, int num_pages,
                                int page_size, int layers, int64_t row_bytes, void* stream) {
   attn_status st = check_cache(B, max_pages, num_pages, page_size,
-                               {block_table, seqlens, page_refs, table_out, refs_out, page_map, workspace});
+                               {page_refs, refs_out, page_map, workspace}, {block_table, seqlens, table_out});
   if (st != ATTN_OK) return st;
-  if (B == 0) return ATTN_OK;
   st = check_pool(k_pool, v_pool, layers, row_bytes);
   if (st != ATTN_OK) return st;
-  if (table_out == block_table || refs_out == page_refs) return ATTN_ERR_INVALID;
+  if ((B > 0 && table_out == block_table) || refs_out == page_refs) return ATTN_ERR_INVALID;
   CompactParams p{block_table, seqlens, page_refs, table_out, refs_out, page_map, workspace,
                   B, max_pages, num_pages, log2_of(page_size), nullptr};
   int sms = 0;

@@ -216,6 +216,7 @@ __device__ inline bool tree_unit_mode(const TreeParams& p, const TreeLine& line,
   if ((threadIdx.x & 31) == 0) scratch[warp] = hand;
   __syncthreads();
   for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) hand = max(hand, scratch[i]);
+  fence_proxy_async_smem();  // `cost` lies where the first copies will land
   __syncthreads();
   return always || hand <= line.q + line.q / 16 + 2 * p.unit_cost + 8;
 }

@@ -343,7 +343,9 @@ attn_status attn_dense_schedule(int B, int Hq, int Hkv, int Lq, int Lk, const at
  * (any element type and head dimension).  page_size as for attn_fwd_paged;
  * B <= 8192.  An index out of range never faults: the entry is left out, and
  * the device error word's bit for bad cache indices is set.  All are
- * deterministic, need no setting of anything beforehand and can be captured.
+ * deterministic and need no setting of anything beforehand.  They can be
+ * captured into a graph, after a first call of the kind (which loads kernels).
+ * With B = 0 what concerns the pool alone (page_refs, moves, page_map) is done.
  *
  * attn_cache_reorder -- new sequence b is old sequence index[b] (int32 [B_out];
  * -1: an empty one).  Forks where an index repeats (the pages are shared),

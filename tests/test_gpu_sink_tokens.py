@@ -85,6 +85,20 @@ def test_dense_strides_alibi_and_bias():
 
 
 @gpu
+def test_more_first_tokens_than_any_cache_holds():
+    inp = inputs.paged([700, 90], 1, 8, 2, 64, 16, 60, seed=3)
+    args = [cuda(x) for x in (inp.q, inp.k_pool, inp.v_pool, inp.block_table, inp.seqlens_k)]
+    a = A.attn_fwd_paged(*args, causal=True, window=(5, -1), sink_tokens=0x7fffffff)
+    ro, rl = _paged_ref(inp, 5, 10 ** 6, 0.0, 64)
+    check(*a, ro, rl, "all")
+    q = cuda(inputs.dense(1, 2, 2, 300, 300, 64, "bf16", seed=1).q)
+    b = A.attn_fwd(q, q, q, causal=True, window=(5, -1), sink_tokens=0x7fffffff)
+    ro, rl = _dense_ref(q.cpu(), q.cpu(), q.cpu(), M.band(300, 300, -1, 0), 1 / 8)
+    check(*b, ro, rl, "dense")
+    no_device_error()
+
+
+@gpu
 def test_fp8():
     inp = inputs.dense(1, 2, 2, 600, 600, 128, "e4m3", seed=21)
     o, lse = A.attn_fwd(cuda(inp.q), cuda(inp.k), cuda(inp.v), causal=True, window=(90, -1), sink_tokens=4)

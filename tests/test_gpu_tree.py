@@ -159,6 +159,75 @@ def test_parity(case):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@gpu
+def test_streams_strided_views_and_a_shared_workspace():
+    """Two streams with a workspace each; a workspace kept from call to call; outputs given;
+    the masks of one tree shape read by sequences of other lengths."""
+    case = ([1500, 40, 333], 33, 8, 2, 128, 64, "bf16", False, 0.0, False, -1, 0)
+    inp, nodes, parents, sees, depth = build(case)
+    ro, rl = reference(inp, sees, depth, nodes, 1 / math.sqrt(128))
+    args = [cuda(x) for x in (inp.q, inp.k_pool, inp.v_pool, inp.block_table, inp.seqlens_k)]
+    mask, dep = A.attn_tree_mask(cuda(parents))
+    need = A.attn_tree_workspace_bytes(33, 8, 2, 128)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [torch.full((need,), 255, dtype=torch.uint8, device="cuda") for _ in streams]  # NaN patterns
+    torch.cuda.synchronize()
+    outs = []
+    for i in range(8):
+        s = streams[i % 2]
+        kw = dict(workspace=spaces[i % 2]) if i < 4 else {}
+        outs.append(A.attn_fwd_paged_tree(*args, mask, stream=s, **kw))
+    torch.cuda.synchronize()
+    no_device_error()
+    check(*outs[0], ro, rl, "stream")
+    for o, lse in outs[1:]:
+        assert torch.equal(o, outs[0][0]) and torch.equal(lse, outs[0][1])
+    o, lse = torch.empty_like(args[0]), torch.empty_like(outs[0][1])
+    A.attn_fwd_paged_tree(*args, mask, o=o, lse=lse)
+    assert torch.equal(o, outs[0][0]) and torch.equal(lse, outs[0][1])
+    o, none = A.attn_fwd_paged_tree(*args, mask, lse=False)
+    assert none is None and torch.equal(o, outs[0][0])
+    no_device_error()
+
+
+@gpu
+def test_many_units_are_dealt_whole():
+    """Units enough per SM for whole ones to be dealt (and far too many of them): the same
+    answer as the definition, every row written."""
+    for B, Hkv, T, most in ((60, 8, 5, 400), (250, 2, 3, 300), (40, 16, 70, 260)):
+        rng = np.random.default_rng(B)
+        case = ([int(x) for x in rng.integers(0, most, B)], T, 2 * Hkv, Hkv, 64, 32, "f16", True, 0.0, False, -1, 0)
+        inp, nodes, parents, sees, depth = build(case)
+        ro, rl = reference(inp, sees, depth, nodes, 1 / 8)
+        tl = cuda(torch.tensor(nodes, dtype=torch.int32))
+        mask, _ = A.attn_tree_mask(cuda(parents), tl)
+        o = torch.full_like(cuda(inp.q), float("nan"))
+        lse = torch.full((B, 2 * Hkv, T), float("nan"), device="cuda")
+        A.attn_fwd_paged_tree(cuda(inp.q), cuda(inp.k_pool), cuda(inp.v_pool), cuda(inp.block_table),
+                              cuda(inp.seqlens_k), mask, tree_lens=tl, o=o, lse=lse)
+        torch.cuda.synchronize()
+        no_device_error()
+        check(o, lse, ro, rl, f"B {B}")
+
+
+@gpu
+def test_bad_pages_are_reported_not_followed():
+    case = ([300, 64], 4, 8, 2, 64, 64, "bf16", False, 0.0, False, -1, 0)
+    inp, nodes, parents, sees, depth = build(case)
+    bt = cuda(inp.block_table)
+    bt[0, 2], bt[1, 0] = -7, 1 << 30
+    mask, _ = A.attn_tree_mask(cuda(parents))
+    o, lse = A.attn_fwd_paged_tree(cuda(inp.q), cuda(inp.k_pool), cuda(inp.v_pool), bt, cuda(inp.seqlens_k), mask)
+    assert A.attn_device_error() == 1 << 22 and torch.isfinite(o.float()).all()
+    sl = cuda(inp.seqlens_k).clone()
+    sl[0], sl[1] = 1 << 30, -5  # lengths past the table, and below zero
+    bt = cuda(inp.block_table)
+    o, lse = A.attn_fwd_paged_tree(cuda(inp.q), cuda(inp.k_pool), cuda(inp.v_pool), bt, sl, mask)
+    torch.cuda.synchronize()
+    A.attn_device_error()
+    assert not o[1].any() and torch.isneginf(lse[1]).all()
+
+
 def test_refusals_before_a_launch():
     """Host-side checks of the tree entry points (no GPU needed)."""
     lib = A.library()
