@@ -934,51 +934,46 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
 #pragma unroll 1
         for (int c = pair ? 0 : t * (D / 2); c < (pair ? D : (t + 1) * (D / 2)); c += 32) put(c, v);
       } else if (pair) {
+        // 32 columns at a time: with all of O in registers the row pointers spill
+        // (16 sequences, 64 nodes, 4096 keys: 78.5 against 80.3 us).
         if (mine) {
-          uint32_t ov[D];
-#pragma unroll
-          for (int c = 0; c < D; c += 32)
-            tmem_ld32(tmem + C::tm_o(t) + lane_base + c, *reinterpret_cast<uint32_t(*)[32]>(&ov[c]));
-          tmem_ld_wait();
-          reg_fence(ov);
-          tc_fence_before();
-          mbar_arrive(&sm.o_free[t]);
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D; c += 32) {
+            uint32_t ov[32];
+            tmem_ld32(tmem + C::tm_o(t) + lane_base + c, ov);
+            tmem_ld_wait();
+            reg_fence(ov);
             float v[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = zero ? 0.0f : __uint_as_float(ov[c + i]) * scale0;
+            for (int i = 0; i < 32; ++i) v[i] = zero ? 0.0f : __uint_as_float(ov[i]) * scale0;
             put(c, v);
           }
-        } else {
-          mbar_arrive(&sm.o_free[t]);
         }
+        tc_fence_before();
+        mbar_arrive(&sm.o_free[t]);
         ++seg;
       } else {
         // Half the columns of both streams' accumulators.
-        const int c0 = t * (D / 2);
         const bool one = n == 1;  // the second stream had no tile
-        uint32_t ov[D];
-#pragma unroll
-        for (int c = 0; c < D / 2; c += 32) {
-          tmem_ld32(tmem + C::tm_o(0) + lane_base + c0 + c, *reinterpret_cast<uint32_t(*)[32]>(&ov[c]));
-          tmem_ld32(tmem + C::tm_o(1) + lane_base + c0 + c, *reinterpret_cast<uint32_t(*)[32]>(&ov[D / 2 + c]));
-        }
-        tmem_ld_wait();
-        reg_fence(ov);
-        tc_fence_before();
-        mbar_arrive(&sm.o_free[0]);
-        mbar_arrive(&sm.o_free[1]);
-#pragma unroll
-        for (int c = 0; c < D / 2; c += 32) {
+#pragma unroll 1
+        for (int c = t * (D / 2); c < (t + 1) * (D / 2); c += 32) {
+          uint32_t o0[32], o1[32];
+          tmem_ld32(tmem + C::tm_o(0) + lane_base + c, o0);
+          tmem_ld32(tmem + C::tm_o(1) + lane_base + c, o1);
+          tmem_ld_wait();
+          reg_fence(o0);
+          reg_fence(o1);
           float v[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const float x = __uint_as_float(ov[c + i]) * scale0;
-            v[i] = zero ? 0.0f : one ? x : fmaf(__uint_as_float(ov[D / 2 + c + i]), scale1, x);
+            const float x = __uint_as_float(o0[i]) * scale0;
+            v[i] = zero ? 0.0f : one ? x : fmaf(__uint_as_float(o1[i]), scale1, x);
           }
-          put(c0 + c, v);
+          put(c, v);
         }
+        tc_fence_before();
+        mbar_arrive(&sm.o_free[0]);
+        mbar_arrive(&sm.o_free[1]);
         ++seg;
       }
       if (row_in && (pair ? mine || n == 0 : t == 0)) {

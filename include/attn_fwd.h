@@ -177,6 +177,9 @@ attn_status attn_fwd_varlen(const void* q, const void* k, const void* v, void* o
  *   [k_lo, k_hi) of the sequence, and W = attn_paged_window_pages(); with
  *   sink_tokens the splits tile the sequence's visible pages in order, the
  *   ceil(sink_tokens / page_size) first ones and then f_b .. e_b - 1.
+ *   With sink_tokens num_splits = 0 takes attn_paged_keep_splits, and one
+ *   split (chosen or given) runs the tree attention's kernel where the
+ *   sequences are enough to fill the GPU.
  *   When num_splits > 1, o_partial (fp32 [num_splits][B][Hq][Lq][d]) and
  *   lse_partial (fp32 [num_splits][B][Hq][Lq]) are caller-owned scratch of
  *   attn_paged_workspace_bytes() bytes in total, and attn_splitkv_combine is
