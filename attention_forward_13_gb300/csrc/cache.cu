@@ -153,7 +153,48 @@ __device__ __forceinline__ void load8(const int32_t* refs, int p, int n, int (&v
 }
 
 // ---------------------------------------------------------------------------
-// Reserve: a plan, then a second kernel copies the shared last pages.
+// Page copies.  A pool is [layers][num_pages][page bytes].
+struct PoolParams {
+  uint8_t *k, *v;
+  int64_t page_bytes, layer_bytes;
+  int layers;
+};
+
+// Bytes [off, off + n) of page src to page dst of one pool and layer; n a
+// multiple of 16, by a group of kCopiers threads.  Eight 16-byte loads per thread
+// go out before the first store.
+constexpr int kCopiers = 128;
+__device__ __forceinline__ void copy_chunk(const uint8_t* src, uint8_t* dst, int n) {
+  constexpr int U = 8;
+  const int tid = threadIdx.x & (kCopiers - 1);
+  for (int i0 = 0; i0 < n; i0 += kCopiers * 16 * U) {
+    uint4 x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + (u * kCopiers + tid) * 16;
+      if (i < n) x[u] = __ldcs(reinterpret_cast<const uint4*>(src + i));
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + (u * kCopiers + tid) * 16;
+      if (i < n) __stcs(reinterpret_cast<uint4*>(dst + i), x[u]);
+    }
+  }
+}
+
+// Task t of the copies of one page pair: layer, pool and chunk.
+__device__ __forceinline__ void copy_task(const PoolParams& q, int src, int dst, int t, int chunks) {
+  const int chunk = t % chunks, lk = t / chunks;
+  uint8_t* pool = (lk & 1) ? q.v : q.k;
+  const int64_t base = (lk >> 1) * q.layer_bytes + static_cast<int64_t>(chunk) * kChunk;
+  const int n = static_cast<int>(q.page_bytes - static_cast<int64_t>(chunk) * kChunk < kChunk
+                                     ? q.page_bytes - static_cast<int64_t>(chunk) * kChunk
+                                     : kChunk);
+  copy_chunk(pool + base + src * q.page_bytes, pool + base + dst * q.page_bytes, n);
+}
+
+// ---------------------------------------------------------------------------
+// Reserve.
 struct ReserveParams {
   const int32_t *table, *seqlens, *refs, *add;
   int32_t *table_out, *seqlens_out, *refs_out, *free_out;
@@ -165,13 +206,18 @@ struct ReserveParams {
 // page with other holders left copies it (the first `refs - 1` growers of a
 // page do, the last holder keeps it).  New pages are the free pages in rising
 // order, dealt to the sequences in order.  All or nothing.  Every CTA works the
-// plan out (it is short), CTA 0 deals the pages and writes the counts, and all
-// share the rows of the table (one CTA alone writes a 2 MB table in 50 us).
-__global__ void __launch_bounds__(1024) reserve_plan_kernel(const ReserveParams p) {
+// plan out for itself, which is short; a second kernel for the copies would have
+// to wait for the first (64 beams, 16 layers: 47.9 us with two kernels, 45.1 with
+// one; four beams 15.4 and 13.3).  CTA 0 writes the new pages and the counts, and
+// all share the rows of the table (one CTA alone writes a 2 MB table in 50 us)
+// and the copies: eight groups of 128 threads a CTA, 16 KB a task.
+__global__ void __launch_bounds__(1024, 1) reserve_kernel(const ReserveParams p, const PoolParams q, int chunks) {
   extern __shared__ int sh[];
   int* last = sh;              // [B] page that the sequence would share, or -1
   int* start = sh + p.B;       // [B] first new page's number; then one past the end
   int* first = sh + 2 * p.B + 1;  // [B] first new column
+  int* fresh = sh + 3 * p.B + 1;  // [B] first new page
+  int* copiers = sh + 4 * p.B + 1;  // [B] the sequences that copy, in order
   __shared__ int scratch[32];
   __shared__ long long wide[32];
   const int tid = threadIdx.x, n_thr = blockDim.x;
@@ -192,16 +238,16 @@ __global__ void __launch_bounds__(1024) reserve_plan_kernel(const ReserveParams 
   }
   __syncthreads();
   long long total = 0;  // (thousands of long rows pass 32 bits; no pool holds them, but the answer says so)
+  int copying = 0;   // sequences that copy
   bool bad = false;  // a sequence outgrows its row of the table: nothing is reserved
   for (int b0 = 0; b0 < p.B; b0 += n_thr) {
     const int b = b0 + tid;
     long long need = 0;
-    int col = 0;
+    int col = 0, copied = 0;
     if (b < p.B) {
       const int len = max(p.seqlens[b], 0), add = max(p.add[b], 0);
       const int has = held_pages(len, p.page_log2, p.max_pages);
       const int64_t want = (static_cast<int64_t>(len) + add + (1 << p.page_log2) - 1) >> p.page_log2;
-      int copied = 0;
       if (last[b] >= 0) {
         int before = 0;
         for (int i = 0; i < b; ++i) before += last[i] == last[b];
@@ -219,6 +265,12 @@ __global__ void __launch_bounds__(1024) reserve_plan_kernel(const ReserveParams 
       first[b] = col;
     }
     total += all;
+    if (__syncthreads_or(copied)) {
+      int n;
+      const int k = copying + block_scan(copied, scratch, n);
+      if (copied) copiers[k] = b;
+      copying += n;
+    }
   }
   if (tid == 0) start[p.B] = static_cast<int>(total);
   bad = __syncthreads_or(bad);
@@ -255,7 +307,8 @@ __global__ void __launch_bounds__(1024) reserve_plan_kernel(const ReserveParams 
             j < keep ? p.table[static_cast<int64_t>(b) * p.max_pages + j] : -1;
     if (lane == 0) p.seqlens_out[b] = len + (fits ? max(p.add[b], 0) : 0);
   }
-  if (blockIdx.x > 0) return;
+  const bool writer = blockIdx.x == 0;
+  if (!writer && !(fits && copying > 0)) return;
   // Deal the free pages out and write the counts.
   int rank0 = 0;
   for (int p0 = 0; p0 < p.num_pages; p0 += n_thr * 8) {
@@ -279,89 +332,27 @@ __global__ void __launch_bounds__(1024) reserve_plan_kernel(const ReserveParams 
             if (start[mid] <= k) lo = mid;
             else hi = mid - 1;
           }
-          p.table_out[static_cast<int64_t>(lo) * p.max_pages + first[lo] + (k - start[lo])] = q0 + i;
+          if (k == start[lo]) fresh[lo] = q0 + i;
+          if (writer)
+            p.table_out[static_cast<int64_t>(lo) * p.max_pages + first[lo] + (k - start[lo])] = q0 + i;
           refs = 1;
         }
         ++k;
       }
-      p.refs_out[q0 + i] = refs;
+      if (writer) p.refs_out[q0 + i] = refs;
     }
   }
   __syncthreads();
-  if (fits)  // the copied pages have one holder less
-    for (int b = tid; b < p.B; b += n_thr)
-      if (last[b] >= 0 && first[b] < held_pages(max(p.seqlens[b], 0), p.page_log2, p.max_pages))
-        atomicSub(&p.refs_out[last[b]], 1);
-}
-
-// ---------------------------------------------------------------------------
-// Page copies.  A pool is [layers][num_pages][page bytes].
-struct PoolParams {
-  uint8_t *k, *v;
-  int64_t page_bytes, layer_bytes;
-  int layers;
-};
-
-// Bytes [off, off + n) of page src to page dst of one pool and layer; n a
-// multiple of 16.  Eight 16-byte loads per thread go out before the first store.
-__device__ __forceinline__ void copy_chunk(const uint8_t* src, uint8_t* dst, int n) {
-  constexpr int U = 8;
-  for (int i0 = 0; i0 < n; i0 += blockDim.x * 16 * U) {
-    uint4 x[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + (u * blockDim.x + threadIdx.x) * 16;
-      if (i < n) x[u] = __ldcs(reinterpret_cast<const uint4*>(src + i));
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + (u * blockDim.x + threadIdx.x) * 16;
-      if (i < n) __stcs(reinterpret_cast<uint4*>(dst + i), x[u]);
-    }
-  }
-}
-
-// Task t of the copies of one page pair: layer, pool and chunk.
-__device__ __forceinline__ void copy_task(const PoolParams& q, int src, int dst, int t, int chunks) {
-  const int chunk = t % chunks, lk = t / chunks;
-  uint8_t* pool = (lk & 1) ? q.v : q.k;
-  const int64_t base = (lk >> 1) * q.layer_bytes + static_cast<int64_t>(chunk) * kChunk;
-  const int n = static_cast<int>(q.page_bytes - static_cast<int64_t>(chunk) * kChunk < kChunk
-                                     ? q.page_bytes - static_cast<int64_t>(chunk) * kChunk
-                                     : kChunk);
-  copy_chunk(pool + base + src * q.page_bytes, pool + base + dst * q.page_bytes, n);
-}
-
-// Copies of reserve: where a sequence's last page changed between the tables.
-// Held to eight CTAs per SM (64 registers): 49.8 -> 47.5 us for 64 beams.  The
-// kernel that moves pages loses by the same bound (95 -> 102 us, 4096 pages: its
-// chunk no longer stays in registers).
-__global__ void __launch_bounds__(128, 8) reserve_copy_kernel(const ReserveParams p, const PoolParams q, int chunks) {
-  extern __shared__ int sh[];  // [B] sequences that copy
-  __shared__ int count;
-  if (threadIdx.x == 0) count = 0;
-  pdl_launch_dependents();
-  pdl_wait();
-  __syncthreads();
-  for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
-    const int has = held_pages(max(p.seqlens[b], 0), p.page_log2, p.max_pages);
-    if (has == 0 || p.seqlens_out[b] == p.seqlens[b]) continue;
-    const int64_t at = static_cast<int64_t>(b) * p.max_pages + has - 1;
-    const int src = p.table[at], dst = p.table_out[at];
-    if (src != dst && src >= 0 && src < p.num_pages && dst >= 0 && dst < p.num_pages)
-      sh[atomicAdd(&count, 1)] = b;  // (any order: the copies are independent)
-  }
-  __syncthreads();
-  const int per = chunks * 2 * q.layers;
-  for (int i = 0; i < count; ++i) {
-    const int b = sh[i];
-    const int has = held_pages(p.seqlens[b], p.page_log2, p.max_pages);
-    const int64_t at = static_cast<int64_t>(b) * p.max_pages + has - 1;
-    const int src = p.table[at], dst = p.table_out[at];
-    // Task t of sequence b belongs to CTA (b * per + t) mod grid.
-    const uint32_t r = static_cast<uint32_t>(b) * (static_cast<uint32_t>(per) % gridDim.x) % gridDim.x;
-    int t = static_cast<int>(blockIdx.x >= r ? blockIdx.x - r : blockIdx.x + gridDim.x - r);
-    for (; t < per; t += gridDim.x) copy_task(q, src, dst, t, chunks);
+  if (!fits) return;
+  if (writer)  // the copied pages have one holder less
+    for (int i = tid; i < copying; i += n_thr) atomicSub(&p.refs_out[last[copiers[i]]], 1);
+  const int per = chunks * 2 * q.layers, groups = n_thr / kCopiers;
+  const int64_t tasks = static_cast<int64_t>(copying) * per;
+  for (int64_t task = static_cast<int64_t>(tid / kCopiers) * gridDim.x + blockIdx.x; task < tasks;
+       task += static_cast<int64_t>(groups) * gridDim.x) {
+    const int64_t i = task / per;
+    const int b = copiers[i];
+    copy_task(q, last[b], fresh[b], static_cast<int>(task - i * per), chunks);
   }
 }
 
@@ -690,14 +681,11 @@ attn_status attn_cache_reserve(void* k_pool, void* v_pool, const int32_t* block_
   if (host_device_state(&p.err, &sms) != ATTN_OK) return ATTN_ERR_CUDA;
   const PoolParams q = pool_params(k_pool, v_pool, layers, row_bytes, page_size, num_pages);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch(reserve_plan_kernel, dim3(table_ctas(B, max_pages, 1)), 1024, (3 * (size_t)B + 1) * 4, s, p);
-  if (e == cudaSuccess && B > 0) {
-    const int chunks = chunks_of(q);
-    const int64_t tasks = static_cast<int64_t>(B) * chunks * 2 * layers;
-    const int grid = static_cast<int>(std::min<int64_t>(tasks, 8 * static_cast<int64_t>(sms)));
-    e = launch(reserve_copy_kernel, dim3(grid), 128, (size_t)B * 4, s, p, q, chunks);
-  }
-  return host_finish(e, "attn_cache_reserve_plan+attn_cache_reserve_copy");
+  const int chunks = chunks_of(q);
+  const int64_t tasks = static_cast<int64_t>(B) * chunks * 2 * layers;
+  const int grid = static_cast<int>(std::max<int64_t>(table_ctas(B, max_pages, 1), std::min<int64_t>(tasks, sms)));
+  return host_finish(launch(reserve_kernel, dim3(grid), 1024, (5 * (size_t)B + 1) * 4, s, p, q, chunks),
+                     "attn_cache_reserve");
 }
 
 attn_status attn_cache_accept(void* k_pool, void* v_pool, const int32_t* block_table, const int32_t* seqlens,
