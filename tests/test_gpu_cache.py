@@ -206,6 +206,38 @@ def test_compact(state):
 
 
 @gpu
+@pytest.mark.parametrize("B", [1025, 2600, 8192])  # past one block of threads; the most there may be
+def test_many_sequences(B):
+    rng = np.random.default_rng(B)
+    c = Cache(rng, [int(n) for n in rng.integers(0, 70, B)], 16, 2 * B, Hkv=1, d=8, dtype=torch.float16)
+    c.width += 2
+    pools, table, lens, refs = c.gpu()
+    index = [int(i) for i in rng.integers(-1, B, B)]  # (about a third share their pages)
+    table, lens, refs = A.attn_cache_reorder(table, lens, refs, i32(index), c.page)
+    rows, wl, wr = P.reorder(c.rows, c.lens, c.refs, index, c.page)
+    assert lens.tolist() == wl and refs.tolist() == wr
+    same_table(table, rows)
+    add = [int(n) for n in rng.integers(0, 9, B)]
+    host = c.np_pools()
+    rows, wl, wr, free = P.reserve(host, rows, wl, wr, add, c.page, c.width)
+    assert free >= 0
+    table, lens, refs, f = A.attn_cache_reserve(*pools, table, lens, refs, i32(add))
+    assert f.tolist() == [free] and lens.tolist() == wl and refs.tolist() == wr
+    same_table(table, rows)
+    for pool, want in zip(pools, host):
+        assert np.array_equal(raw(pool, want), want)
+    path = [sorted(rng.permutation(n)[:int(rng.integers(0, n + 1))].tolist()) for n in add]
+    width = max(len(x) for x in path)
+    wl, wr = P.accept(host, rows, wl, wr, path, add, c.page)
+    lens, refs = A.attn_cache_accept(*pools, table, lens, refs, i32([x + [0] * (width - len(x)) for x in path]),
+                                     i32([len(x) for x in path]), i32(add))
+    assert lens.tolist() == wl and refs.tolist() == wr
+    for pool, want in zip(pools, host):
+        assert np.array_equal(raw(pool, want), want)
+    no_device_error()
+
+
+@gpu
 def test_a_cache_without_sequences():
     """Pages that only something outside the table holds."""
     refs = i32([0, 2, 0, 0, 1, 1])
