@@ -211,6 +211,57 @@ def test_many_units_are_dealt_whole():
 
 
 @gpu
+@pytest.mark.parametrize("B", [257, 385, 900])  # past the order's 256, past a block's threads, past two
+def test_many_sequences(B):
+    rng = np.random.default_rng(B)
+    case = ([int(x) for x in rng.integers(0, 200, B)], 4, 2, 1, 64, 16, "f16", True, 0.0, False, -1, 0)
+    inp, nodes, parents, sees, depth = build(case)
+    ro, rl = reference(inp, sees, depth, nodes, 1 / 8)
+    tl = cuda(torch.tensor(nodes, dtype=torch.int32))
+    mask, _ = A.attn_tree_mask(cuda(parents), tl)
+    o, lse = A.attn_fwd_paged_tree(cuda(inp.q), cuda(inp.k_pool), cuda(inp.v_pool), cuda(inp.block_table),
+                                   cuda(inp.seqlens_k), mask, tree_lens=tl)
+    torch.cuda.synchronize()
+    no_device_error()
+    check(o, lse, ro, rl, f"B {B}")
+
+
+@gpu
+def test_pages_past_32_bits():
+    """The same sequences in a small pool and at the end of one of 40000 pages (2.6e9 elements,
+    5 GB each): the same bits, and the same after the pool has been closed up."""
+    page, Hkv, d, num, T = 64, 8, 128, 40000, 6
+    inp = inputs.paged([700, 65, 1300], T, 4 * Hkv, Hkv, d, page, 40, seed=3)
+    parents = cuda(torch.tensor([[-1, 0, 0, 1, 3, 2]] * 3, dtype=torch.int32))
+    mask, depth = A.attn_tree_mask(parents)
+    lens = cuda(inp.seqlens_k)
+
+    def run(kp, vp, table):
+        tree = A.attn_fwd_paged_tree(cuda(inp.q), kp, vp, table, lens, mask, tree_depth=depth)
+        win = A.attn_fwd_paged_tree(cuda(inp.q), kp, vp, table, lens, mask, tree_depth=depth, window=(200, -1),
+                                    sink_tokens=5)
+        one = A.attn_fwd_paged(cuda(inp.q[:, :1].contiguous()), kp, vp, table, lens, window=(200, -1), causal=True,
+                               sink_tokens=5)
+        chunk = A.attn_fwd_paged(cuda(inp.q), kp, vp, table, lens, window=(200, -1), causal=True, sink_tokens=5)
+        return tree + win + one + chunk
+
+    small = cuda(inp.k_pool), cuda(inp.v_pool)
+    want = run(*small, cuda(inp.block_table))
+    pools = [torch.empty(num, page, Hkv, d, dtype=inp.q.dtype, device="cuda") for _ in range(2)]
+    for big, x in zip(pools, small):
+        big[num - 40:] = x
+    table = cuda(inp.block_table) + (num - 40)
+    assert all(torch.equal(x, y) for x, y in zip(run(*pools, table), want))
+    refs = torch.zeros(num, dtype=torch.int32, device="cuda")
+    for row, n in zip(table.tolist(), inp.seqlens_k.tolist()):
+        refs[row[:-(-n // page)]] += 1
+    table, refs, _ = A.attn_cache_compact(*pools, table, lens, refs)
+    assert int(table.max()) < 40
+    assert all(torch.equal(x, y) for x, y in zip(run(*pools, table.clamp(min=0)), want))
+    no_device_error()
+
+
+@gpu
 def test_bad_pages_are_reported_not_followed():
     case = ([300, 64], 4, 8, 2, 64, 64, "bf16", False, 0.0, False, -1, 0)
     inp, nodes, parents, sees, depth = build(case)
