@@ -487,11 +487,59 @@ struct CompactParams {
   unsigned int* err;
 };
 
+constexpr int kOnePass = 8192;  // eight pages for each of 1024 threads
+
 __global__ void __launch_bounds__(1024) compact_plan_kernel(const CompactParams p) {
   __shared__ int scratch[32];
   const int tid = threadIdx.x, n_thr = blockDim.x;
   pdl_launch_dependents();
   pdl_wait();
+  if (p.num_pages <= kOnePass) {
+    // The counts fit the block's registers: one load and one scan.  With r(q)
+    // the live pages before page q, hole q below `live` is number q - r(q), and
+    // live page q above it moves as number r(q) - r(live).  There are as many
+    // holes as moves, so at most kOnePass / 2.  (Against the passes below, whose
+    // numbers go through global memory: a pool of 300 pages 10.3 -> 8.2 us, 4096
+    // pages 96.1 -> 94.4, both with the moves.)
+    __shared__ int hole[kOnePass / 2];
+    __shared__ int before_live;
+    const int q0 = tid * 8;
+    int v[8], c = 0;
+    load8(p.refs, q0, p.num_pages, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c += v[i] > 0;
+    int live;
+    const int rank = block_scan(c, scratch, live);
+    int r = rank;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (q0 + i == live) before_live = r;
+      if (q0 + i < live && v[i] <= 0) hole[q0 + i - r] = q0 + i;
+      r += v[i] > 0;
+    }
+    if (tid == 0 && live == kOnePass) before_live = live;  // (no thread has a page `live`)
+    __syncthreads();
+    const int base = before_live;
+    r = rank;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int q = q0 + i;
+      if (q >= p.num_pages) break;
+      int to = v[i] > 0 ? q : -1;
+      if (q >= live) {
+        p.refs_out[q] = 0;
+        if (v[i] > 0) {
+          to = hole[r - base];
+          p.moved[1 + r - base] = q;
+        }
+      }
+      if (to >= 0) p.refs_out[to] = v[i];
+      p.map[q] = to;
+      r += v[i] > 0;
+    }
+    if (tid == 0) p.moved[0] = live - base;
+    return;
+  }
   int live = 0;
   for (int p0 = 0; p0 < p.num_pages; p0 += n_thr * 8) {
     int v[8];

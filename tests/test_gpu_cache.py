@@ -206,6 +206,27 @@ def test_compact(state):
 
 
 @gpu
+@pytest.mark.parametrize("num", [1, 9, 8191, 8192, 8193, 20000])  # around what one block's registers hold
+@pytest.mark.parametrize("live", [0.0, 0.03, 0.5, 0.97, 1.0])
+def test_compact_pool_sizes(num, live):
+    rng = np.random.default_rng(num)
+    refs = [int(rng.integers(1, 4)) if rng.random() < live else 0 for _ in range(num)]
+    pools = [torch.from_numpy(rng.integers(0, 1 << 15, (num, 16, 1, 8)).astype(np.int16)).view(torch.float16).cuda()
+             for _ in range(2)]
+    host = [pool.view(torch.uint8).cpu().numpy().reshape(1, num, 16, -1).copy() for pool in pools]
+    held = [p for p in range(num) if refs[p] > 0][-3:]
+    rows, wr, go = P.compact(host, [held], [16 * len(held)], refs, 16)
+    table = i32([held + [1 << 20] * (4 - len(held))])
+    t, r, m = A.attn_cache_compact(*pools, table, i32([16 * len(held)]), i32(refs))
+    assert r.tolist() == wr and m.tolist() == go
+    same_table(t, rows)
+    n = sum(x > 0 for x in wr)
+    for pool, want in zip(pools, host):
+        assert np.array_equal(raw(pool, want)[:, :n], want[:, :n])
+    no_device_error()
+
+
+@gpu
 @pytest.mark.parametrize("B", [1025, 2600, 8192])  # past one block of threads; the most there may be
 def test_many_sequences(B):
     rng = np.random.default_rng(B)
