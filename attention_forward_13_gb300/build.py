@@ -18,7 +18,7 @@ LIB = os.path.join(BUILD, "libattn_fwd.so")
 SOURCES = ["prefill_d128.cu", "prefill_d64.cu", "prefill_keep_d128.cu", "prefill_keep_d64.cu",
            "decode_d128.cu", "decode_d64.cu", "tree_d128.cu", "tree_d64.cu", "combine.cu",
            "api.cu", "tree_api.cu", "cache.cu", "paged_noalloc.cu"]
-HEADERS = ["ptx.cuh", "common.cuh", "softmax.cuh", "launch.h", "host.h", "prefill_kernel.cuh",
+HEADERS = ["ptx.cuh", "common.cuh", "softmax.cuh", "launch.h", "host.h", "pages.h", "prefill_kernel.cuh",
            "decode_kernel.cuh", "tree_kernel.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v"]

@@ -15,6 +15,7 @@
 //    several independent accesses in flight per thread.
 #include "host.h"
 #include "launch.h"
+#include "pages.h"
 #include "ptx.cuh"
 
 #include <algorithm>
@@ -29,14 +30,6 @@ constexpr int kRange = 8192;     // pages counted at a time in shared memory
 constexpr int kMaxSeqs = 8192;   // sequences per call
 constexpr int kMaxCtas = 152;
 constexpr int kChunk = 16384;    // bytes of a page that a CTA copies at a time
-
-__device__ __forceinline__ int pages_of(int len, int page_log2) {
-  return (len + (1 << page_log2) - 1) >> page_log2;
-}
-
-__device__ __forceinline__ int held_pages(int len, int page_log2, int max_pages) {
-  return min(pages_of(max(len, 0), page_log2), max_pages);
-}
 
 __device__ __forceinline__ void report(unsigned int* err) {
   if (err) atomicOr(err, 1u << kErrCacheBadIndex);
