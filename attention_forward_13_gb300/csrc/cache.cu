@@ -672,15 +672,9 @@ int table_ctas(int B, int max_pages, int least) {
   return static_cast<int>(std::max<int64_t>(least, std::min<int64_t>(n, kMaxCtas)));
 }
 
-template <class... P, class... A>
-cudaError_t launch(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
-  if (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-  }
-  return launch_pdl(kern, grid, threads, smem, s, args...);
-}
+// Dynamic shared memory of a call over B sequences.
+constexpr size_t reorder_smem(int B) { return (kRange + static_cast<size_t>(B)) * 4; }  // accept's too
+constexpr size_t reserve_smem(int B) { return (5 * static_cast<size_t>(B) + 1) * 4; }
 
 }  // namespace
 
@@ -698,8 +692,9 @@ attn_status attn_cache_reorder(const int32_t* block_table, const int32_t* seqlen
   ReorderParams p{block_table, seqlens, page_refs, index, table_out, seqlens_out, refs_out,
                   B_in, B_out, max_pages, num_pages, log2_of(page_size), nullptr};
   if (host_device_state(&p.err, nullptr) != ATTN_OK) return ATTN_ERR_CUDA;
-  return host_finish(launch(reorder_kernel, dim3(table_ctas(B_out, max_pages, ref_ctas(num_pages))), 512, (kRange + (size_t)B_in) * 4,
-                            static_cast<cudaStream_t>(stream), p),
+  return host_finish(launch_pdl_upto<reorder_kernel>(reorder_smem(kMaxSeqs),
+                                                     dim3(table_ctas(B_out, max_pages, ref_ctas(num_pages))), 512,
+                                                     reorder_smem(B_in), static_cast<cudaStream_t>(stream), p),
                      "attn_cache_reorder");
 }
 
@@ -725,7 +720,8 @@ attn_status attn_cache_reserve(void* k_pool, void* v_pool, const int32_t* block_
   const int chunks = chunks_of(q);
   const int64_t tasks = static_cast<int64_t>(B) * chunks * 2 * layers;
   const int grid = static_cast<int>(std::max<int64_t>(table_ctas(B, max_pages, 1), std::min<int64_t>(tasks, sms)));
-  return host_finish(launch(reserve_kernel, dim3(grid), 1024, (5 * (size_t)B + 1) * 4, s, p, q, chunks),
+  return host_finish(launch_pdl_upto<reserve_kernel>(reserve_smem(kMaxSeqs), dim3(grid), 1024, reserve_smem(B), s, p,
+                                                     q, chunks),
                      "attn_cache_reserve");
 }
 
@@ -750,8 +746,8 @@ attn_status attn_cache_accept(void* k_pool, void* v_pool, const int32_t* block_t
   const PoolParams q = pool_params(k_pool, v_pool, layers, row_bytes, page_size, num_pages);
   const int64_t blocks = p.ref_ctas + static_cast<int64_t>(B) * 2 * layers * p.row_ctas;
   if (blocks > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
-  return host_finish(launch(accept_kernel, dim3(static_cast<unsigned>(blocks)), 128, (kRange + (size_t)B) * 4,
-                            static_cast<cudaStream_t>(stream), p, q),
+  return host_finish(launch_pdl_upto<accept_kernel>(reorder_smem(kMaxSeqs), dim3(static_cast<unsigned>(blocks)), 128,
+                                                    reorder_smem(B), static_cast<cudaStream_t>(stream), p, q),
                      "attn_cache_accept");
 }
 
@@ -771,9 +767,9 @@ attn_status attn_cache_compact(void* k_pool, void* v_pool, const int32_t* block_
   if (host_device_state(&p.err, &sms) != ATTN_OK) return ATTN_ERR_CUDA;
   const PoolParams q = pool_params(k_pool, v_pool, layers, row_bytes, page_size, num_pages);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch(compact_plan_kernel, dim3(1), 1024, 0, s, p);
+  cudaError_t e = launch_pdl(compact_plan_kernel, dim3(1), 1024, 0, s, p);
   if (e == cudaSuccess)
-    e = launch(compact_move_kernel, dim3(8 * sms), 128, 0, s, p, q, chunks_of(q));
+    e = launch_pdl(compact_move_kernel, dim3(8 * sms), 128, 0, s, p, q, chunks_of(q));
   return host_finish(e, "attn_cache_compact_plan+attn_cache_compact_move");
 }
 

@@ -1,7 +1,9 @@
 // launch.h -- host-side launchers of the kernels (one per translation unit),
 // called by the C ABI layer in api.cu after validation.
 #pragma once
+#include <atomic>
 #include <cstddef>
+#include <cstdint>
 #include <cuda_runtime.h>
 #include "common.cuh"
 
@@ -56,6 +58,26 @@ cudaError_t launch_pdl(void (*kern)(P...), dim3 grid, int threads, size_t smem, 
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+// The same for a kernel whose dynamic shared memory grows with the call, up to
+// `most` bytes: the limit is raised to that once per device and never lowered, so
+// that no call depends on the ones before it or on another host thread's.  (The
+// 48 KB a block may have unasked count the kernel's own shared arrays too.)
+template <auto kKern, class... A>
+cudaError_t launch_pdl_upto(size_t most, dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                            const A&... args) {
+  static std::atomic<uint64_t> raised{0};  // bit per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(raised.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(kKern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
+    if (e != cudaSuccess) return e;
+    raised.fetch_or(bit, std::memory_order_release);
+  }
+  return launch_pdl(kKern, grid, threads, smem, stream, args...);
 }
 
 cudaError_t launch_selftest_timeout(unsigned int* err, unsigned long long timeout_ns,

@@ -163,15 +163,12 @@ attn_status attn_tree_mask(const int32_t* parents, const int32_t* tree_lens, uin
   unsigned int* err = nullptr;
   if (host_device_state(&err, nullptr) != ATTN_OK) return ATTN_ERR_CUDA;
   const int W = (T + 31) / 32;
-  const int smem = (T * W + T) * 4;
+  constexpr int kMost = ATTN_TREE_MAX_NODES;
   int threads = (T * W + 31) / 32 * 32;
   if (threads > 1024) threads = 1024;
-  cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024)
-    e = cudaFuncSetAttribute(tree_mask_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess)
-    e = launch_pdl(tree_mask_kernel, dim3(B), threads, smem, static_cast<cudaStream_t>(stream), parents,
-                   tree_lens, mask, depth, T, W, err);
+  const cudaError_t e = launch_pdl_upto<tree_mask_kernel>(
+      (kMost * (kMost / 32) + kMost) * 4, dim3(B), threads, (T * W + T) * 4, static_cast<cudaStream_t>(stream), parents,
+      tree_lens, mask, depth, T, W, err);
   return host_finish(e, "attn_tree_mask");
 }
 
