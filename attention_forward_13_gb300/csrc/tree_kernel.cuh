@@ -858,14 +858,16 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
         a1 = ex2_approx(e1.x - ms);
         l = e0.y * a0 + e1.y * a1;
       }
-      // Everything that does not need O comes before the wait for it.
+      // Everything that does not need O comes before the wait for it.  (l is 0 where
+      // the row has seen nothing, and NaN, which has to come out, where a score was:
+      // hence comparisons with 0 and not l > 0.)
       float scale0 = a0, scale1 = a1, lse = -INFINITY;
       if (s.whole) {
         const float ms = m == -INFINITY ? 0.0f : m;
-        float mfin = ms, ltot = l, norm = l > 0.0f ? rcp_approx(l) : 0.0f;
+        float mfin = ms, ltot = l, norm = l != 0.0f ? rcp_approx(l) : 0.0f;
         if (p.sink != nullptr && row_in) {
           const float sl = p.sink[hq] * kLog2e;
-          if (l > 0.0f) {
+          if (l != 0.0f) {
             mfin = fmaxf(ms, sl);
             const float a = ex2_approx(ms - mfin);
             ltot = l * a + ex2_approx(sl - mfin);
@@ -875,11 +877,11 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
             ltot = 1.0f;
           }
         }
-        if (ltot > 0.0f) lse = (mfin + __log2f(ltot)) * kLn2;
+        if (ltot != 0.0f) lse = (mfin + __log2f(ltot)) * kLn2;
         scale0 *= norm;
         scale1 *= norm;
       }
-      const bool zero = !(l > 0.0f);  // nothing seen: O is 0 whatever the accumulator holds
+      const bool zero = l == 0.0f;  // nothing seen: O is 0 whatever the accumulator holds
       const int slot = cta * 2 + (s.k0 > 0 ? 0 : 1);  // a piece that starts inside its unit is the first
       const int prow = (pair ? t * 128 : 0) + r;      // row of the piece
       const int prows = pair ? 256 : 128;
@@ -1060,7 +1062,7 @@ __global__ void __launch_bounds__(256) attn_tree_merge_kernel(const __grid_const
       acc[7] = fmaf(v1[i].w, wgt, acc[7]);
     }
   }
-  const float norm = z > 0.0f ? 1.0f / z : 0.0f;
+  const float norm = z != 0.0f ? 1.0f / z : 0.0f;  // (a NaN piece makes z NaN, and so the row)
   T* out = reinterpret_cast<T*>(p.o) + ((static_cast<int64_t>(b) * p.T + qi) * p.Hq + hq) * D + col;
   uint32_t w4[4];
 #pragma unroll
@@ -1070,7 +1072,7 @@ __global__ void __launch_bounds__(256) attn_tree_merge_kernel(const __grid_const
   }
   *reinterpret_cast<uint4*>(out) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
   if (col == 0 && p.lse != nullptr)
-    p.lse[(static_cast<int64_t>(b) * p.Hq + hq) * p.T + qi] = z > 0.0f ? (M + __log2f(z)) * kLn2 : -INFINITY;
+    p.lse[(static_cast<int64_t>(b) * p.Hq + hq) * p.T + qi] = z != 0.0f ? (M + __log2f(z)) * kLn2 : -INFINITY;
 }
 
 template <int D, bool BF16, bool SOFTCAP, bool pair>
