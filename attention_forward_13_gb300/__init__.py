@@ -279,7 +279,7 @@ def attn_fwd_paged(q, k_pool, v_pool, block_table, seqlens_k, num_splits=0, o=No
         num_splits = 1  # chunked prefill: the prefill kernel, no split-KV scratch
     elif num_splits == 0:
         pages = attn_paged_window_pages(Lq, page, max_pages, window, causal, top_left, sink_tokens)
-        if sink_tokens > 0 and window is not None and window[0] >= 0:
+        if sink_tokens > 0 and window is not None and 0 <= window[0] < 1 << 30:
             num_splits = attn_paged_keep_splits(B, Hkv, page, pages)
         else:
             num_splits = attn_paged_auto_splits(B, Hkv, pages)

@@ -135,14 +135,19 @@ float resolve_scale(const attn_opts* o, int d) {
   return (o != nullptr && o->scale > 0.0f) ? o->scale : 1.0f / sqrtf(static_cast<float>(d));
 }
 
+// A bound of 2^30 or more reaches past every key, as K and V of 2^30 keys do not
+// fit the GPU: it counts as unbounded, and the kernels' sums of positions and
+// bounds stay within 32 bits.
+int resolve_bound(int keys) { return keys < 0 || keys >= (1 << 30) ? -1 : keys; }
+
 // Effective key bounds (negative = unbounded); causal is a right bound of 0.
 void resolve_window(const attn_opts* opts, int* wl, int* wr) {
   *wl = -1;
   *wr = -1;
   if (opts == nullptr) return;
   if (opts->use_window) {
-    *wl = opts->window_left < 0 ? -1 : opts->window_left;
-    *wr = opts->window_right < 0 ? -1 : opts->window_right;
+    *wl = resolve_bound(opts->window_left);
+    *wr = resolve_bound(opts->window_right);
   }
   if (opts->causal) *wr = 0;  // any window_right >= 0 is looser than causal
 }
@@ -150,7 +155,9 @@ void resolve_window(const attn_opts* opts, int* wl, int* wr) {
 // First tokens that stay visible left of the window; without a left bound
 // every earlier key is visible anyway.
 int resolve_keep(const attn_opts* opts) {
-  if (opts == nullptr || !opts->use_window || opts->window_left < 0) return 0;
+  int wl, wr;
+  resolve_window(opts, &wl, &wr);
+  if (wl < 0) return 0;
   return std::min(opts->sink_tokens, 1 << 30);  // (more than any sequence holds; the kernels round it up)
 }
 
@@ -311,6 +318,12 @@ bool host_make_map(CUtensorMap* m, const void* base, bool bf16, int rank, const 
 attn_status host_check_opts(const attn_opts* opts, int Hq, bool allow_bias) {
   return check_opts(opts, Hq, allow_bias);
 }
+int host_left(const attn_opts* opts) {
+  int wl, wr;
+  resolve_window(opts, &wl, &wr);
+  return wl;
+}
+int host_keep(const attn_opts* opts) { return resolve_keep(opts); }
 float host_scale(const attn_opts* opts, int d) { return resolve_scale(opts, d); }
 uint64_t host_timeout_ns() { return kTimeoutNs; }
 attn_status host_finish(cudaError_t e, const char* name) {

@@ -12,6 +12,9 @@ bool host_make_map(CUtensorMap* m, const void* base, bool bf16, int rank, const 
                    const uint64_t* strides_bytes, const uint32_t* box);
 // Options every attention entry point checks, and their resolved values.
 attn_status host_check_opts(const attn_opts* opts, int Hq, bool allow_bias);
+// Left bound of the window (negative: none) and the first tokens visible left of it.
+int host_left(const attn_opts* opts);
+int host_keep(const attn_opts* opts);
 float host_scale(const attn_opts* opts, int d);
 uint64_t host_timeout_ns();
 // Records the kernel name of attn_last_kernel_name and turns a launch's

@@ -23,6 +23,7 @@
 // device memory.
 #include "../../include/attn_fwd.h"
 #include "common.cuh"
+#include "host.h"
 #include "launch.h"
 
 #include <cmath>
@@ -77,9 +78,8 @@ extern "C" attn_status attn_fwd_paged_noalloc(const void* q, const void* k_pool,
   // is lowered until it fits (one split needs no scratch at all).
   if (num_splits == 0) {
     const int pages = attn_paged_window_pages(Lq, page_size, max_pages_per_seq, opts);
-    const bool keep = opts != nullptr && opts->use_window && opts->window_left >= 0 && opts->sink_tokens > 0;
-    num_splits = keep ? attn_paged_keep_splits(B, Hkv, page_size, pages)
-                      : attn_paged_auto_splits(B, Hkv, pages);
+    num_splits = attn::host_keep(opts) > 0 ? attn_paged_keep_splits(B, Hkv, page_size, pages)
+                                           : attn_paged_auto_splits(B, Hkv, pages);
     while (num_splits > 1 &&
            attn_paged_workspace_bytes(B, Lq, Hq, d, num_splits) > ATTN_NOALLOC_SCRATCH_BYTES)
       --num_splits;

@@ -129,8 +129,8 @@ attn_status tree_params(TreeParams* out, const void* q, const void* k_pool, cons
   while ((1 << p.page_log2) < page_size) ++p.page_log2;
   p.num_pages = num_pages;
   p.max_pages = max_pages;
-  p.win_left = opts != nullptr && opts->use_window && opts->window_left >= 0 ? opts->window_left : -1;
-  p.sink_tokens = p.win_left >= 0 ? opts->sink_tokens : 0;
+  p.win_left = host_left(opts);
+  p.sink_tokens = host_keep(opts);
   p.scale = host_scale(opts, d);
   p.scale_log2 = p.scale * kLog2e;
   p.softcap = opts != nullptr && opts->softcap > 0.0f ? opts->softcap : 0.0f;
@@ -244,7 +244,7 @@ bool host_chain_applies(int B, int Lq, int Hq, int Hkv, int page_size, int max_p
   int sms = 0;
   if (opts == nullptr || host_device_state(nullptr, &sms) != ATTN_OK) return false;
   const int grid = sms < kTreeMaxCtas ? sms : kTreeMaxCtas;
-  return opts->use_window && opts->window_left >= 0 && opts->sink_tokens > 0 && !opts->top_left &&
+  return host_keep(opts) > 0 && !opts->top_left &&
          opts->alibi_slopes == nullptr && (opts->causal || opts->window_right == 0 || Lq == 1) &&
          Lq <= queries_per_tile(g) && Hq <= 65535 && B <= 256 && static_cast<int64_t>(B) * Hkv >= 2 * grid &&
          line_fits(B, Hkv, page_size, max_pages);

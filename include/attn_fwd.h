@@ -77,7 +77,8 @@ typedef struct {
  * row i of a sequence with Lq queries and Lk keys sits on key diagonal
  * i + Lk - Lq.  Causal keeps keys j <= i + Lk - Lq.  A window keeps
  * i + Lk - Lq - window_left <= j <= i + Lk - Lq + window_right, a negative
- * bound meaning unbounded on that side; with causal also set both apply.
+ * bound meaning unbounded on that side (one of 2^30 or more too: no key lies
+ * that far off); with causal also set both apply.
  * sink_tokens > 0 keeps the keys j < sink_tokens visible left of the window
  * as well (the page's sink_size: first tokens a streaming cache never drops);
  * the right bound still applies to them, and without a left bound it changes
