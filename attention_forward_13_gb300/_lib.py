@@ -21,9 +21,9 @@ class attn_opts(ctypes.Structure):
                 ("sink", ctypes.c_void_p), ("use_window", ctypes.c_int),
                 ("window_left", ctypes.c_int), ("window_right", ctypes.c_int),
                 ("top_left", ctypes.c_int), ("alibi_slopes", ctypes.c_void_p),
-                ("alibi_stride", ctypes.c_int), ("bias", ctypes.c_void_p),
-                ("bias_strides", attn_strides), ("scale_p", ctypes.c_float),
-                ("scale_o", ctypes.c_float), ("sink_tokens", ctypes.c_int)]
+                ("alibi_stride", ctypes.c_int), ("sink_tokens", ctypes.c_int),
+                ("bias", ctypes.c_void_p), ("bias_strides", attn_strides),
+                ("scale_p", ctypes.c_float), ("scale_o", ctypes.c_float)]
 
 
 STATUS = {0: "ATTN_OK", 1: "ATTN_ERR_INVALID", 2: "ATTN_ERR_UNSUPPORTED", 3: "ATTN_ERR_CUDA",

@@ -131,6 +131,10 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // Element strides: positive and a whole number of 16-byte units.
 bool stride_ok(int64_t s, int eb = 2) { return s > 0 && (s * eb) % 16 == 0; }
 
+// What callers built before sink_tokens pass: it took the padding in front of bias.
+static_assert(sizeof(attn_opts) == 96 && offsetof(attn_opts, sink_tokens) == 52 && offsetof(attn_opts, bias) == 56,
+              "attn_opts keeps its size and its fields' places");
+
 float resolve_scale(const attn_opts* o, int d) {
   return (o != nullptr && o->scale > 0.0f) ? o->scale : 1.0f / sqrtf(static_cast<float>(d));
 }

@@ -71,9 +71,9 @@ typedef struct {
 } attn_strides;
 
 /*
- * Options.  A zero-initialised struct is plain softmax attention with the
- * default scale.  Masks (Composable Kernel mask from window_size_left /
- * window_size_right, generic attention mask) are bottom-right aligned: query
+ * Options.  A zero-initialised struct (all its bytes: memset, or = {0} as
+ * compilers do it) is plain softmax attention with the default scale.  Masks
+ * (Composable Kernel mask from window_size_left / window_size_right, generic attention mask) are bottom-right aligned: query
  * row i of a sequence with Lq queries and Lk keys sits on key diagonal
  * i + Lk - Lq.  Causal keeps keys j <= i + Lk - Lq.  A window keeps
  * i + Lk - Lq - window_left <= j <= i + Lk - Lq + window_right, a negative
@@ -102,6 +102,10 @@ typedef struct {
    * the scaled score (natural-log units).  NULL: off. */
   const float* alibi_slopes;
   int alibi_stride;
+  int sink_tokens;   /* keys j < sink_tokens stay visible left of the window; 0: none.
+                        (Younger than the fields after it: it lies in what was padding, so
+                        the struct keeps its size and a program built before it still
+                        passes one the library stays within.) */
   /* Elementwise bias (CK bias kargs), attn_fwd only: device, the input dtype,
    * element (b, h, i, j) at bias + b*batch + h*head + i*row + j (strides in
    * elements, multiples of 8, 0 broadcasts; 16-byte aligned base), added to
@@ -116,7 +120,6 @@ typedef struct {
    * bias with ATTN_E4M3. */
   float scale_p;
   float scale_o;
-  int sink_tokens;   /* keys j < sink_tokens stay visible left of the window; 0: none */
 } attn_opts;
 /* Combinations not built: soft-cap with ALiBi or bias (the pages do not fix
  * the order), ALiBi with bias, bias outside attn_fwd: ATTN_ERR_UNSUPPORTED. */
