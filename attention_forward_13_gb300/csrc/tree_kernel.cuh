@@ -741,13 +741,15 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
           const uint32_t* bits = p.tree_mask + node_row * p.words;
           const int sh0 = j0 - e.q.base;  // first column, counted from node 0
           const int wd = sh0 >> 5, bit = sh0 & 31;
+          // (Ordinary loads here and of the depth: the kernel that writes them may
+          // still run when this one starts, which the read-only path does not allow.)
           uint32_t wds[5];
 #pragma unroll
           for (int c = 0; c < 5; ++c)
-            wds[c] = wd + c >= 0 && wd + c < p.words ? __ldg(bits + wd + c) : 0u;
+            wds[c] = wd + c >= 0 && wd + c < p.words ? bits[wd + c] : 0u;
           int lo = 0;  // lowest key before the nodes that the window leaves
           if (p.win_left >= 0)
-            lo = e.q.base + max(0, min(__ldg(p.tree_depth + node_row), e.q.n - 1)) - p.win_left;
+            lo = e.q.base + max(0, min(p.tree_depth[node_row], e.q.n - 1)) - p.win_left;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const int k0 = j0 + 32 * c;
