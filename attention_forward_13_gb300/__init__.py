@@ -500,20 +500,27 @@ def attn_cache_reserve(k_pool, v_pool, block_table, seqlens, page_refs, add):
 
 
 @_on_stream
-def attn_cache_accept(k_pool, v_pool, block_table, seqlens, page_refs, path, path_lens, tree_lens):
-    """Keeps of each sequence's drafted nodes (the last tree_lens[b] positions) the nodes
-    path[b, :path_lens[b]] (int32 [B,A], rising), moved together behind the tokens before
-    them, and gives the pages past them back.  Returns (seqlens, page_refs); the pools are
-    updated in place, the table stays."""
-    dev, B, max_pages = _cache_state(block_table, seqlens, page_refs, path, path_lens, tree_lens)
+def attn_cache_accept(k_pool, v_pool, block_table, seqlens, page_refs, path, path_lens, tree_lens=None, T=None):
+    """Keeps of each sequence's drafted nodes (the last tree_lens[b] positions, at most T; the
+    last T without tree_lens) the nodes path[b, :path_lens[b]] (int32 [B,A], rising), moved
+    together behind the tokens before them, and gives the pages past them back.  Returns
+    (seqlens, page_refs); the pools are updated in place, the table stays."""
+    dev, B, max_pages = _cache_state(block_table, seqlens, page_refs, path, path_lens,
+                                     *(() if tree_lens is None else (tree_lens,)))
     layers, num_pages, page, row = _pools(k_pool, v_pool, page_refs)
+    if T is None:
+        if tree_lens is None:
+            raise ValueError("T, the nodes of every sequence, is needed without tree_lens")
+        T = max_pages * page
+    elif T < 0:
+        raise ValueError("T must not be negative")
     if path.dim() != 2:
         raise ValueError("path must be [B,A]")
     lens_out, refs_out = torch.empty_like(seqlens), torch.empty_like(page_refs)
     _check(_call(library().attn_cache_accept, dev, k_pool.data_ptr(), v_pool.data_ptr(),
                  block_table.data_ptr(), seqlens.data_ptr(), page_refs.data_ptr(), path.data_ptr(),
-                 path_lens.data_ptr(), tree_lens.data_ptr(), lens_out.data_ptr(), refs_out.data_ptr(), B,
-                 path.shape[1], max_pages * page, max_pages, num_pages, page, layers, row),
+                 path_lens.data_ptr(), _data(tree_lens), lens_out.data_ptr(), refs_out.data_ptr(), B,
+                 path.shape[1], int(T), max_pages, num_pages, page, layers, row),
            "attn_cache_accept")
     return lens_out, refs_out
 
