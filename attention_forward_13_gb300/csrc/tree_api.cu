@@ -75,8 +75,10 @@ __global__ void __launch_bounds__(1024)
 // one does not hold all T nodes.
 int queries_per_tile(int g) { return 128 / g; }
 
-// Tile slots of the whole call, at most: the kernels count them in 32 bits.
+// Tile slots of the whole call, at most, and the end of a sequence's last tile:
+// the kernels count both in 32 bits.
 bool line_fits(int B, int units, int page_size, int max_pages) {
+  if (static_cast<int64_t>(max_pages) * page_size > 0x7fffffffLL - 255) return false;
   return static_cast<double>(B) * units * ((static_cast<double>(max_pages) * page_size + 127) / 128 + 8) <
          2147483647.0;
 }
@@ -194,8 +196,7 @@ attn_status attn_fwd_paged_tree(const void* q, const void* k_pool, const void* v
     return ATTN_ERR_UNSUPPORTED;
   const int g = Hq / Hkv;
   if (static_cast<int64_t>(num_pages) * page_size > 0x7fffffffLL ||
-      static_cast<int64_t>(max_pages_per_seq) * page_size > 0x7fffffffLL || T > ATTN_TREE_MAX_NODES || g > 128 ||
-      Hq > 65535)
+      !line_fits(1, 1, page_size, max_pages_per_seq) || T > ATTN_TREE_MAX_NODES || g > 128 || Hq > 65535)
     return ATTN_ERR_UNSUPPORTED;
   if (B == 0 || T == 0) return ATTN_OK;
   if (q == nullptr || k_pool == nullptr || v_pool == nullptr || block_table == nullptr ||

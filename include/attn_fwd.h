@@ -262,7 +262,9 @@ attn_status attn_tree_mask(const int32_t* parents, const int32_t* tree_lens, uin
  *   workspace: attn_tree_workspace_bytes() bytes of device memory, 16-byte
  *   aligned, needed by every call; nothing in it has to be set, and calls that
  *   may overlap on the GPU (also replays of captured graphs) each need one.
- *   Hq / Hkv <= 128, T <= ATTN_TREE_MAX_NODES.  Results do not depend on what
+ *   Hq / Hkv <= 128, T <= ATTN_TREE_MAX_NODES, Hq <= 65535, tables of at most
+ *   2^31 - 256 positions, and B x Hkv x (blocks of queries) x (128-key tiles of a
+ *   table row + 8) below 2^31; else ATTN_ERR_UNSUPPORTED.  Results do not depend on what
  *   else runs: sums are taken in a fixed order.
  */
 size_t attn_tree_workspace_bytes(int T, int Hq, int Hkv, int d);
