@@ -359,9 +359,13 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // (no room at d = 128 to round the base up by hand: dynamic shared memory
   // starts at the window's 1024-byte base, and a launch where it does not ends
-  // here with an error)
+  // here with an error, and nothing for the merge kernel to do)
   if ((smem_u32(smem_raw) & 1023u) != 0) {
-    if (threadIdx.x == 0 && p.err) atomicOr(p.err, 1u << kErrTreeTeardown);
+    pdl_wait();
+    if (threadIdx.x == 0) {
+      if (p.err) atomicOr(p.err, 1u << kErrTreeTeardown);
+      if (p.o_part != nullptr) p.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    }
     return;
   }
   TreeSmem<C>& sm = *reinterpret_cast<TreeSmem<C>*>(smem_raw);

@@ -29,3 +29,17 @@ def test_no_read_only_loads_of_what_an_earlier_kernel_may_write(name):
     text = code(name)
     for form in ("__ldg", "ld.global.nc", "__restrict__", "tex1D"):
         assert form not in text, form
+
+
+def test_every_exit_of_the_tree_kernel_leaves_the_merge_kernel_its_answer():
+    """The merge kernel follows whatever p.cut says.  No exit may leave what the workspace
+    held before: the one before the work starts (shared memory not where it has to be,
+    which no launch here shows) writes "no unit", after the kernel before has let go of
+    the workspace."""
+    text = code("tree_kernel.cuh")
+    body = text[text.index("attn_tree_kernel(const"):text.index("attn_tree_merge_kernel(const")]
+    exits = [m.start() for m in re.finditer(r"(?m)^ +return;", body)]  # (others leave a lambda)
+    assert len(exits) == 1
+    early = body[body.index("& 1023u"):exits[0]]
+    assert "p.cut[blockIdx.x] = make_int4(-1, 0, 0, 0)" in early
+    assert "pdl_wait()" in early and early.index("pdl_wait()") < early.index("p.cut[")
