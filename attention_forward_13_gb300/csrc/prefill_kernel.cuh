@@ -168,14 +168,16 @@ struct PrefillSmem : PrefillSmemFp8<C>, PrefillSmemOrder<ORD> {
 // FP8: one 128-key V tile, e4m3 rows of 128 bytes (128B-swizzled as TMA
 // wrote them) -> fp16 in the MN-major layout the P.V MMA reads (two 64-column
 // 128B-swizzled atoms).  64 threads, 16 of the 1024 (row, 16-byte piece)
-// pairs each; e4m3 -> fp16 is exact.
-template <class C>
-__device__ __forceinline__ void widen_v_tile(const uint8_t* raw, uint8_t* out, int ct) {
+// pairs each; e4m3 -> fp16 is exact.  TAIL: rows from `live` on become zeros
+// (in group mode they are another sequence's, and 0 * NaN in P.V is not 0).
+template <class C, bool TAIL>
+__device__ __forceinline__ void widen_v_tile(const uint8_t* raw, uint8_t* out, int ct, int live) {
 #pragma unroll 4
   for (int k = 0; k < 16; ++k) {
     const int i = ct + 64 * k;
     const int r = i >> 3, u = i & 7;  // key row, 16-byte piece (columns 16u .. 16u+15)
-    const uint4 x = *reinterpret_cast<const uint4*>(raw + r * 128 + ((u ^ (r & 7)) << 4));
+    uint4 x = *reinterpret_cast<const uint4*>(raw + r * 128 + ((u ^ (r & 7)) << 4));
+    if (TAIL && r >= live) x = make_uint4(0u, 0u, 0u, 0u);
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
     uint32_t h[8];
 #pragma unroll
@@ -787,12 +789,22 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
         ++qn;
         if (!ok) break;
         umma_commit_warp(&sm.k_empty[g % C::NS], lead);
-        // Paged cache: the tile that ends inside a page (none: -1), worked out
+        // Rows [live, end) of the last step's tile, if any, lie behind the
+        // sequence's end and in memory that may hold anything: the rest of the
+        // last page, or in group mode the next sequence (and what follows the
+        // last one).  0 * NaN in P.V is not 0, so they are zeroed.  Worked out
         // per item: at every step it cost this warp 1.3 % (chunked prefill of 8
         // sequences, 512 queries: 1053 against 1039 TFLOP/s).
-        int tail_key = -1;
-        if constexpr (ORD && !FP8)
-          if (p.block_table != nullptr && it.Lk % p.page_size != 0) tail_key = it.Lk / C::BN * C::BN;
+        auto tail_rows = [&](int& live, int& end) {
+          live = it.Lk - kv_key<MASK>(it, it.cnt - 1);
+          end = p.block_table != nullptr ? min(C::BN, (live + p.page_size - 1) & ~(p.page_size - 1)) : C::BN;
+        };
+        int tail = -1;
+        if constexpr (ORD && !FP8) {
+          int live, end;
+          tail_rows(live, end);
+          if (live < end) tail = it.cnt - 1;
+        }
         // Every streamed K/V tile is waited for and released at its step, used
         // or not (a narrow window can leave a tile to neither query tile).
         for (int u = 0; ok && u < it.cnt; ++u) {
@@ -804,11 +816,9 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
             ok = w.wait(&sm.v_full[s], (gu / C::NS) & 1, kErrPrefillVFull);
           if (!ok) break;
           if constexpr (ORD && !FP8) {
-            // Paged cache: rows of the last page behind the sequence's end
-            // may hold anything, and 0 * NaN in P.V is not 0: zero them.
-            if (kv_key<MASK>(it, u) == tail_key) {
-              const int live = it.Lk - tail_key;
-              const int end = min(C::BN, (live + p.page_size - 1) / p.page_size * p.page_size);
+            if (u == tail) {
+              int live, end;
+              tail_rows(live, end);
               for (int i = lane; i < (end - live) * C::NCHUNK * 8; i += 32) {
                 const int row = live + i / (C::NCHUNK * 8), c = (i >> 3) % C::NCHUNK;
                 *reinterpret_cast<uint4*>(sm.v[s] + c * C::CHUNK_BYTES + row * 128 + (i & 7) * 16) =
@@ -886,7 +896,7 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
                __all_sync(0xffffffffu,
                           w.wait(&sm.vc_empty[c], ((g / C::NVC) & 1) ^ 1, kErrPrefillVEmpty));
           if (!ok) break;
-          widen_v_tile<C>(sm.v[s], sm.vc[c], ct);
+          widen_v_tile<C, ORD>(sm.v[s], sm.vc[c], ct, it.Lk - kv_key<MASK>(it, j));
           fence_proxy_async_smem();  // the tensor core reads what these threads wrote
           mbar_arrive(&sm.vc_full[c]);
           mbar_arrive(&sm.v_empty[s]);
