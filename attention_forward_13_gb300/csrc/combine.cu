@@ -35,38 +35,39 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const CombineParams p
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   const float sink_l2 = (p.sink != nullptr) ? p.sink[h] * kLog2e : -INFINITY;
-  const float m2 = fmaxf(m * kLog2e, sink_l2);  // log2 units
+  // Log2 units; 0 where no part has seen anything.  (fmaxf passes NaN over: a part
+  // whose LSE is NaN makes z and the row NaN below.)
+  const float mx = fmaxf(m * kLog2e, sink_l2);
+  const float m2 = mx == -INFINITY ? 0.0f : mx;
 
   float acc[VPL];
 #pragma unroll
   for (int i = 0; i < VPL; ++i) acc[i] = 0.0f;
   float z = 0.0f;
-  if (m2 != -INFINITY) {
-    for (int s = 0; s < p.num_splits; ++s) {
-      const float ls = p.lse_part[s * rows + r];
-      if (ls == -INFINITY) continue;
-      const float wgt = exp2f(ls * kLog2e - m2);
-      z += wgt;
-      const float* src = p.o_part + (s * rows + r) * D + lane * VPL;
-      if constexpr (VPL == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(src);
-        acc[0] += wgt * v.x;
-        acc[1] += wgt * v.y;
-        acc[2] += wgt * v.z;
-        acc[3] += wgt * v.w;
-      } else {
+  for (int s = 0; s < p.num_splits; ++s) {
+    const float ls = p.lse_part[s * rows + r];
+    if (ls == -INFINITY) continue;
+    const float wgt = exp2f(ls * kLog2e - m2);
+    z += wgt;
+    const float* src = p.o_part + (s * rows + r) * D + lane * VPL;
+    if constexpr (VPL == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(src);
+      acc[0] += wgt * v.x;
+      acc[1] += wgt * v.y;
+      acc[2] += wgt * v.z;
+      acc[3] += wgt * v.w;
+    } else {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) acc[i] += wgt * src[i];
-      }
+      for (int i = 0; i < VPL; ++i) acc[i] += wgt * src[i];
     }
-    if (p.sink != nullptr) z += exp2f(sink_l2 - m2);
   }
-  const float inv = (z > 0.0f) ? 1.0f / z : 0.0f;
+  if (p.sink != nullptr) z += exp2f(sink_l2 - m2);
+  const float inv = (z != 0.0f) ? 1.0f / z : 0.0f;
   T* dst = reinterpret_cast<T*>(p.o) + ((static_cast<int64_t>(b) * p.Lq + qi) * p.Hq + h) * D +
            lane * VPL;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) dst[i] = T(acc[i] * inv);
-  if (lane == 0 && p.lse != nullptr) p.lse[r] = (z > 0.0f) ? (m2 + log2f(z)) * kLn2 : -INFINITY;
+  if (lane == 0 && p.lse != nullptr) p.lse[r] = (z != 0.0f) ? (m2 + log2f(z)) * kLn2 : -INFINITY;
 }
 
 cudaError_t launch_combine(const CombineParams& p, bool bf16, cudaStream_t stream, char* name,

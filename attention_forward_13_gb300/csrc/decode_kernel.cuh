@@ -514,17 +514,19 @@ __global__ void __launch_bounds__(192, 2)
           out_row(r, h, qi);
           const int64_t row = (static_cast<int64_t>(b) * p.Hq + h) * p.Lq + qi;
           const float msub = (m_use[r] == -INFINITY) ? 0.0f : m_use[r];
+          // (l is 0 where the row has seen nothing, NaN, which has to come out,
+          // where a score was: hence comparisons with 0 and not l > 0.)
           float oscale, lse;
           if (partial_out) {
-            oscale = l[r] > 0.0f ? 1.0f / l[r] : 0.0f;
-            lse = l[r] > 0.0f ? (msub + __log2f(l[r])) * kLn2 : -INFINITY;
+            oscale = l[r] != 0.0f ? 1.0f / l[r] : 0.0f;
+            lse = l[r] != 0.0f ? (msub + __log2f(l[r])) * kLn2 : -INFINITY;
             p.o_part[(split * rows_total + row) * D + tid] = __uint_as_float(ov[r]) * oscale;
             if (tid == 0) p.lse_part[split * rows_total + row] = lse;
           } else {
             float mfin = msub, ltot = l[r];
             if (p.sink != nullptr) {
               const float sl = p.sink[h] * kLog2e;
-              if (l[r] > 0.0f) {
+              if (l[r] != 0.0f) {
                 mfin = fmaxf(msub, sl);
                 const float a = ex2_approx(msub - mfin);
                 ltot = l[r] * a + ex2_approx(sl - mfin);
@@ -535,9 +537,9 @@ __global__ void __launch_bounds__(192, 2)
                 oscale = 0.0f;
               }
             } else {
-              oscale = l[r] > 0.0f ? 1.0f / l[r] : 0.0f;
+              oscale = l[r] != 0.0f ? 1.0f / l[r] : 0.0f;
             }
-            lse = ltot > 0.0f ? (mfin + __log2f(ltot)) * kLn2 : -INFINITY;
+            lse = ltot != 0.0f ? (mfin + __log2f(ltot)) * kLn2 : -INFINITY;
             reinterpret_cast<T*>(p.o)[((static_cast<int64_t>(b) * p.Lq + qi) * p.Hq + h) * D +
                                       tid] = T(__uint_as_float(ov[r]) * oscale);
             if (tid == 0 && p.lse != nullptr) p.lse[row] = lse;

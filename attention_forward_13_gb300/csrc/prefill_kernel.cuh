@@ -1228,11 +1228,13 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
       }
       const float msub = (m_use == -INFINITY) ? 0.0f : m_use;
       const bool row_ok = qi < it.Lq;
+      // (l is 0 where the row has seen nothing, NaN, which has to come out, where a
+      // score was: hence comparisons with 0 and not l > 0.)
       float oscale;  // 1 / denominator (with the sink's share)
       float mfin = msub, ltot = l;
       if (p.sink != nullptr) {
         const float sl = p.sink[hr] * kLog2e;
-        if (l > 0.0f) {
+        if (l != 0.0f) {
           mfin = fmaxf(msub, sl);
           const float a = ex2_approx(msub - mfin);
           ltot = l * a + ex2_approx(sl - mfin);
@@ -1243,9 +1245,9 @@ __global__ void __launch_bounds__(PrefillCfg<D, DT>::THREADS, 1)
           oscale = 0.0f;
         }
       } else {
-        oscale = (l > 0.0f) ? 1.0f / l : 0.0f;
+        oscale = (l != 0.0f) ? 1.0f / l : 0.0f;
       }
-      const float lse_out = (ltot > 0.0f) ? (mfin + __log2f(ltot)) * kLn2 : -INFINITY;  // natural log
+      const float lse_out = (ltot != 0.0f) ? (mfin + __log2f(ltot)) * kLn2 : -INFINITY;  // natural log
       // The warp's 32 rows are 32 consecutive queries of one head when the
       // stores go by TMA (host: at most 4 heads per tile): its first one and
       // its head are the box's coordinates.

@@ -37,6 +37,12 @@
  *  - Element strides: the innermost (head-dim) stride is always 1; row, head
  *    and batch strides are in elements and must be multiples of 8 (16 bytes);
  *    base pointers must be 16-byte aligned.
+ *  - NaN among the scores a row sees makes its O and LSE NaN; LSE = -inf means
+ *    that it has seen nothing.  Masked scores may be anything.  A masked key's
+ *    weight is 0, and 0 times an infinite or NaN V is NaN: V has to be finite
+ *    within a sequence, also where only some of a call's rows see it.  What lies
+ *    behind a sequence's end may hold anything (the rest of its last page, other
+ *    pages, the next packed sequence), and so may pages that a window leaves out.
  *  - Supported: d in {64, 128}; fp16 or bf16 Q/K/V/O; Hq % Hkv == 0.
  */
 #ifndef ATTN_FWD_H
@@ -281,7 +287,8 @@ attn_status attn_fwd_paged_tree(const void* q, const void* k_pool, const void* v
  * the definition of LSE; FlashAttention-3 epilogue num_splits layout):
  *   M = max_s LSE_s,  w_s = exp(LSE_s - M),
  *   LSE = M + ln(sum_s w_s + exp(sink[h] - M)),  O = sum_s exp(LSE_s - LSE) O_s.
- *   Splits with LSE_s = -inf contribute nothing; if none contributes and
+ *   Splits with LSE_s = -inf contribute nothing, one of NaN makes the row NaN;
+ *   if none contributes and
  *   there is no sink, O = 0 and LSE = -inf.
  *   o_partial fp32 [num_splits][B][Hq][Lq][d]; lse_partial fp32
  *   [num_splits][B][Hq][Lq]; sink fp32 [Hq] or NULL (added once, here);
