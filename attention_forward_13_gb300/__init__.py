@@ -398,7 +398,8 @@ def attn_fwd_paged_tree(q, k_pool, v_pool, block_table, seqlens_k, tree_mask, tr
     """Attention of drafted nodes over a paged cache.  q [B,T,Hq,d]; the nodes' K/V are the
     last T (or tree_lens[b]) of the seqlens_k[b] positions; node i sees every earlier
     position and the nodes of its tree_mask row (attn_tree_mask).  ``window`` = (left, -1)
-    with tree_depth limits the earlier positions, the first ``sink_tokens`` staying visible.
+    with tree_depth limits the earlier positions, the first ``sink_tokens`` staying visible; it
+    cuts no nodes (where a path is longer than the window, clear those ancestors' bits).
     Returns (o [B,T,Hq,d], lse fp32 [B,Hq,T] or None)."""
     B, T, Hq, d = q.shape
     num_pages, page, Hkv, dk = k_pool.shape

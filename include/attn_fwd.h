@@ -263,7 +263,10 @@ attn_status attn_tree_mask(const int32_t* parents, const int32_t* tree_lens, uin
  *   opts: scale, softcap, sink; a window with window_right < 0 keeps of the
  *   positions below base those >= base + depth_i - window_left and the first
  *   sink_tokens (tree_depth, device int32 [B][T], is needed then; depths are
- *   clamped to [0, n_b)), and the pages it leaves out are not read.  Causal,
+ *   clamped to [0, n_b)), and the pages it leaves out are not read.  It does not
+ *   cut nodes: where a path is longer than the window, the caller clears the bits
+ *   of the ancestors more than window_left above a node (with depths, those with
+ *   depth_j < depth_i - window_left).  Causal,
  *   top_left, window_right >= 0, ALiBi, bias: ATTN_ERR_UNSUPPORTED.
  *   workspace: attn_tree_workspace_bytes() bytes of device memory, 16-byte
  *   aligned, needed by every call; nothing in it has to be set, and calls that
@@ -355,8 +358,8 @@ attn_status attn_dense_schedule(int B, int Hq, int Hkv, int Lq, int Lk, const at
  * (table entries past the held ones are written as -1).  An output may not
  * overlap an input, except refs_out = page_refs in attn_cache_reorder and
  * attn_cache_accept.  Pools are [layers][num_pages][page_size][row]: the same
- * table for every layer, row_bytes = Hkv * d * element size, a multiple of 16
- * (any element type and head dimension).  page_size as for attn_fwd_paged;
+ * table for every layer, row_bytes = Hkv * d * element size, a multiple of 16 of
+ * at most 2^24 (any element type and head dimension).  page_size as for attn_fwd_paged;
  * B <= 8192.  An index out of range never faults: the entry is left out, and
  * the device error word's bit for bad cache indices is set.  All are
  * deterministic and need no setting of anything beforehand.  They can be
