@@ -4,7 +4,9 @@ Every function here only marshals torch tensors (device pointers, sizes,
 strides, the current CUDA stream) into the C library ``libattn_fwd.so``; all
 arithmetic runs in the library's CUDA kernels.  There is no fallback: if the
 library is missing and cannot be built, or a call fails, an exception is
-raised.  Output tensors are allocated with torch when not given.
+raised.  Output tensors are allocated with torch when not given.  Work goes to
+the current stream; ``stream=s`` makes a call what it is under
+``torch.cuda.stream(s)``, allocations included.
 
     o, lse = attn_fwd(q, k, v, causal=True)                 # [B,H,L,d]
     o, lse = attn_fwd_varlen(q, k, v, cu_q, cu_k, max_q)    # [total,H,d]
@@ -21,6 +23,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 
 import torch
 
@@ -150,6 +153,26 @@ def _check_sink(sink, Hq, device):
     return sink.contiguous()
 
 
+def _on_stream(fn):
+    """With ``stream`` given, the call runs as under ``torch.cuda.stream(stream)``: what it
+    allocates and copies on the way belongs to the stream that uses it.  A function that
+    names ``stream`` among its parameters takes it by position too."""
+    names = list(inspect.signature(fn).parameters)
+    at = names.index("stream") if "stream" in names else len(names)
+
+    @functools.wraps(fn)
+    def call(*args, **kwargs):
+        stream = kwargs.pop("stream", None)
+        if len(args) > at:
+            stream, args = args[at], args[:at] + (None,) + args[at + 1:]
+        if stream is None:
+            return fn(*args, **kwargs)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kwargs)
+    return call
+
+
+@_on_stream
 def attn_fwd(q, k, v, o=None, lse=True, causal=False, scale=None, softcap=0.0, sink=None,
              stream=None, window=None, top_left=False, alibi_slopes=None, bias=None,
              scale_p=None, scale_o=None, sink_tokens=0):
@@ -184,6 +207,7 @@ def attn_fwd(q, k, v, o=None, lse=True, causal=False, scale=None, softcap=0.0, s
     return o, lse_t
 
 
+@_on_stream
 def attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, o=None, lse=True,
                     causal=False, scale=None, softcap=0.0, sink=None, stream=None, window=None,
                     top_left=False, alibi_slopes=None, scale_p=None, scale_o=None, sink_tokens=0):
@@ -263,6 +287,7 @@ def attn_dense_schedule(B, Hq, Lq, Lk, grid, causal=False, window=None, top_left
     return [list(item[off[c]:off[c + 1]]) for c in range(grid)]
 
 
+@_on_stream
 def attn_fwd_paged(q, k_pool, v_pool, block_table, seqlens_k, num_splits=0, o=None, lse=True,
                    causal=False, scale=None, softcap=0.0, sink=None, workspace=None,
                    stream=None, window=None, top_left=False, alibi_slopes=None, sink_tokens=0):
@@ -311,6 +336,7 @@ def attn_fwd_paged(q, k_pool, v_pool, block_table, seqlens_k, num_splits=0, o=No
     return o, lse_t
 
 
+@_on_stream
 def attn_fwd_paged_noalloc(q, k_pool, v_pool, block_table, seqlens_k, num_splits=0, o=None,
                            lse=True, causal=False, scale=None, softcap=0.0, sink=None,
                            stream=None, window=None, top_left=False, alibi_slopes=None,
@@ -352,18 +378,6 @@ def _ints(device, names, *tensors):
     for t in tensors:
         if t is not None and not (t.dtype is torch.int32 and t.device == device and t.is_contiguous()):
             raise ValueError(f"{names} must be contiguous int32 on {device}")
-
-
-def _on_stream(fn):
-    """With ``stream`` given, the call runs with that stream current: what it allocates (and
-    frees again) then belongs to the stream that uses it."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kwargs):
-        if stream is None:
-            return fn(*args, **kwargs)
-        with torch.cuda.stream(stream):
-            return fn(*args, **kwargs)
-    return call
 
 
 def _data(t):
@@ -542,6 +556,7 @@ def attn_cache_compact(k_pool, v_pool, block_table, seqlens, page_refs):
     return table_out, refs_out, page_map
 
 
+@_on_stream
 def attn_splitkv_combine(o_partial, lse_partial, sink=None, dtype=torch.bfloat16, o=None,
                          lse=True, stream=None):
     """Merge split partials.  o_partial fp32 [S,B,Hq,Lq,d], lse_partial fp32 [S,B,Hq,Lq].
