@@ -24,6 +24,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import inspect
+import math
 
 import torch
 
@@ -172,6 +173,19 @@ def _on_stream(fn):
     return call
 
 
+def _check_alike(q, k, v, o, lse, lse_shape):
+    """Types, devices and shapes of a dense or packed call (strides are checked by the library)."""
+    dev, dt = q.device, q.dtype
+    if k.dtype is not dt or v.dtype is not dt or o.dtype is not dt or k.device != dev or v.device != dev or \
+            o.device != dev:
+        raise ValueError("q, k, v and o must be of one type and on one device")
+    if v.shape != k.shape or k.shape[-1] != q.shape[-1] or o.shape != q.shape:
+        raise ValueError("k and v must be alike, with q's head dimension, and o like q")
+    if lse is not None and (lse.dtype is not torch.float32 or lse.numel() != math.prod(lse_shape) or
+                            not lse.is_contiguous() or lse.device != dev):
+        raise ValueError(f"lse must be contiguous fp32 {list(lse_shape)}")
+
+
 @_on_stream
 def attn_fwd(q, k, v, o=None, lse=True, causal=False, scale=None, softcap=0.0, sink=None,
              stream=None, window=None, top_left=False, alibi_slopes=None, bias=None,
@@ -193,6 +207,9 @@ def attn_fwd(q, k, v, o=None, lse=True, causal=False, scale=None, softcap=0.0, s
         lse_t = torch.empty((B, Hq, Lq), dtype=torch.float32, device=q.device)
     elif isinstance(lse, torch.Tensor):
         lse_t = lse
+    if k.dim() != 4 or k.shape[0] != B:
+        raise ValueError("k and v must be [B,Hkv,Lk,d]")
+    _check_alike(q, k, v, o, lse_t, (B, Hq, Lq))
     sink = _check_sink(sink, Hq, q.device)
     alibi_slopes = _check_alibi(alibi_slopes, B, Hq, q.device)
     if bias is not None and (bias.dtype != q.dtype or bias.device != q.device):
@@ -226,6 +243,9 @@ def attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, o=None, l
         lse_t = torch.empty((Hq, total_q), dtype=torch.float32, device=q.device)
     elif isinstance(lse, torch.Tensor):
         lse_t = lse
+    if k.dim() != 3 or cu_seqlens_k.numel() != B + 1:
+        raise ValueError("k and v must be [total_k,Hkv,d], both cu_seqlens [B+1]")
+    _check_alike(q, k, v, o, lse_t, (Hq, total_q))
     sink = _check_sink(sink, Hq, q.device)
     alibi_slopes = _check_alibi(alibi_slopes, B, Hq, q.device)
     opts = _opts(scale, causal, softcap, sink, window, top_left, alibi_slopes, None, scale_p,
@@ -287,6 +307,26 @@ def attn_dense_schedule(B, Hq, Lq, Lk, grid, causal=False, window=None, top_left
     return [list(item[off[c]:off[c + 1]]) for c in range(grid)]
 
 
+def _check_paged(q, k_pool, v_pool, block_table, seqlens_k, o, lse):
+    """What the paged kernels take for granted of their tensors; returns max_pages."""
+    dev = q.device
+    for t in (q, k_pool, v_pool, block_table, seqlens_k, o):
+        if not t.is_contiguous() or t.device != dev:
+            raise ValueError("paged inputs and o must be contiguous and on one device")
+    if block_table.dtype is not torch.int32 or seqlens_k.dtype is not torch.int32:
+        raise ValueError("block_table and seqlens_k must be int32")
+    B, Lq, Hq, d = q.shape
+    if k_pool.dtype is not q.dtype or v_pool.dtype is not q.dtype or o.dtype is not q.dtype or \
+            v_pool.shape != k_pool.shape or k_pool.shape[3] != d or o.shape != q.shape:
+        raise ValueError("q, o [B,Lq,Hq,d] and the pools [num_pages,page,Hkv,d] must be of one type")
+    if block_table.dim() != 2 or block_table.shape[0] != B or seqlens_k.numel() != B:
+        raise ValueError("block_table must be [B,max_pages], seqlens_k [B]")
+    if lse is not None and (lse.dtype is not torch.float32 or lse.numel() != B * Hq * Lq or
+                            not lse.is_contiguous() or lse.device != dev):
+        raise ValueError("lse must be contiguous fp32 [B,Hq,Lq]")
+    return block_table.shape[1]
+
+
 @_on_stream
 def attn_fwd_paged(q, k_pool, v_pool, block_table, seqlens_k, num_splits=0, o=None, lse=True,
                    causal=False, scale=None, softcap=0.0, sink=None, workspace=None,
@@ -296,10 +336,14 @@ def attn_fwd_paged(q, k_pool, v_pool, block_table, seqlens_k, num_splits=0, o=No
     Returns (o [B,Lq,Hq,d], lse fp32 [B,Hq,Lq] or None)."""
     B, Lq, Hq, d = q.shape
     num_pages, page, Hkv, _ = k_pool.shape
-    max_pages = block_table.shape[1]
-    for t in (q, k_pool, v_pool, block_table, seqlens_k):
-        if not t.is_contiguous():
-            raise ValueError("paged inputs must be contiguous")
+    if o is None:
+        o = torch.empty((B, Lq, Hq, d), dtype=q.dtype, device=q.device)
+    lse_t = None
+    if lse is True:
+        lse_t = torch.empty((B, Hq, Lq), dtype=torch.float32, device=q.device)
+    elif isinstance(lse, torch.Tensor):
+        lse_t = lse
+    max_pages = _check_paged(q, k_pool, v_pool, block_table, seqlens_k, o, lse_t)
     if Lq * (Hq // Hkv) > 16:
         num_splits = 1  # chunked prefill: the prefill kernel, no split-KV scratch
     elif num_splits == 0:
@@ -308,17 +352,13 @@ def attn_fwd_paged(q, k_pool, v_pool, block_table, seqlens_k, num_splits=0, o=No
             num_splits = attn_paged_keep_splits(B, Hkv, page, pages)
         else:
             num_splits = attn_paged_auto_splits(B, Hkv, pages)
-    if o is None:
-        o = torch.empty((B, Lq, Hq, d), dtype=q.dtype, device=q.device)
-    lse_t = None
-    if lse is True:
-        lse_t = torch.empty((B, Hq, Lq), dtype=torch.float32, device=q.device)
-    elif isinstance(lse, torch.Tensor):
-        lse_t = lse
     o_part = lse_part = None
     if num_splits > 1:
         rows = B * Hq * Lq
         need = num_splits * rows * (d + 1)
+        if workspace is not None and (workspace.dtype is not torch.float32 or workspace.device != q.device or
+                                      workspace.dim() != 1 or not workspace.is_contiguous()):
+            raise ValueError("workspace must be contiguous fp32 [n] on the same device")
         if workspace is None or workspace.numel() < need:
             workspace = torch.empty(need, dtype=torch.float32, device=q.device)
         o_part = workspace[: num_splits * rows * d]
@@ -354,6 +394,7 @@ def attn_fwd_paged_noalloc(q, k_pool, v_pool, block_table, seqlens_k, num_splits
         lse_t = torch.empty((B, Hq, Lq), dtype=torch.float32, device=q.device)
     elif isinstance(lse, torch.Tensor):
         lse_t = lse
+    max_pages = _check_paged(q, k_pool, v_pool, block_table, seqlens_k, o, lse_t)
     sink = _check_sink(sink, Hq, q.device)
     alibi_slopes = _check_alibi(alibi_slopes, B, Hq, q.device)
     opts = _opts(scale, causal, softcap, sink, window, top_left, alibi_slopes,
@@ -361,7 +402,7 @@ def attn_fwd_paged_noalloc(q, k_pool, v_pool, block_table, seqlens_k, num_splits
     st = library().attn_fwd_paged_noalloc(_ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_table),
                                           _ptr(seqlens_k), _ptr(o), _ptr(lse_t), B, Lq, Hq, Hkv,
                                           d, _dtype_code(q), page, num_pages,
-                                          block_table.shape[1], num_splits, ctypes.byref(opts),
+                                          max_pages, num_splits, ctypes.byref(opts),
                                           _stream(stream))
     _check(st, "attn_fwd_paged_noalloc")
     return o, lse_t
