@@ -64,7 +64,8 @@ def _dtype_code(t: torch.Tensor) -> int:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    """The address of a tensor for the C library (None: NULL)."""
+    return None if t is None else t.data_ptr()
 
 
 # The current stream's handle without building a Stream object (3 us a call on a
@@ -74,9 +75,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _stream(stream):
     if stream is None and _raw_stream is not None:
-        return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
+        return _raw_stream(torch.cuda.current_device())
     s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    return s.cuda_stream
 
 
 def _call(fn, device, *args):
@@ -173,17 +174,29 @@ def _on_stream(fn):
     return call
 
 
-def _check_alike(q, k, v, o, lse, lse_shape):
-    """Types, devices and shapes of a dense or packed call (strides are checked by the library)."""
-    dev, dt = q.device, q.dtype
-    if k.dtype is not dt or v.dtype is not dt or o.dtype is not dt or k.device != dev or v.device != dev or \
-            o.device != dev:
-        raise ValueError("q, k, v and o must be of one type and on one device")
-    if v.shape != k.shape or k.shape[-1] != q.shape[-1] or o.shape != q.shape:
-        raise ValueError("k and v must be alike, with q's head dimension, and o like q")
-    if lse is not None and (lse.dtype is not torch.float32 or lse.numel() != math.prod(lse_shape) or
-                            not lse.is_contiguous() or lse.device != dev):
+def _outputs(q, o, lse, lse_shape):
+    """(o, lse or None): new tensors, or the given ones checked (o like q, any strides)."""
+    if o is None:
+        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    elif o.dtype is not q.dtype or o.device != q.device or o.shape != q.shape:
+        raise ValueError("o must be like q")
+    if lse is True:
+        return o, torch.empty(lse_shape, dtype=torch.float32, device=q.device)
+    if not isinstance(lse, torch.Tensor):
+        return o, None
+    if lse.dtype is not torch.float32 or lse.numel() != math.prod(lse_shape) or not lse.is_contiguous() or \
+            lse.device != q.device:
         raise ValueError(f"lse must be contiguous fp32 {list(lse_shape)}")
+    return o, lse
+
+
+def _check_alike(q, k, v, dims):
+    """Types, devices and shapes of a dense or packed call (strides are checked by the library)."""
+    dt, dev, shape = q.dtype, q.get_device(), k.shape
+    if k.dtype is not dt or v.dtype is not dt or k.get_device() != dev or v.get_device() != dev:
+        raise ValueError("q, k and v must be of one type and on one device")
+    if len(shape) != dims or v.shape != shape or shape[-1] != q.shape[-1]:
+        raise ValueError("k and v must be alike, with q's head dimension")
 
 
 @_on_stream
@@ -199,21 +212,18 @@ def attn_fwd(q, k, v, o=None, lse=True, causal=False, scale=None, softcap=0.0, s
     e4m3, scale_o * scale_p * softmax(S) V saturated.  Returns (o [B,Hq,Lq,d], lse fp32
     [B,Hq,Lq] or None)."""
     B, Hq, Lq, d = q.shape
-    Hkv, Lk = k.shape[1], k.shape[2]
-    if o is None:
-        o = torch.empty((B, Hq, Lq, d), dtype=q.dtype, device=q.device)
-    lse_t = None
-    if lse is True:
-        lse_t = torch.empty((B, Hq, Lq), dtype=torch.float32, device=q.device)
-    elif isinstance(lse, torch.Tensor):
-        lse_t = lse
-    if k.dim() != 4 or k.shape[0] != B:
+    _check_alike(q, k, v, 4)
+    Bk, Hkv, Lk, _ = k.shape
+    if Bk != B:
         raise ValueError("k and v must be [B,Hkv,Lk,d]")
-    _check_alike(q, k, v, o, lse_t, (B, Hq, Lq))
+    o, lse_t = _outputs(q, o, lse, (B, Hq, Lq))
     sink = _check_sink(sink, Hq, q.device)
     alibi_slopes = _check_alibi(alibi_slopes, B, Hq, q.device)
-    if bias is not None and (bias.dtype != q.dtype or bias.device != q.device):
-        raise ValueError("bias must have the input dtype and device")
+    if bias is not None:
+        if bias.dtype != q.dtype or bias.device != q.device:
+            raise ValueError("bias must have the input dtype and device")
+        if bias.dim() != 4 or bias.shape[3] < Lk or any(x not in (1, y) for x, y in zip(bias.shape, (B, Hq, Lq))):
+            raise ValueError("bias must be [B|1, Hq|1, Lq|1, Lk]")
     opts = _opts(scale, causal, softcap, sink, window, top_left, alibi_slopes, bias, scale_p,
                  scale_o, sink_tokens)
     st = library().attn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse_t), B, Hq, Hkv, Lq, Lk,
@@ -231,21 +241,15 @@ def attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, o=None, l
     """Group mode.  q [total_q,Hq,d], k/v [total_k,Hkv,d], cu_seqlens int32 [B+1] on the
     device.  Returns (o [total_q,Hq,d], lse fp32 [Hq,total_q] or None)."""
     total_q, Hq, d = q.shape
-    total_k, Hkv = k.shape[0], k.shape[1]
+    _check_alike(q, k, v, 3)
+    total_k, Hkv, _ = k.shape
     B = cu_seqlens_q.numel() - 1
     for cu in (cu_seqlens_q, cu_seqlens_k):
         if cu.dtype != torch.int32 or cu.device != q.device or not cu.is_contiguous():
             raise ValueError("cu_seqlens must be contiguous int32 on the device")
-    if o is None:
-        o = torch.empty((total_q, Hq, d), dtype=q.dtype, device=q.device)
-    lse_t = None
-    if lse is True:
-        lse_t = torch.empty((Hq, total_q), dtype=torch.float32, device=q.device)
-    elif isinstance(lse, torch.Tensor):
-        lse_t = lse
-    if k.dim() != 3 or cu_seqlens_k.numel() != B + 1:
-        raise ValueError("k and v must be [total_k,Hkv,d], both cu_seqlens [B+1]")
-    _check_alike(q, k, v, o, lse_t, (Hq, total_q))
+    if cu_seqlens_k.numel() != B + 1:
+        raise ValueError("both cu_seqlens must be [B+1]")
+    o, lse_t = _outputs(q, o, lse, (Hq, total_q))
     sink = _check_sink(sink, Hq, q.device)
     alibi_slopes = _check_alibi(alibi_slopes, B, Hq, q.device)
     opts = _opts(scale, causal, softcap, sink, window, top_left, alibi_slopes, None, scale_p,
@@ -307,24 +311,23 @@ def attn_dense_schedule(B, Hq, Lq, Lk, grid, causal=False, window=None, top_left
     return [list(item[off[c]:off[c + 1]]) for c in range(grid)]
 
 
-def _check_paged(q, k_pool, v_pool, block_table, seqlens_k, o, lse):
+def _check_paged(q, k_pool, v_pool, block_table, seqlens_k, o):
     """What the paged kernels take for granted of their tensors; returns max_pages."""
-    dev = q.device
-    for t in (q, k_pool, v_pool, block_table, seqlens_k, o):
-        if not t.is_contiguous() or t.device != dev:
-            raise ValueError("paged inputs and o must be contiguous and on one device")
+    dev, dt = q.get_device(), q.dtype
+    for t in (q, k_pool, v_pool, block_table, seqlens_k):
+        if not t.is_contiguous() or t.get_device() != dev:
+            raise ValueError("paged inputs must be contiguous and on one device")
+    if o is not None and not o.is_contiguous():
+        raise ValueError("o must be contiguous")
     if block_table.dtype is not torch.int32 or seqlens_k.dtype is not torch.int32:
         raise ValueError("block_table and seqlens_k must be int32")
-    B, Lq, Hq, d = q.shape
-    if k_pool.dtype is not q.dtype or v_pool.dtype is not q.dtype or o.dtype is not q.dtype or \
-            v_pool.shape != k_pool.shape or k_pool.shape[3] != d or o.shape != q.shape:
-        raise ValueError("q, o [B,Lq,Hq,d] and the pools [num_pages,page,Hkv,d] must be of one type")
-    if block_table.dim() != 2 or block_table.shape[0] != B or seqlens_k.numel() != B:
+    shape = k_pool.shape
+    if k_pool.dtype is not dt or v_pool.dtype is not dt or v_pool.shape != shape or shape[3] != q.shape[3]:
+        raise ValueError("the pools [num_pages,page,Hkv,d] must be alike, of q's type and head dimension")
+    B, max_pages = block_table.shape
+    if B != q.shape[0] or seqlens_k.numel() != B:
         raise ValueError("block_table must be [B,max_pages], seqlens_k [B]")
-    if lse is not None and (lse.dtype is not torch.float32 or lse.numel() != B * Hq * Lq or
-                            not lse.is_contiguous() or lse.device != dev):
-        raise ValueError("lse must be contiguous fp32 [B,Hq,Lq]")
-    return block_table.shape[1]
+    return max_pages
 
 
 @_on_stream
@@ -336,14 +339,8 @@ def attn_fwd_paged(q, k_pool, v_pool, block_table, seqlens_k, num_splits=0, o=No
     Returns (o [B,Lq,Hq,d], lse fp32 [B,Hq,Lq] or None)."""
     B, Lq, Hq, d = q.shape
     num_pages, page, Hkv, _ = k_pool.shape
-    if o is None:
-        o = torch.empty((B, Lq, Hq, d), dtype=q.dtype, device=q.device)
-    lse_t = None
-    if lse is True:
-        lse_t = torch.empty((B, Hq, Lq), dtype=torch.float32, device=q.device)
-    elif isinstance(lse, torch.Tensor):
-        lse_t = lse
-    max_pages = _check_paged(q, k_pool, v_pool, block_table, seqlens_k, o, lse_t)
+    max_pages = _check_paged(q, k_pool, v_pool, block_table, seqlens_k, o)
+    o, lse_t = _outputs(q, o, lse, (B, Hq, Lq))
     if Lq * (Hq // Hkv) > 16:
         num_splits = 1  # chunked prefill: the prefill kernel, no split-KV scratch
     elif num_splits == 0:
@@ -387,14 +384,8 @@ def attn_fwd_paged_noalloc(q, k_pool, v_pool, block_table, seqlens_k, num_splits
     here only when not given."""
     B, Lq, Hq, d = q.shape
     num_pages, page, Hkv, _ = k_pool.shape
-    if o is None:
-        o = torch.empty((B, Lq, Hq, d), dtype=q.dtype, device=q.device)
-    lse_t = None
-    if lse is True:
-        lse_t = torch.empty((B, Hq, Lq), dtype=torch.float32, device=q.device)
-    elif isinstance(lse, torch.Tensor):
-        lse_t = lse
-    max_pages = _check_paged(q, k_pool, v_pool, block_table, seqlens_k, o, lse_t)
+    max_pages = _check_paged(q, k_pool, v_pool, block_table, seqlens_k, o)
+    o, lse_t = _outputs(q, o, lse, (B, Hq, Lq))
     sink = _check_sink(sink, Hq, q.device)
     alibi_slopes = _check_alibi(alibi_slopes, B, Hq, q.device)
     opts = _opts(scale, causal, softcap, sink, window, top_left, alibi_slopes,
@@ -421,11 +412,6 @@ def _ints(device, names, *tensors):
             raise ValueError(f"{names} must be contiguous int32 on {device}")
 
 
-def _data(t):
-    """The address of a tensor for the C library (None: NULL)."""
-    return None if t is None else t.data_ptr()
-
-
 @_on_stream
 def attn_tree_mask(parents, tree_lens=None, mask=None, depth=None):
     """Visibility masks and depths of draft trees.  parents int32 [B,T] (-1: follows the
@@ -441,7 +427,7 @@ def attn_tree_mask(parents, tree_lens=None, mask=None, depth=None):
     if mask.shape != (B, T, W) or depth.shape != (B, T) or \
             (tree_lens is not None and tree_lens.shape != (B,)):
         raise ValueError("tree_lens is [B], mask [B,T,ceil(T/32)], depth [B,T]")
-    _check(_call(library().attn_tree_mask, dev, parents.data_ptr(), _data(tree_lens),
+    _check(_call(library().attn_tree_mask, dev, parents.data_ptr(), _ptr(tree_lens),
                  mask.data_ptr(), depth.data_ptr(), B, T), "attn_tree_mask")
     return mask, depth
 
@@ -488,7 +474,7 @@ def attn_fwd_paged_tree(q, k_pool, v_pool, block_table, seqlens_k, tree_mask, tr
     opts = _opts(scale, False, softcap, sink, window, sink_tokens=sink_tokens)
     st = _call(library().attn_fwd_paged_tree, dev, q.data_ptr(), k_pool.data_ptr(),
                v_pool.data_ptr(), block_table.data_ptr(), seqlens_k.data_ptr(), tree_mask.data_ptr(),
-               _data(tree_lens), _data(tree_depth), o.data_ptr(), _data(lse_t), B, T, Hq, Hkv, d,
+               _ptr(tree_lens), _ptr(tree_depth), o.data_ptr(), _ptr(lse_t), B, T, Hq, Hkv, d,
                _dtype_code(q), page, num_pages, block_table.shape[1], workspace.data_ptr(),
                workspace.numel() * workspace.element_size(), ctypes.byref(opts))
     _check(st, "attn_fwd_paged_tree")
@@ -575,7 +561,7 @@ def attn_cache_accept(k_pool, v_pool, block_table, seqlens, page_refs, path, pat
     lens_out, refs_out = torch.empty_like(seqlens), torch.empty_like(page_refs)
     _check(_call(library().attn_cache_accept, dev, k_pool.data_ptr(), v_pool.data_ptr(),
                  block_table.data_ptr(), seqlens.data_ptr(), page_refs.data_ptr(), path.data_ptr(),
-                 path_lens.data_ptr(), _data(tree_lens), lens_out.data_ptr(), refs_out.data_ptr(), B,
+                 path_lens.data_ptr(), _ptr(tree_lens), lens_out.data_ptr(), refs_out.data_ptr(), B,
                  path.shape[1], int(T), max_pages, num_pages, page, layers, row),
            "attn_cache_accept")
     return lens_out, refs_out

@@ -55,6 +55,9 @@ DENSE = {
     "k of another head dimension": ((Q4, torch.zeros(2, 2, 9, 128, dtype=torch.float16),
                                      torch.zeros(2, 2, 9, 128, dtype=torch.float16)), {}),
     "k of fewer batches": ((Q4, K4[:1], K4[:1]), {}),
+    "a bias of fewer keys": ((Q4, K4, K4), dict(bias=torch.zeros(1, 1, 8, 8, dtype=torch.float16))),
+    "a bias of fewer rows": ((Q4, K4, K4), dict(bias=torch.zeros(2, 4, 7, 9, dtype=torch.float16))),
+    "a bias of fewer heads": ((Q4, K4, K4), dict(bias=torch.zeros(2, 2, 8, 9, dtype=torch.float16))),
     "o of another type": ((Q4, K4, K4), dict(o=Q4.float())),
     "o of another shape": ((Q4, K4, K4), dict(o=Q4[:, :, :7])),
     "a short lse": ((Q4, K4, K4), dict(lse=torch.zeros(2, 4, 7))),
