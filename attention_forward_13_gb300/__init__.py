@@ -589,16 +589,19 @@ def attn_splitkv_combine(o_partial, lse_partial, sink=None, dtype=torch.bfloat16
     """Merge split partials.  o_partial fp32 [S,B,Hq,Lq,d], lse_partial fp32 [S,B,Hq,Lq].
     Returns (o [B,Lq,Hq,d] in ``dtype``, lse fp32 [B,Hq,Lq] or None)."""
     S, B, Hq, Lq, d = o_partial.shape
+    dev = o_partial.device
+    if o_partial.dtype is not torch.float32 or lse_partial.dtype is not torch.float32 or \
+            lse_partial.shape != o_partial.shape[:4] or lse_partial.device != dev:
+        raise ValueError("o_partial must be fp32 [S,B,Hq,Lq,d], lse_partial fp32 [S,B,Hq,Lq]")
     if o is None:
-        o = torch.empty((B, Lq, Hq, d), dtype=dtype, device=o_partial.device)
-    lse_t = None
-    if lse is True:
-        lse_t = torch.empty((B, Hq, Lq), dtype=torch.float32, device=o_partial.device)
-    elif isinstance(lse, torch.Tensor):
-        lse_t = lse
-    sink = _check_sink(sink, Hq, o_partial.device)
-    st = library().attn_splitkv_combine(_ptr(o_partial.contiguous()),
-                                        _ptr(lse_partial.contiguous()), S, B, Hq, Lq, d,
+        o = torch.empty((B, Lq, Hq, d), dtype=dtype, device=dev)
+    elif o.shape != (B, Lq, Hq, d) or not o.is_contiguous() or o.device != dev:
+        raise ValueError("o must be contiguous [B,Lq,Hq,d]")
+    _, lse_t = _outputs(o, o, lse, (B, Hq, Lq))
+    sink = _check_sink(sink, Hq, dev)
+    # (Held by name until the call: a copy's memory may not go to the next copy.)
+    o_partial, lse_partial = o_partial.contiguous(), lse_partial.contiguous()
+    st = library().attn_splitkv_combine(_ptr(o_partial), _ptr(lse_partial), S, B, Hq, Lq, d,
                                         _ptr(sink), _ptr(o), _dtype_code(o), _ptr(lse_t),
                                         _stream(stream))
     _check(st, "attn_splitkv_combine")
