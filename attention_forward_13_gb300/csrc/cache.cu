@@ -204,9 +204,10 @@ struct ReserveParams {
 // 47.9 us with two kernels, 45.1 with one; four beams 15.4 and 13.3).  The search
 // for earlier holders of a page is quadratic in the sequences: the call takes 10
 // us at 64, 12 at 256, 25 at 1024, 192 at 4096 and 670 at 8192 (pages of 64, no
-// page shared; 4 to 10 us more where pairs share their pages and one of each copies).  CTA 0 writes the new pages and the counts, and
-// all share the rows of the table (one CTA alone writes a 2 MB table in 50 us)
-// and the copies: eight groups of 128 threads a CTA, 16 KB a task.
+// page shared; 4 to 10 us more where pairs share their pages and one of each
+// copies).  CTA 0 writes the new pages and the counts, and all share the rows of
+// the table (one CTA alone writes a 2 MB table in 50 us) and the copies: eight
+// groups of 128 threads a CTA, 16 KB a task.
 __global__ void __launch_bounds__(1024, 1) reserve_kernel(const ReserveParams p, const PoolParams q, int chunks) {
   extern __shared__ int sh[];
   int* last = sh;              // [B] page that the sequence would share, or -1

@@ -1011,8 +1011,9 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
 // some twenty with eight), which one thread reads one after the other: latency
 // bound, hence narrow column slices, four pieces in flight and one pass with a
 // running maximum.  (One user with 131072 keys, d = 128, both kernels: 46 us with
-// one kv head, 52 with two, 112 with eight; reading K and V takes 10, 20 and 79.)  It is launched with programmatic serialisation, so
-// that only its first read waits for the tree kernel.
+// one kv head, 52 with two, 112 with eight; reading K and V takes 10, 20 and 79.)
+// It is launched with programmatic serialisation, so that only its first read
+// waits for the tree kernel.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(256) attn_tree_merge_kernel(const __grid_constant__ TreeParams p) {
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;

@@ -79,7 +79,8 @@ typedef struct {
 /*
  * Options.  A zero-initialised struct (all its bytes: memset, or = {0} as
  * compilers do it) is plain softmax attention with the default scale.  Masks
- * (Composable Kernel mask from window_size_left / window_size_right, generic attention mask) are bottom-right aligned: query
+ * (Composable Kernel mask from window_size_left / window_size_right, generic
+ * attention mask) are bottom-right aligned: query
  * row i of a sequence with Lq queries and Lk keys sits on key diagonal
  * i + Lk - Lq.  Causal keeps keys j <= i + Lk - Lq.  A window keeps
  * i + Lk - Lq - window_left <= j <= i + Lk - Lq + window_right, a negative
