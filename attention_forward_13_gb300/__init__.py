@@ -18,6 +18,13 @@ the current stream; ``stream=s`` makes a call what it is under
     table, lens, refs, free = attn_cache_reserve(k_pool, v_pool, table, lens, refs, add)
     lens, refs = attn_cache_accept(k_pool, v_pool, table, lens, refs, path, path_lens, tree_lens)
     table, refs, page_map = attn_cache_compact(k_pool, v_pool, table, lens, refs)
+    slots, positions, cu, seq = attn_cache_slots(table, lens, add, tokens, page, num_pages)
+    inv_freq = attn_rope_freqs(rotary_dim)                  # fp64, once per model
+    q, k = attn_rope(q, k, inv_freq, positions)
+    q = attn_cache_append(k, v, k_pool, v_pool, slots, q=q, inv_freq=inv_freq, positions=positions)
+    o, state = attn_linear_fwd(q, k, v, log_decay)          # [B,H,L,d], a decay per head
+    o, state = attn_linear_fwd_varlen(q, k, v, cu, max_seqlen, log_decay, state=state)
+    o = attn_linear_step(q, k, v, log_decay, state)         # one token each, state in place
 """
 from __future__ import annotations
 
@@ -35,7 +42,10 @@ __all__ = ["attn_fwd", "attn_fwd_varlen", "attn_fwd_paged", "attn_splitkv_combin
            "attn_selftest_timeout", "attn_last_kernel_name", "attn_paged_window_pages", "attn_paged_keep_splits",
            "attn_fwd_paged_noalloc", "attn_dense_schedule", "attn_tree_mask",
            "attn_tree_workspace_bytes", "attn_fwd_paged_tree", "attn_cache_reorder",
-           "attn_cache_reserve", "attn_cache_accept", "attn_cache_compact", "gqa_pack", "AttnError", "library"]
+           "attn_cache_reserve", "attn_cache_accept", "attn_cache_compact",
+           "attn_cache_slots", "attn_rope_freqs", "attn_rope", "attn_cache_append",
+           "attn_linear_workspace_bytes", "attn_linear_fwd", "attn_linear_fwd_varlen", "attn_linear_step",
+           "gqa_pack", "AttnError", "library"]
 
 
 class AttnError(RuntimeError):
@@ -581,6 +591,264 @@ def attn_cache_compact(k_pool, v_pool, block_table, seqlens, page_refs):
                  refs_out.data_ptr(), page_map.data_ptr(), work.data_ptr(), B, max_pages, num_pages, page,
                  layers, row), "attn_cache_compact")
     return table_out, refs_out, page_map
+
+
+@_on_stream
+def attn_cache_slots(block_table, seqlens, add, num_tokens, page_size, num_pages):
+    """The slot map of the last add[b] (int32 [B]) of each sequence's seqlens[b] tokens, packed
+    in order of the sequences, room for ``num_tokens`` of them (rows past the last: sequence
+    -1, position 0, slot -1).  Returns (slots [num_tokens], positions [num_tokens], cu_seqlens
+    [B+1], sequence [num_tokens]), int32."""
+    dev, B, max_pages = _cache_state(block_table, seqlens, add)
+    n = int(num_tokens)
+    if n < 0:
+        raise ValueError("num_tokens must not be negative")
+    slots, positions, sequence = (torch.empty(n, dtype=torch.int32, device=dev) for _ in range(3))
+    cu = torch.empty(B + 1, dtype=torch.int32, device=dev)
+    _check(_call(library().attn_cache_slots, dev, block_table.data_ptr(), seqlens.data_ptr(), add.data_ptr(),
+                 slots.data_ptr(), positions.data_ptr(), cu.data_ptr(), sequence.data_ptr(), B, n, max_pages,
+                 int(num_pages), int(page_size)), "attn_cache_slots")
+    return slots, positions, cu, sequence
+
+
+_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "parts": 3, "ramp": 4}
+
+
+def attn_rope_freqs(rotary_dim, base=10000.0, scaling="plain", factor=1.0, original_len=0.0, slow_turns=1.0,
+                    fast_turns=32.0, device="cuda"):
+    """Rotary frequencies base^(-2i / rotary_dim), fp64 [rotary_dim / 2] on ``device``, scaled for
+    long contexts: "linear" (all divided by factor), "base" (a larger base), "parts" and
+    "ramp" (pairs of at most slow_turns turns in original_len positions divided by
+    factor, those of fast_turns or more kept, between them weighted by turns or by index)."""
+    if scaling not in _SCALINGS:
+        raise ValueError(f"scaling must be one of {', '.join(_SCALINGS)}")
+    f = (ctypes.c_double * max(1, int(rotary_dim) // 2))()
+    _check(library().attn_rope_freqs(int(rotary_dim), float(base), _SCALINGS[scaling], float(factor),
+                                     float(original_len), float(slow_turns), float(fast_turns), f),
+           "attn_rope_freqs")
+    return torch.tensor(list(f), dtype=torch.float64, device=device)
+
+
+def _rope_opts(inv_freq, d, device, interleaved, inverse, scale):
+    if inv_freq.dtype is not torch.float64 or inv_freq.dim() != 1 or inv_freq.device != device or \
+            not inv_freq.is_contiguous() or 2 * inv_freq.shape[0] > d:
+        raise ValueError("inv_freq must be contiguous fp64 [rotary_dim / 2] on the same device, rotary_dim <= d")
+    return _lib.attn_rope_opts(inv_freq.data_ptr(), 2 * inv_freq.shape[0], 1 if interleaved else 0,
+                               1 if inverse else 0, float(scale))
+
+
+def _like(t, out, name):
+    """A new contiguous tensor like t, or ``out`` checked to be one (any strides)."""
+    if out is None:
+        return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    if out.dtype is not t.dtype or out.device != t.device or out.shape != t.shape:
+        raise ValueError(f"{name} must be like its input")
+    return out
+
+
+def _rows(t):
+    """Strides of dense [B,H,L,d] or packed [N,H,d] rows (None: no tensor)."""
+    if t is None:
+        return _lib.attn_strides(0, 0, 0)
+    return _strides_bhld(t) if t.dim() == 4 else _strides_thd(t)
+
+
+@_on_stream
+def attn_rope(q, k, inv_freq, positions=None, interleaved=False, inverse=False, scale=1.0, q_out=None, k_out=None):
+    """Rotary positions.  q [B,Hq,L,d] and k [B,Hkv,L,d], or packed [N,H,d] (k may be None); the
+    first 2 * len(inv_freq) elements of a head turn by position * inv_freq (attn_rope_freqs),
+    in halves or interleaved pairs, times ``scale``.  positions int32 [L] or [B,L], packed [N];
+    None: the row.  ``inverse`` turns back.  q_out and k_out may be q and k.  Returns (q_out, k_out)."""
+    dims, dev = q.dim(), q.device
+    if dims not in (3, 4):
+        raise ValueError("q must be [B,Hq,L,d] or [N,Hq,d]")
+    if dims == 4:
+        B, Hq, L, d = q.shape
+    else:
+        B, (L, Hq, d) = 1, q.shape
+    Hkv = 0
+    if k is not None:
+        if k.dtype is not q.dtype or k.device != dev or k.dim() != dims or k.shape[-1] != d or \
+                (k.shape[0], k.shape[2]) != (B, L) and dims == 4 or dims == 3 and k.shape[0] != L:
+            raise ValueError("k must be like q but for its heads")
+        Hkv = k.shape[1]
+    stride = 0
+    if positions is not None:
+        _ints(dev, "positions", positions)
+        if positions.shape == (L,):
+            pass
+        elif dims == 4 and positions.shape == (B, L):
+            stride = L
+        else:
+            raise ValueError("positions must be [L] or [B,L], of packed rows [N]")
+    opts = _rope_opts(inv_freq, d, dev, interleaved, inverse, scale)
+    q_out = _like(q, q_out, "q_out")
+    if k is not None:
+        k_out = _like(k, k_out, "k_out")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    _check(_call(library().attn_rope, dev, q.data_ptr(), q_out.data_ptr(), _ptr(k), _ptr(k_out), _ptr(positions),
+                 stride, B, L, Hq, Hkv, d, _dtype_code(q), _rows(q), _rows(q_out), _rows(k), _rows(k_out),
+                 ctypes.byref(opts)), "attn_rope")
+    return q_out, k_out
+
+
+@_on_stream
+def attn_cache_append(k, v, k_pool, v_pool, slots, q=None, inv_freq=None, positions=None, interleaved=False,
+                      scale=1.0, q_out=None):
+    """Writes packed new tokens' k and v [N,Hkv,d] into the pools [num_pages,page,Hkv,d] by slot
+    (int32 [N], attn_cache_slots; -1: not written; no slot twice).  With ``inv_freq`` and
+    ``positions`` (int32 [N]) k is rotated on the way, and so is q [N,Hq,d], every row, into
+    q_out (q itself, or a new tensor).  Returns q_out (None without q)."""
+    dev, dt = k.device, k.dtype
+    if k.dim() != 3 or v.shape != k.shape or v.dtype is not dt or v.device != dev:
+        raise ValueError("k and v must be [N,Hkv,d], alike")
+    N, Hkv, d = k.shape
+    if k_pool.dim() != 4 or v_pool.shape != k_pool.shape or k_pool.shape[2:] != (Hkv, d) or \
+            not k_pool.dtype is v_pool.dtype is dt or not k_pool.device == v_pool.device == dev or \
+            not k_pool.is_contiguous() or not v_pool.is_contiguous():
+        raise ValueError("the pools must be contiguous [num_pages,page,Hkv,d], of k's type, on its device")
+    _ints(dev, "slots and positions", slots, positions)
+    if slots.shape != (N,) or (positions is not None and positions.shape != (N,)):
+        raise ValueError("slots and positions must be [N]")
+    Hq = 0
+    if q is not None:
+        if q.dim() != 3 or q.dtype is not dt or q.device != dev or q.shape[0] != N or q.shape[2] != d:
+            raise ValueError("q must be [N,Hq,d], of k's type, on its device")
+        Hq = q.shape[1]
+        q_out = _like(q, q_out, "q_out")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    opts = None
+    if inv_freq is not None:
+        if positions is None:
+            raise ValueError("positions are needed to rotate")
+        opts = ctypes.byref(_rope_opts(inv_freq, d, dev, interleaved, False, scale))
+    _check(_call(library().attn_cache_append, dev, _ptr(q), _ptr(q_out), k.data_ptr(), v.data_ptr(),
+                 k_pool.data_ptr(), v_pool.data_ptr(), slots.data_ptr(), _ptr(positions), N, Hq, Hkv, d,
+                 _dtype_code(k), k_pool.shape[1], k_pool.shape[0], _rows(q), _rows(q_out), _rows(k), _rows(v), opts),
+           "attn_cache_append")
+    return q_out
+
+
+def attn_linear_workspace_bytes(B, Hq, max_seqlen, d) -> int:
+    """Bytes of device memory attn_linear_fwd and attn_linear_fwd_varlen work in (may be 0)."""
+    return int(library().attn_linear_workspace_bytes(B, Hq, max_seqlen, d))
+
+
+def _linear_states(log_decay, state, state_out, state_index, B, Hq, d, device):
+    """(state, state_out, num_states) of a linear-attention call, checked."""
+    if log_decay.dtype is not torch.float32 or log_decay.shape != (Hq,) or log_decay.device != device or \
+            not log_decay.is_contiguous():
+        raise ValueError("log_decay must be contiguous fp32 [Hq] on the same device")
+    if state_index is not None:
+        _ints(device, "state_index", state_index)
+        if state_index.shape != (B,):
+            raise ValueError("state_index must be [B]")
+    if state_out is True:
+        if state_index is None:
+            state_out = torch.empty((B, Hq, d, d), dtype=torch.float32, device=device)
+        elif state is None:
+            raise ValueError("with state_index and no state, state_out must be a tensor, None or False")
+        else:
+            state_out = state
+    elif state_out is False:
+        state_out = None
+    n = None
+    for s in (state, state_out):
+        if s is None:
+            continue
+        if s.dtype is not torch.float32 or s.device != device or s.dim() != 4 or s.shape[1:] != (Hq, d, d) or \
+                not s.is_contiguous() or (state_index is None and s.shape[0] != B) or n not in (None, s.shape[0]):
+            raise ValueError("states must be contiguous fp32 [B,Hq,d,d] ([n,Hq,d,d] with state_index), alike")
+        n = s.shape[0]
+    return state, state_out, n or 0
+
+
+def _linear_workspace(workspace, B, Hq, max_seqlen, d, device):
+    need = attn_linear_workspace_bytes(B, Hq, max_seqlen, d)
+    if workspace is None:
+        return (torch.empty(need, dtype=torch.uint8, device=device) if need else None), need
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous on the same device")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+@_on_stream
+def attn_linear_fwd(q, k, v, log_decay, state=None, state_out=True, state_index=None, scale=None, o=None,
+                    workspace=None):
+    """Linear attention with a decay per head: S_t = e^log_decay S_(t-1) + k_t v_t^T, o_t = scale *
+    q_t^T S_t.  q [B,Hq,L,d], k/v [B,Hkv,L,d], log_decay fp32 [Hq] (<= 0).  ``state``: fp32
+    [B,Hq,d,d] before the first token (None: 0); ``state_out``: where the last one goes (True: a
+    new tensor; ``state`` itself: in place; False: not kept).  With ``state_index`` (int32 [B], -1:
+    none) both are a pool's rows, and True means in place.  Returns (o, state_out)."""
+    B, Hq, L, d = q.shape
+    _check_alike(q, k, v, 4)
+    Hkv = k.shape[1]
+    if k.shape != (B, Hkv, L, d):
+        raise ValueError("k and v must be [B,Hkv,L,d]")
+    dev = q.device
+    o = _like(q, o, "o")
+    state, state_out, n = _linear_states(log_decay, state, state_out, state_index, B, Hq, d, dev)
+    work, size = _linear_workspace(workspace, B, Hq, L, d, dev)
+    st = _call(library().attn_linear_fwd, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+               log_decay.data_ptr(), _ptr(state), _ptr(state_out), _ptr(state_index), n, B, Hq, Hkv, L, d,
+               _dtype_code(q), _strides_bhld(q), _strides_bhld(k), _strides_bhld(v), _strides_bhld(o),
+               float(scale or 0.0), _ptr(work), size)
+    _check(st, "attn_linear_fwd")
+    return o, state_out
+
+
+@_on_stream
+def attn_linear_fwd_varlen(q, k, v, cu_seqlens, max_seqlen, log_decay, state=None, state_out=True, state_index=None,
+                           scale=None, o=None, workspace=None):
+    """attn_linear_fwd of packed sequences: q [total,Hq,d], k/v [total,Hkv,d], cu_seqlens int32
+    [B+1] on the device, max_seqlen >= every length.  Rows behind the last sequence are not written."""
+    total, Hq, d = q.shape
+    _check_alike(q, k, v, 3)
+    Hkv = k.shape[1]
+    if k.shape[0] != total:
+        raise ValueError("k and v must be [total,Hkv,d]")
+    dev = q.device
+    _ints(dev, "cu_seqlens", cu_seqlens)
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens must be [B+1]")
+    B = cu_seqlens.shape[0] - 1
+    o = _like(q, o, "o")
+    state, state_out, n = _linear_states(log_decay, state, state_out, state_index, B, Hq, d, dev)
+    work, size = _linear_workspace(workspace, B, Hq, int(max_seqlen), d, dev)
+    st = _call(library().attn_linear_fwd_varlen, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+               cu_seqlens.data_ptr(), log_decay.data_ptr(), _ptr(state), _ptr(state_out), _ptr(state_index), n, B,
+               total, int(max_seqlen), Hq, Hkv, d, _dtype_code(q), _strides_thd(q), _strides_thd(k),
+               _strides_thd(v), _strides_thd(o), float(scale or 0.0), _ptr(work), size)
+    _check(st, "attn_linear_fwd_varlen")
+    return o, state_out
+
+
+@_on_stream
+def attn_linear_step(q, k, v, log_decay, state, state_index=None, scale=None, o=None):
+    """One token per sequence: q [B,Hq,d], k/v [B,Hkv,d]; ``state`` (fp32 [B,Hq,d,d], or a pool's rows
+    by state_index) is read and updated in place.  Returns o [B,Hq,d]."""
+    B, Hq, d = q.shape
+    _check_alike(q, k, v, 3)
+    Hkv = k.shape[1]
+    if k.shape[0] != B:
+        raise ValueError("k and v must be [B,Hkv,d]")
+    dev = q.device
+    o = _like(q, o, "o")
+    _, _, n = _linear_states(log_decay, state, state, state_index, B, Hq, d, dev)
+    st = _call(library().attn_linear_step, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+               log_decay.data_ptr(), state.data_ptr(), _ptr(state_index), n, B, Hq, Hkv, d, _dtype_code(q),
+               _step_strides(q), _step_strides(k), _step_strides(v), _step_strides(o), float(scale or 0.0))
+    _check(st, "attn_linear_step")
+    return o
+
+
+def _step_strides(t):
+    s = t.stride()
+    if s[2] != 1:
+        raise ValueError("innermost (head-dim) stride must be 1")
+    return _lib.attn_strides(s[0], s[1], 0)
 
 
 @_on_stream

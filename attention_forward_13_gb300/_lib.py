@@ -26,6 +26,11 @@ class attn_opts(ctypes.Structure):
                 ("scale_p", ctypes.c_float), ("scale_o", ctypes.c_float)]
 
 
+class attn_rope_opts(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("inverse", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
 STATUS = {0: "ATTN_OK", 1: "ATTN_ERR_INVALID", 2: "ATTN_ERR_UNSUPPORTED", 3: "ATTN_ERR_CUDA",
           4: "ATTN_ERR_TIMEOUT"}
 ATTN_F16, ATTN_BF16, ATTN_E4M3 = 0, 1, 2
@@ -35,7 +40,9 @@ EXPORTS = ("attn_fwd", "attn_fwd_varlen", "attn_fwd_paged", "attn_splitkv_combin
            "attn_last_kernel_name", "attn_device_error", "attn_selftest_timeout",
            "attn_fwd_paged_noalloc", "attn_paged_window_pages", "attn_dense_schedule",
            "attn_tree_mask", "attn_tree_workspace_bytes", "attn_fwd_paged_tree", "attn_cache_reorder",
-           "attn_cache_reserve", "attn_cache_accept", "attn_cache_compact", "attn_paged_keep_splits")
+           "attn_cache_reserve", "attn_cache_accept", "attn_cache_compact", "attn_paged_keep_splits",
+           "attn_cache_slots", "attn_rope_freqs", "attn_rope", "attn_cache_append",
+           "attn_linear_workspace_bytes", "attn_linear_fwd", "attn_linear_fwd_varlen", "attn_linear_step")
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
 _lock = threading.Lock()
@@ -75,6 +82,16 @@ def _declare(lib):
     lib.attn_cache_reserve.argtypes = [_P] * 10 + [_I] * 5 + [ctypes.c_int64, _P]
     lib.attn_cache_accept.argtypes = [_P] * 10 + [_I] * 7 + [ctypes.c_int64, _P]
     lib.attn_cache_compact.argtypes = [_P] * 9 + [_I] * 5 + [ctypes.c_int64, _P]
+    D, Z, R = ctypes.c_double, ctypes.c_size_t, ctypes.POINTER(attn_rope_opts)
+    lib.attn_cache_slots.argtypes = [_P] * 7 + [_I] * 5 + [_P]
+    lib.attn_rope_freqs.argtypes = [_I, D, _I, D, D, D, D, ctypes.POINTER(D)]
+    lib.attn_rope.argtypes = [_P] * 5 + [ctypes.c_int64] + [_I] * 6 + [S] * 4 + [R, _P]
+    lib.attn_cache_append.argtypes = [_P] * 8 + [_I] * 7 + [S] * 4 + [R, _P]
+    lib.attn_linear_workspace_bytes.argtypes = [_I] * 4
+    lib.attn_linear_workspace_bytes.restype = Z
+    lib.attn_linear_fwd.argtypes = [_P] * 8 + [_I] * 7 + [S] * 4 + [ctypes.c_float, _P, Z, _P]
+    lib.attn_linear_fwd_varlen.argtypes = [_P] * 9 + [_I] * 8 + [S] * 4 + [ctypes.c_float, _P, Z, _P]
+    lib.attn_linear_step.argtypes = [_P] * 7 + [_I] * 6 + [S] * 4 + [ctypes.c_float, _P]
     lib.attn_status_string.argtypes = [_I]
     lib.attn_status_string.restype = ctypes.c_char_p
     lib.attn_last_kernel_name.argtypes = []
@@ -84,7 +101,9 @@ def _declare(lib):
     for name in ("attn_fwd", "attn_fwd_varlen", "attn_fwd_paged", "attn_splitkv_combine",
                  "attn_device_error", "attn_selftest_timeout", "attn_fwd_paged_noalloc",
                  "attn_tree_mask", "attn_fwd_paged_tree", "attn_cache_reorder", "attn_cache_reserve",
-                 "attn_cache_accept", "attn_cache_compact"):
+                 "attn_cache_accept", "attn_cache_compact", "attn_cache_slots", "attn_rope_freqs",
+                 "attn_rope", "attn_cache_append", "attn_linear_fwd", "attn_linear_fwd_varlen",
+                 "attn_linear_step"):
         getattr(lib, name).restype = _I
 
 

@@ -1,7 +1,7 @@
 // cache.cu -- upkeep of a paged K/V cache on the device: forking and re-ordering
 // sequences, reserving pages for coming tokens (with copy-on-write of a shared
-// last page), keeping the accepted nodes of a draft tree, closing the holes of
-// the pool.  include/attn_fwd.h states the rules; all of them read and write
+// last page), the slots of those tokens, keeping the accepted nodes of a draft
+// tree, closing the holes of the pool.  include/attn_fwd.h states the rules; all of them read and write
 // lengths, tables and reference counts in device memory, so that a serving loop
 // needs no round trip to the host.
 //
@@ -626,6 +626,68 @@ __global__ void __launch_bounds__(128) compact_move_kernel(const CompactParams p
 }
 
 // ---------------------------------------------------------------------------
+// Slot map: where the new tokens of every sequence go, in packed order.  Latency
+// bound: one launch, each CTA sums the counts for itself (8192 of them: 16 rounds
+// of the block) and finds its tokens' sequences by bisection in shared memory.
+struct SlotsParams {
+  const int32_t *table, *seqlens, *add;
+  int32_t *slots, *positions, *cu, *sequence;
+  int B, N, max_pages, num_pages, page_log2;
+  unsigned int* err;
+};
+
+constexpr int kSlotTokens = 1024;  // tokens per CTA
+
+__global__ void __launch_bounds__(512) slots_kernel(const SlotsParams p) {
+  extern __shared__ int cu[];  // [B + 1], none above N
+  __shared__ long long scratch[32];
+  pdl_launch_dependents();
+  pdl_wait();
+  bool bad = false;
+  long long before = 0;
+  for (int b0 = 0; b0 < p.B; b0 += blockDim.x) {
+    const int b = b0 + threadIdx.x;
+    const int n = b < p.B ? p.add[b] : 0;
+    bad |= n < 0;
+    long long all;
+    const long long at = before + block_scan<long long>(max(n, 0), scratch, all);
+    if (b < p.B) cu[b] = static_cast<int>(min(at, static_cast<long long>(p.N)));
+    before += all;
+  }
+  if (threadIdx.x == 0) cu[p.B] = static_cast<int>(min(before, static_cast<long long>(p.N)));
+  __syncthreads();
+  if (blockIdx.x == 0) {
+    if (bad || (threadIdx.x == 0 && before > p.N)) report(p.err);
+    for (int b = threadIdx.x; b <= p.B; b += blockDim.x) p.cu[b] = cu[b];
+  }
+  const int total = cu[p.B];
+  const int t0 = blockIdx.x * kSlotTokens, t1 = min(p.N, t0 + kSlotTokens);
+  for (int t = t0 + threadIdx.x; t < t1; t += blockDim.x) {
+    int slot = -1, position = 0, b = -1;
+    if (t < total) {
+      int lo = 0, hi = p.B;  // cu[lo] <= t < cu[hi]
+      while (hi - lo > 1) {
+        const int m = (lo + hi) >> 1;
+        if (cu[m] <= t) lo = m;
+        else hi = m;
+      }
+      b = lo;
+      const long long pos = static_cast<long long>(p.seqlens[b]) - p.add[b] + (t - cu[b]);
+      if (pos >= 0 && (pos >> p.page_log2) < p.max_pages) {
+        position = static_cast<int>(pos);
+        const int page = p.table[static_cast<int64_t>(b) * p.max_pages + (position >> p.page_log2)];
+        if (page >= 0 && page < p.num_pages)
+          slot = (page << p.page_log2) + (position & ((1 << p.page_log2) - 1));
+      }
+      if (slot < 0) report(p.err);
+    }
+    p.slots[t] = slot;
+    p.positions[t] = position;
+    p.sequence[t] = b;
+  }
+}
+
+// ---------------------------------------------------------------------------
 bool page_size_ok(int s) { return s == 16 || s == 32 || s == 64 || s == 128 || s == 256; }
 int log2_of(int s) {
   int l = 0;
@@ -679,6 +741,7 @@ int table_ctas(int B, int max_pages, int least) {
 // Dynamic shared memory of a call over B sequences.
 constexpr size_t reorder_smem(int B) { return (kRange + static_cast<size_t>(B)) * 4; }  // accept's too
 constexpr size_t reserve_smem(int B) { return (5 * static_cast<size_t>(B) + 1) * 4; }
+constexpr size_t slots_smem(int B) { return (static_cast<size_t>(B) + 1) * 4; }
 
 }  // namespace
 
@@ -775,6 +838,24 @@ attn_status attn_cache_compact(void* k_pool, void* v_pool, const int32_t* block_
   if (e == cudaSuccess)
     e = launch_pdl(compact_move_kernel, dim3(8 * sms), 128, 0, s, p, q, chunks_of(q));
   return host_finish(e, "attn_cache_compact_plan+attn_cache_compact_move");
+}
+
+attn_status attn_cache_slots(const int32_t* block_table, const int32_t* seqlens, const int32_t* add, int32_t* slots,
+                             int32_t* positions, int32_t* cu_seqlens, int32_t* sequence, int B, int num_tokens,
+                             int max_pages, int num_pages, int page_size, void* stream) {
+  if (num_tokens < 0) return ATTN_ERR_INVALID;
+  attn_status st = check_cache(B, max_pages, num_pages, page_size, {cu_seqlens}, {block_table, seqlens, add});
+  if (st != ATTN_OK) return st;
+  for (const void* p : {slots, positions, sequence})
+    if (num_tokens > 0 && (p == nullptr || !host_aligned(p, 4))) return ATTN_ERR_INVALID;
+  SlotsParams p{block_table, seqlens, add, slots, positions, cu_seqlens, sequence, B, num_tokens,
+                max_pages, num_pages, log2_of(page_size), nullptr};
+  if (host_device_state(&p.err, nullptr) != ATTN_OK) return ATTN_ERR_CUDA;
+  if (num_tokens > 0x7fffffff - kSlotTokens) return ATTN_ERR_UNSUPPORTED;
+  const int grid = std::max(1, (num_tokens + kSlotTokens - 1) / kSlotTokens);
+  return host_finish(launch_pdl_upto<slots_kernel>(slots_smem(kMaxSeqs), dim3(grid), 512, slots_smem(B),
+                                                   static_cast<cudaStream_t>(stream), p),
+                     "attn_cache_slots");
 }
 
 }  // extern "C"

@@ -355,7 +355,7 @@ attn_status attn_dense_schedule(int B, int Hq, int Hkv, int Lq, int Lk, const at
  *   first ceil(seqlens[b] / page_size) entries of its row; and page_refs int32
  *   [num_pages]: how many table entries hold each page (more where something
  *   else, a prefix store say, holds it too); 0 marks a free page.
- * The four calls below take that state and write the next one to *_out buffers
+ * The first four calls below take that state and write the next one to *_out buffers
  * (table entries past the held ones are written as -1).  An output may not
  * overlap an input, except refs_out = page_refs in attn_cache_reorder and
  * attn_cache_accept.  Pools are [layers][num_pages][page_size][row]: the same
@@ -416,6 +416,125 @@ attn_status attn_cache_compact(void* k_pool, void* v_pool, const int32_t* block_
                                int32_t* refs_out, int32_t* page_map, int32_t* workspace, int B,
                                int max_pages, int num_pages, int page_size, int layers,
                                int64_t row_bytes, void* stream);
+
+/* attn_cache_slots -- the slot map of a ragged batch of new tokens.  seqlens[b] counts
+ * sequence b's last add[b] >= 0 tokens, whose pages are in its table row
+ * (attn_cache_reserve sees to both); packed in order of the sequences they are the
+ * rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of the layer's q, k and v.
+ *   cu_seqlens int32 [B + 1] (as attn_fwd_varlen takes them); of each of the
+ *   num_tokens rows sequence, positions (in the sequence, from 0) and slots
+ *   (physical page * page_size + row of the page) int32 [num_tokens].  Rows past
+ *   the last token get sequence -1, position 0, slot -1.
+ *   Tokens past num_tokens are left out (cu_seqlens stops at num_tokens), a count
+ *   below 0 counts as 0, a token before position 0, past the table row or in a page
+ *   outside [0, num_pages) gets slot -1: each sets the device error word's bit for
+ *   bad cache indices. */
+attn_status attn_cache_slots(const int32_t* block_table, const int32_t* seqlens, const int32_t* add, int32_t* slots,
+                             int32_t* positions, int32_t* cu_seqlens, int32_t* sequence, int B, int num_tokens,
+                             int max_pages, int num_pages, int page_size, void* stream);
+
+/*
+ * Rotary positions.  Elements 2i, 2i + 1 (interleaved) or i, i + rotary_dim / 2 of
+ * a head's first rotary_dim form pair i, which turns by a = position * inv_freq[i]:
+ *   (x, y) -> scale * (x cos a - y sin a, y cos a + x sin a),
+ * by -a with `inverse` (which undoes it, and with the same scale is also its
+ * gradient).  Elements from rotary_dim on are copied as they are.  Angles are
+ * exact to 2^-53 of inv_freq at any int32 position; negative ones turn back.
+ */
+typedef struct {
+  const double* inv_freq; /* device fp64 [rotary_dim / 2], radians per position */
+  int rotary_dim;         /* even, at most d; 0: no rotation */
+  int interleaved;
+  int inverse;
+  float scale;            /* factor on the rotated elements; 0 means 1 */
+} attn_rope_opts;
+
+/* attn_rope_freqs -- the frequencies base^(-2 i / rotary_dim), scaled for contexts longer
+ * than the original_len positions a model was trained on (host only, fp64):
+ *   ATTN_ROPE_LINEAR   all divided by factor (positions interpolated);
+ *   ATTN_ROPE_BASE     base grown by factor^(r / (r - 2)), so that the slowest pair is
+ *                      divided by factor and the fastest kept;
+ *   ATTN_ROPE_PARTS    pairs that make fast_turns or more turns in original_len kept, those
+ *                      of slow_turns or fewer divided by factor, between them a mean
+ *                      weighted linearly in the turns;
+ *   ATTN_ROPE_RAMP     the same with weights linear in the pair's index between the indices
+ *                      of fast_turns (rounded down) and slow_turns (rounded up).
+ * inv_freq: host [rotary_dim / 2].  A temperature that goes with a scaling (0.1 ln(factor) + 1,
+ * say) is the `scale` of attn_rope_opts. */
+typedef enum {
+  ATTN_ROPE_PLAIN = 0,
+  ATTN_ROPE_LINEAR = 1,
+  ATTN_ROPE_BASE = 2,
+  ATTN_ROPE_PARTS = 3,
+  ATTN_ROPE_RAMP = 4
+} attn_rope_scaling;
+attn_status attn_rope_freqs(int rotary_dim, double base, attn_rope_scaling scaling, double factor,
+                            double original_len, double slow_turns, double fast_turns, double* inv_freq);
+
+/* attn_rope -- rotates q [B][Hq][L][d] and k [B][Hkv][L][d] (any strides; packed rows are
+ * B = 1, L = rows) into q_out and k_out, which are the inputs themselves or do not
+ * overlap them.  Hq or Hkv may be 0 (its pointers are not used).  positions: device int32, that of row
+ * l of batch b at positions[b * positions_batch_stride + l] (stride 0: one vector for
+ * all), or NULL: l.  d a multiple of 8, at most 512; fp16 or bf16. */
+attn_status attn_rope(const void* q, void* q_out, const void* k, void* k_out, const int32_t* positions,
+                      int64_t positions_batch_stride, int B, int L, int Hq, int Hkv, int d, attn_dtype dtype,
+                      attn_strides sq, attn_strides sq_out, attn_strides sk, attn_strides sk_out,
+                      const attn_rope_opts* rope, void* stream);
+
+/* attn_cache_append -- writes the keys and values of packed new tokens (k, v [num_tokens][Hkv][d],
+ * head and row strides) into the pools [num_pages][page_size][Hkv][d]: token t's to row
+ * slots[t] % page_size of page slots[t] / page_size.  Slot -1: not written; any other slot
+ * outside the pool neither, and the device error word's bit for bad cache indices
+ * is set.  No slot may be named twice (of two such tokens either's 16-byte pieces may
+ * stay).  With `rope` (not inverse) k is rotated on the way, by positions [num_tokens], and so
+ * is q [num_tokens][Hq][d], every row of it, into q_out (q itself, or not overlapping it).
+ * rope NULL: no rotation; Hq = 0: no q.  d a multiple of 8, at most 512; fp16 or bf16. */
+attn_status attn_cache_append(const void* q, void* q_out, const void* k, const void* v, void* k_pool, void* v_pool,
+                              const int32_t* slots, const int32_t* positions, int num_tokens, int Hq, int Hkv, int d,
+                              attn_dtype dtype, int page_size, int num_pages, attn_strides sq, attn_strides sq_out,
+                              attn_strides sk, attn_strides sv, const attn_rope_opts* rope, void* stream);
+
+/*
+ * Linear attention with a decay per head.  With g = log_decay[h] <= 0 (device fp32
+ * [Hq], natural log; -inf keeps nothing), per sequence and query head, kv head h / (Hq / Hkv):
+ *   S_t = e^g S_(t-1) + k_t v_t^T  (a d x d matrix, rows k, columns v),  o_t = scale * q_t^T S_t.
+ * scale <= 0 selects 1 / sqrt(d).  d in {64, 128}, fp16 or bf16; states fp32
+ * [num_states][Hq][d][d] contiguous, 16-byte aligned.  state_in NULL: S before the first token is 0;
+ * state_out NULL: the last state is not kept; state_out = state_in: in place, else
+ * they do not overlap.  state_index: device int32 [B], the state of sequence b in
+ * both, or NULL: b.  Index -1: starts from 0 and is not kept (a padded row); any other outside
+ * [0, num_states), or one that an earlier sequence of the call has, is treated so too and
+ * sets the device error word's bit for bad cache indices.
+ * log_decay above 0 is allowed as long as nothing overflows: e^(128 g) and the results.
+ * NaN or infinity in a sequence's q, k, v or state may make all that sequence's outputs
+ * and its state NaN, and no other's; what lies behind a sequence's end may hold anything.
+ *
+ * attn_linear_fwd -- whole prompts or chunks, dense: q, o [B][Hq][L][d], k, v
+ * [B][Hkv][L][d].  attn_linear_fwd_varlen -- packed sequences, as attn_fwd_varlen: rows
+ * behind the last sequence are not written.  Sequences of no tokens hand
+ * their state on.
+ *   workspace: attn_linear_workspace_bytes() bytes (may be 0, then NULL will do),
+ *   16-byte aligned; nothing in it has to be set, and calls that may overlap on the GPU
+ *   each need one.  Results do not depend on what else runs.
+ */
+size_t attn_linear_workspace_bytes(int B, int Hq, int max_seqlen, int d);
+attn_status attn_linear_fwd(const void* q, const void* k, const void* v, void* o, const float* log_decay,
+                            const float* state_in, float* state_out, const int32_t* state_index, int num_states,
+                            int B, int Hq, int Hkv, int L, int d, attn_dtype dtype, attn_strides sq, attn_strides sk,
+                            attn_strides sv, attn_strides so, float scale, void* workspace, size_t workspace_bytes,
+                            void* stream);
+attn_status attn_linear_fwd_varlen(const void* q, const void* k, const void* v, void* o, const int32_t* cu_seqlens,
+                                   const float* log_decay, const float* state_in, float* state_out,
+                                   const int32_t* state_index, int num_states, int B, int total, int max_seqlen, int Hq,
+                                   int Hkv, int d, attn_dtype dtype, attn_strides sq, attn_strides sk, attn_strides sv,
+                                   attn_strides so, float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/* attn_linear_step -- one token per sequence: q, o [B][Hq][d], k, v [B][Hkv][d] (batch and head
+ * strides); `state` is read and written in place. */
+attn_status attn_linear_step(const void* q, const void* k, const void* v, void* o, const float* log_decay, float* state,
+                             const int32_t* state_index, int num_states, int B, int Hq, int Hkv, int d, attn_dtype dtype,
+                             attn_strides sq, attn_strides sk, attn_strides sv, attn_strides so, float scale,
+                             void* stream);
 
 /* Human-readable name of a status. */
 const char* attn_status_string(attn_status status);
