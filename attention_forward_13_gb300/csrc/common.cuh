@@ -46,6 +46,8 @@ enum ErrBits : uint32_t {
   kErrTreeTeardown = 23,
   kErrTreeBadParent = 24,
   kErrCacheBadIndex = 25,
+  kErrLinearWait = 26,
+  kErrLinearTeardown = 27,
 };
 
 // Element types of a prefill instantiation: fp16 / bf16 end to end, or e4m3

@@ -6,19 +6,44 @@
 
 namespace attn {
 
+constexpr int kLinearChunk = 128;  // tokens per chunk
+
 struct LinearParams {
-  const void *q, *k, *v;
+  CUtensorMap tm_q, tm_k, tm_v;  // 4-D (d, rows, heads, batch), box {64, 128, 1, 1}
   void* o;
   const float* log_decay;
   const float* state_in;   // [num_states][Hq][d][d] or nullptr: zeros
   float* state_out;        // likewise, or nullptr: not kept
   const int32_t* index;    // [B] rows of both, or nullptr: b
   const int32_t* cu;       // packed sequences: [B + 1]; nullptr: dense, L rows each
-  int num_states, Hq, group, L, total;
-  attn_strides sq, sk, sv, so;
+  float* work;             // [segs][B][Hq][d][d]: states of all segments but the last, then state_in
+  int num_states, B, Hq, group, L, total;
+  int segs, seg_chunks;    // pieces a sequence is cut into, chunks of each
+  int64_t o_batch, o_head, o_row;
   float scale;
   unsigned int* err;
+  uint64_t timeout_ns;
 };
+
+// Pieces along the sequence.  Heads and halves of 64 columns are a CTA each and walk
+// the chunks in order; where they leave SMs idle, the walk is cut into segments,
+// whose states are summed up first, in a launch of its own that reads k and v once
+// more (and takes about half the time a chunk).
+inline void linear_segments(int B, int Hq, int max_len, int d, int* segs, int* seg_chunks) {
+  const int64_t ctas = static_cast<int64_t>(B) * Hq * (d / 64);
+  const int chunks = max_len / kLinearChunk + (max_len % kLinearChunk != 0 ? 1 : 0);
+  int64_t n = ctas > 0 ? 152 / ctas : 1;
+  n = n < chunks / 2 ? n : chunks / 2;
+  n = n < 16 ? n : 16;
+  n = n > 1 ? n : 1;
+  const int per = chunks > 0 ? static_cast<int>((chunks + n - 1) / n) : 1;
+  *seg_chunks = per;
+  *segs = chunks > 0 ? (chunks + per - 1) / per : 1;
+}
+
+// The two launches (linear_d64.cu, linear_d128.cu).
+template <int D>
+cudaError_t launch_linear_d(const LinearParams& p, bool bf16, cudaStream_t stream);
 
 // The state of sequence b, -1 for none.  Every thread of the block calls it.  A
 // row that is out of range or an earlier sequence's is none, and an error.
@@ -36,7 +61,7 @@ __device__ __forceinline__ int state_of(const int32_t* index, int num_states, in
 
 // First row and length of sequence b, never past the packed tensors whatever
 // cu_seqlens holds.
-__device__ __forceinline__ void sequence_rows(const LinearParams& p, int b, int64_t& row0, int& len) {
+__device__ __forceinline__ void sequence_rows(const LinearParams& p, int b, int& row0, int& len) {
   row0 = 0;
   len = p.L;
   if (p.cu != nullptr) {

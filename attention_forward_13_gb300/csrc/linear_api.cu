@@ -12,6 +12,9 @@ using namespace attn;
 
 namespace {
 
+// Rows of one call: no sum of a row and a segment leaves 32 bits.
+constexpr int kLinearMaxRows = 1 << 30;
+
 template <bool BF16>
 __device__ __forceinline__ float to_float(uint16_t x) {
   if constexpr (BF16) return __uint_as_float(static_cast<uint32_t>(x) << 16);
@@ -108,52 +111,6 @@ cudaError_t launch_step(const StepParams& p, int B, bool bf16, cudaStream_t stre
 }
 
 // ---------------------------------------------------------------------------
-// Simple form of the chunked kernel: a thread walks the tokens with one column of the state.
-constexpr int kTile = 16;
-template <int D, bool BF16>
-__global__ void __launch_bounds__(32) linear_walk_kernel(const LinearParams p) {
-  __shared__ float sq[kTile][D], sk[kTile][D];
-  pdl_launch_dependents();
-  pdl_wait();
-  const int c = blockIdx.x * 32 + threadIdx.x, h = blockIdx.y, b = blockIdx.z, hk = h / p.group;
-  const int slot = state_of(p.index, p.num_states, b, p.err, blockIdx.x == 0 && h == 0);
-  int64_t row0;
-  int len;
-  sequence_rows(p, b, row0, len);
-  const int64_t at = (static_cast<int64_t>(slot) * p.Hq + h) * D * D + c;
-  float s[D];
-#pragma unroll
-  for (int r = 0; r < D; ++r) s[r] = p.state_in != nullptr && slot >= 0 ? p.state_in[at + r * D] : 0.0f;
-  const float decay = expf(p.log_decay[h]);
-  const uint16_t* q = static_cast<const uint16_t*>(p.q) + (p.cu ? 0 : b * p.sq.batch) + h * p.sq.head + row0 * p.sq.row;
-  const uint16_t* k = static_cast<const uint16_t*>(p.k) + (p.cu ? 0 : b * p.sk.batch) + hk * p.sk.head + row0 * p.sk.row;
-  const uint16_t* v = static_cast<const uint16_t*>(p.v) + (p.cu ? 0 : b * p.sv.batch) + hk * p.sv.head + row0 * p.sv.row;
-  uint16_t* o = static_cast<uint16_t*>(p.o) + (p.cu ? 0 : b * p.so.batch) + h * p.so.head + row0 * p.so.row;
-  for (int t0 = 0; t0 < len; t0 += kTile) {
-    const int n = min(kTile, len - t0);
-    __syncwarp();
-    for (int i = threadIdx.x; i < n * D; i += 32) {
-      const int t = i / D, e = i % D;
-      sq[t][e] = to_float<BF16>(q[(t0 + t) * p.sq.row + e]);
-      sk[t][e] = to_float<BF16>(k[(t0 + t) * p.sk.row + e]);
-    }
-    __syncwarp();
-    for (int t = 0; t < n; ++t) {
-      const float x = to_float<BF16>(v[(t0 + t) * p.sv.row + c]);
-      float a = 0.0f;
-#pragma unroll
-      for (int r = 0; r < D; ++r) {
-        s[r] = fmaf(sk[t][r], x, s[r] * decay);
-        a = fmaf(sq[t][r], s[r], a);
-      }
-      o[(t0 + t) * p.so.row + c] = from_float<BF16>(a * p.scale);
-    }
-  }
-  if (p.state_out != nullptr && slot >= 0)
-#pragma unroll
-    for (int r = 0; r < D; ++r) p.state_out[at + r * D] = s[r];
-}
-
 bool strides_ok(const attn_strides& s, bool row, bool batch) {
   return s.head > 0 && s.head % 8 == 0 && (!row || (s.row > 0 && s.row % 8 == 0)) &&
          (!batch || (s.batch > 0 && s.batch % 8 == 0));
@@ -175,24 +132,68 @@ attn_status check_common(const float* log_decay, const float* state_in, const fl
   return ATTN_OK;
 }
 
-attn_status launch_fwd(LinearParams& p, int B, int max_len, int d, bool bf16, cudaStream_t stream) {
+// Everything of a call of the chunked kernels that the dense and the packed form share:
+// rows of a tensor (per batch), batches, the longest sequence.
+attn_status linear_fwd(const void* q, const void* k, const void* v, void* o, const int32_t* cu, const float* log_decay,
+                       const float* state_in, float* state_out, const int32_t* index, int num_states, int B, int rows,
+                       int max_len, int Hq, int Hkv, int d, bool bf16, attn_strides sq, attn_strides sk,
+                       attn_strides sv, attn_strides so, float scale, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  LinearParams p{};
+  if (rows > 0) {
+    for (const void* x : {q, k, v, static_cast<const void*>(o)})
+      if (x == nullptr || !host_aligned(x, 16)) return ATTN_ERR_INVALID;
+    const bool batches = cu == nullptr && B > 1;
+    for (const attn_strides* s : {&sq, &sk, &sv, &so})
+      if (!strides_ok(*s, true, batches)) return ATTN_ERR_INVALID;
+    const uint32_t box[4] = {64, kLinearChunk, 1, 1};
+    auto map = [&](CUtensorMap* m, const void* base, const attn_strides& s, int heads) {
+      const uint64_t dims[4] = {(uint64_t)d, (uint64_t)rows, (uint64_t)heads, cu != nullptr ? 1u : (uint64_t)B};
+      const uint64_t st[3] = {(uint64_t)s.row * 2, (uint64_t)s.head * 2,
+                              batches ? (uint64_t)s.batch * 2 : (uint64_t)s.head * 2};
+      return host_make_map(m, base, bf16, 4, dims, st, box);
+    };
+    if (!map(&p.tm_q, q, sq, Hq) || !map(&p.tm_k, k, sk, Hkv) || !map(&p.tm_v, v, sv, Hkv)) return ATTN_ERR_INVALID;
+  }
+  linear_segments(B, Hq, max_len, d, &p.segs, &p.seg_chunks);
+  if (attn_linear_workspace_bytes(B, Hq, max_len, d) > 0 &&
+      (workspace == nullptr || !host_aligned(workspace, 16) ||
+       workspace_bytes < attn_linear_workspace_bytes(B, Hq, max_len, d)))
+    return ATTN_ERR_INVALID;
+  p.o = o;
+  p.cu = cu;
+  p.log_decay = log_decay;
+  p.state_in = state_in;
+  p.state_out = state_out;
+  p.index = index;
+  p.work = static_cast<float*>(workspace);
+  p.num_states = num_states;
+  p.B = B;
+  p.Hq = Hq;
+  p.group = Hq / Hkv;
+  p.L = rows;
+  p.total = rows;
+  p.o_batch = so.batch;
+  p.o_head = so.head;
+  p.o_row = so.row;
+  p.scale = scale > 0.0f ? scale : 1.0f / sqrtf(static_cast<float>(d));
+  p.timeout_ns = host_timeout_ns();
   if (host_device_state(&p.err, nullptr) != ATTN_OK) return ATTN_ERR_CUDA;
-  const dim3 grid(d / 32, p.Hq, B);
-  cudaError_t e;
-  if (d == 64)
-    e = bf16 ? launch_pdl(linear_walk_kernel<64, true>, grid, 32, 0, stream, p)
-             : launch_pdl(linear_walk_kernel<64, false>, grid, 32, 0, stream, p);
-  else
-    e = bf16 ? launch_pdl(linear_walk_kernel<128, true>, grid, 32, 0, stream, p)
-             : launch_pdl(linear_walk_kernel<128, false>, grid, 32, 0, stream, p);
-  return host_finish(e, "attn_linear_fwd");
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return host_finish(d == 64 ? launch_linear_d<64>(p, bf16, s) : launch_linear_d<128>(p, bf16, s),
+                     p.segs > 1 ? "attn_linear_chunk_states+attn_linear_chunk" : "attn_linear_chunk");
 }
 
 }  // namespace
 
 extern "C" {
 
-size_t attn_linear_workspace_bytes(int B, int Hq, int max_seqlen, int d) { return 0; }
+size_t attn_linear_workspace_bytes(int B, int Hq, int max_seqlen, int d) {
+  if (B <= 0 || Hq <= 0 || max_seqlen <= 0 || (d != 64 && d != 128)) return 0;
+  int segs, chunks;
+  linear_segments(B, Hq, max_seqlen, d, &segs, &chunks);
+  return segs > 1 ? static_cast<size_t>(segs) * B * Hq * d * d * sizeof(float) : 0;
+}
 
 attn_status attn_linear_fwd(const void* q, const void* k, const void* v, void* o, const float* log_decay,
                             const float* state_in, float* state_out, const int32_t* state_index, int num_states,
@@ -203,20 +204,9 @@ attn_status attn_linear_fwd(const void* q, const void* k, const void* v, void* o
   const attn_status st =
       check_common(log_decay, state_in, state_out, state_index, num_states, B, Hq, Hkv, d, dtype, scale);
   if (st != ATTN_OK || B == 0) return st;
-  if (L > 0) {
-    for (const void* x : {q, k, v, static_cast<const void*>(o)})
-      if (x == nullptr || !host_aligned(x, 16)) return ATTN_ERR_INVALID;
-    for (const attn_strides* s : {&sq, &sk, &sv, &so})
-      if (!strides_ok(*s, true, B > 1)) return ATTN_ERR_INVALID;
-  }
-  LinearParams p{};
-  p.q = q, p.k = k, p.v = v, p.o = o;
-  p.log_decay = log_decay;
-  p.state_in = state_in, p.state_out = state_out, p.index = state_index, p.num_states = num_states;
-  p.Hq = Hq, p.group = Hq / Hkv, p.L = L;
-  p.sq = sq, p.sk = sk, p.sv = sv, p.so = so;
-  p.scale = scale > 0.0f ? scale : 1.0f / sqrtf(static_cast<float>(d));
-  return launch_fwd(p, B, L, d, dtype == ATTN_BF16, static_cast<cudaStream_t>(stream));
+  if (L > kLinearMaxRows) return ATTN_ERR_UNSUPPORTED;
+  return linear_fwd(q, k, v, o, nullptr, log_decay, state_in, state_out, state_index, num_states, B, L, L, Hq, Hkv, d,
+                    dtype == ATTN_BF16, sq, sk, sv, so, scale, workspace, workspace_bytes, stream);
 }
 
 attn_status attn_linear_fwd_varlen(const void* q, const void* k, const void* v, void* o, const int32_t* cu_seqlens,
@@ -229,21 +219,9 @@ attn_status attn_linear_fwd_varlen(const void* q, const void* k, const void* v, 
       check_common(log_decay, state_in, state_out, state_index, num_states, B, Hq, Hkv, d, dtype, scale);
   if (st != ATTN_OK || B == 0) return st;
   if (cu_seqlens == nullptr || !host_aligned(cu_seqlens, 4)) return ATTN_ERR_INVALID;
-  if (total > 0) {
-    for (const void* x : {q, k, v, static_cast<const void*>(o)})
-      if (x == nullptr || !host_aligned(x, 16)) return ATTN_ERR_INVALID;
-    for (const attn_strides* s : {&sq, &sk, &sv, &so})
-      if (!strides_ok(*s, true, false)) return ATTN_ERR_INVALID;
-  }
-  LinearParams p{};
-  p.q = q, p.k = k, p.v = v, p.o = o;
-  p.cu = cu_seqlens, p.total = total;
-  p.log_decay = log_decay;
-  p.state_in = state_in, p.state_out = state_out, p.index = state_index, p.num_states = num_states;
-  p.Hq = Hq, p.group = Hq / Hkv, p.L = max_seqlen;
-  p.sq = sq, p.sk = sk, p.sv = sv, p.so = so;
-  p.scale = scale > 0.0f ? scale : 1.0f / sqrtf(static_cast<float>(d));
-  return launch_fwd(p, B, max_seqlen, d, dtype == ATTN_BF16, static_cast<cudaStream_t>(stream));
+  if (total > kLinearMaxRows || max_seqlen > kLinearMaxRows) return ATTN_ERR_UNSUPPORTED;
+  return linear_fwd(q, k, v, o, cu_seqlens, log_decay, state_in, state_out, state_index, num_states, B, total, max_seqlen,
+                    Hq, Hkv, d, dtype == ATTN_BF16, sq, sk, sv, so, scale, workspace, workspace_bytes, stream);
 }
 
 attn_status attn_linear_step(const void* q, const void* k, const void* v, void* o, const float* log_decay, float* state,

@@ -498,7 +498,7 @@ attn_status attn_cache_append(const void* q, void* q_out, const void* k, const v
  * Linear attention with a decay per head.  With g = log_decay[h] <= 0 (device fp32
  * [Hq], natural log; -inf keeps nothing), per sequence and query head, kv head h / (Hq / Hkv):
  *   S_t = e^g S_(t-1) + k_t v_t^T  (a d x d matrix, rows k, columns v),  o_t = scale * q_t^T S_t.
- * scale <= 0 selects 1 / sqrt(d).  d in {64, 128}, fp16 or bf16; states fp32
+ * scale <= 0 selects 1 / sqrt(d).  d in {64, 128}, fp16 or bf16, at most 2^30 rows; states fp32
  * [num_states][Hq][d][d] contiguous, 16-byte aligned.  state_in NULL: S before the first token is 0;
  * state_out NULL: the last state is not kept; state_out = state_in: in place, else
  * they do not overlap.  state_index: device int32 [B], the state of sequence b in
