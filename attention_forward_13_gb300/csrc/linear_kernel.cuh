@@ -67,7 +67,8 @@ struct LinearSmem {
   alignas(1024) uint4 ostage[4][32 * 8];
   float row_scale[2][128];  // fp16: what the rows of P were divided by
   float state_scale[4];     // and the state (read up to two chunks late)
-  float pw[64];             // [31 + n]: w^n for n >= 0
+  float pw[64];             // [31 + n]: w^n for n >= 0, else 0
+  float col[32];            // [j]: w^(31 - j)
   uint64_t qk_full[2], qk_empty[2], v_full[2], v_empty[2];
   uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
   uint64_t sb_full, sb_empty, kv_done, vp_full, teardown;
@@ -155,6 +156,7 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
   const int chunks = (t1 - t0 + C::C - 1) / C::C;
   const float log2w = p.log_decay[h] * kLog2e;
   if (tid < 64) sm.pw[tid] = tid < 31 ? 0.0f : decay_pow(log2w, tid - 31);
+  else if (tid < 96) sm.col[tid - 64] = decay_pow(log2w, 95 - tid);
   if (warp == C::W_MMA) {
     tmem_alloc(&sm.tmem_base, C::TM_COLS);
     tmem_relinquish();
@@ -276,68 +278,75 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
     // ===================== weights: P_ij = scale w^(i-j) q_i . k_j ==============
     if constexpr (!STATES) {
       const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-      // Full blocks of 32 columns left of the diagonal one: w^(i-j) is this row's
-      // power down to the block's last column times the column's from there.
-      float rowf[3];
-#pragma unroll
-      for (int i = 0; i < 3; ++i) rowf[i] = p.scale * decay_pow(log2w, lane + 1 + 32 * i);
       bool ok = true;
       for (int n = 0; ok && n < chunks; ++n) {
         ok = __all_sync(0xffffffffu, w.wait(&sm.s_full[n & 1], (n >> 1) & 1, kErrLinearWait));
         if (!ok) break;
         tc_fence_after();
         const uint32_t base = tmem + C::tm_s(n & 1) + lanes;
-        float fitted = 1.0f;
+        float f = p.scale;
         if constexpr (!BF16) {
           // fp16: the row's largest score decides a power of two that fits its weights (at
           // most 2^11: room for decays a little above 1, and 2^35 below for the small).
           float m = 0.0f;
-#pragma unroll
-          for (int cb = 0; cb < 4; ++cb) {
-            if (cb > warp) continue;
+#pragma unroll 1
+          for (int cb = 0; cb <= warp; ++cb) {
             uint32_t r[32];
             tmem_ld32(base + 32 * cb, r);
             tmem_ld_wait();
             reg_fence(r);
+            const int seen = cb < warp ? 31 : lane;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float x = fabsf(__uint_as_float(r[j]));
-              m = fmaxf(m, cb < warp || j <= lane ? x : 0.0f);
-            }
+            for (int j = 0; j < 32; ++j) m = fmaxf(m, j <= seen ? fabsf(__uint_as_float(r[j])) : 0.0f);
           }
-          float up;
-          fit(m * p.scale, 11, up, fitted);
+          float up, down;
+          fit(m * p.scale, 11, up, down);
           sm.row_scale[n & 1][tid] = up;
+          f *= down;
         }
+        uint32_t pk[16];
+        // Blocks of 32 columns left of the diagonal one: w^(i-j) is the row's power down to
+        // the block's last column times the column's from there.  (From the left: a block's
+        // weights go where the one before it was read.)
+#pragma unroll 1
+        for (int cb = 0; cb < warp; ++cb) {
+          uint32_t r[32];
+          tmem_ld32(base + 32 * cb, r);
+          tmem_ld_wait();
+          reg_fence(r);
+          const float rowf = f * exp2f(log2w * (lane + 1 + 32 * (warp - 1 - cb)));
+          const uint64_t f2 = f2_pack(rowf, rowf);
 #pragma unroll
-        for (int cb = 0; cb < 4; ++cb) {
-          uint32_t pk[16];
-          if (cb > warp) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) pk[j] = 0u;
-          } else {
-            uint32_t r[32];
-            tmem_ld32(base + 32 * cb, r);
-            tmem_ld_wait();
-            reg_fence(r);
-            if (cb < warp) {
-              const int back = warp - cb - 1;
-              const float f = (back == 0 ? rowf[0] : back == 1 ? rowf[1] : rowf[2]) * fitted;
-#pragma unroll
-              for (int j = 0; j < 32; j += 2)  // w^(31 - j)
-                pk[j / 2] = pack16<BF16>(__uint_as_float(r[j]) * (f * sm.pw[62 - j]),
-                                         __uint_as_float(r[j + 1]) * (f * sm.pw[61 - j]));
-            } else {
-              const float f = p.scale * fitted;
-#pragma unroll
-              for (int j = 0; j < 32; j += 2) {
-                const float a = __uint_as_float(r[j]) * (f * sm.pw[31 + lane - j]);
-                const float c = __uint_as_float(r[j + 1]) * (f * sm.pw[30 + lane - j]);
-                pk[j / 2] = pack16<BF16>(j <= lane ? a : 0.0f, j + 1 <= lane ? c : 0.0f);
-              }
-            }
+          for (int j = 0; j < 32; j += 4) {
+            const float4 c = *reinterpret_cast<const float4*>(&sm.col[j]);
+            float x0, x1, x2, x3;
+            f2_unpack(f2_mul(f2_mul(f2_pack(c.x, c.y), f2), f2_pack(__uint_as_float(r[j]), __uint_as_float(r[j + 1]))),
+                      x0, x1);
+            f2_unpack(f2_mul(f2_mul(f2_pack(c.z, c.w), f2), f2_pack(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]))),
+                      x2, x3);
+            pk[j / 2] = pack16<BF16>(x0, x1);
+            pk[j / 2 + 1] = pack16<BF16>(x2, x3);
           }
           tmem_st16(base + 16 * cb, pk);
+        }
+        {
+          uint32_t r[32];
+          tmem_ld32(base + 32 * warp, r);
+          tmem_ld_wait();
+          reg_fence(r);
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            const float a = __uint_as_float(r[j]) * (f * sm.pw[31 + lane - j]);
+            const float c = __uint_as_float(r[j + 1]) * (f * sm.pw[30 + lane - j]);
+            pk[j / 2] = pack16<BF16>(j <= lane ? a : 0.0f, j + 1 <= lane ? c : 0.0f);
+          }
+          tmem_st16(base + 16 * warp, pk);
+        }
+        if (warp < 3) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) pk[j] = 0u;
+#pragma unroll 1
+          for (int cb = warp + 1; cb < 4; ++cb) tmem_st16(base + 16 * cb, pk);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -384,51 +393,61 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
       }
     }
     bool ok = true;
-    auto load = [&](uint64_t* bar, int phase) {  // S from tensor memory
+    // Waits until the products so far are in S.
+    auto reach = [&](uint64_t* bar, int phase) {
       ok = __all_sync(0xffffffffu, w.wait(bar, phase & 1, kErrLinearWait));
-      if (!ok || !mine) return;
       tc_fence_after();
-      uint32_t a[32], c[32];
-      tmem_ld32(at, a);
-      tmem_ld32(at + 32, c);
-      tmem_ld_wait();
-      reg_fence(a);
-      reg_fence(c);
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        s[i] = __uint_as_float(a[i]);
-        s[32 + i] = __uint_as_float(c[i]);
-      }
     };
-    auto store = [&](float f) {  // S times f into tensor memory
-      if (mine) {
+    auto start = [&](float f) {  // S times f into tensor memory
+      if (!mine) return;
 #pragma unroll
-        for (int i = 0; i < 64; i += 32) {
-          uint32_t a[32];
+      for (int i = 0; i < 64; i += 32) {
+        uint32_t a[32];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) a[j] = __float_as_uint(s[i + j] * f);
-          tmem_st32(at + i, a);
-        }
-        tmem_st_wait();
+        for (int j = 0; j < 32; ++j) a[j] = __float_as_uint(s[i + j] * f);
+        tmem_st32(at + i, a);
       }
-      tc_fence_before();
+      tmem_st_wait();
+    };
+    auto finish = [&](float* to) {
+      if (!mine) return;
+#pragma unroll 1
+      for (int i = 0; i < 64; i += 32) {
+        uint32_t a[32];
+        tmem_ld32(at + i, a);
+        tmem_ld_wait();
+        reg_fence(a);
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) *reinterpret_cast<uint4*>(to + i + j) = make_uint4(a[j], a[j + 1], a[j + 2], a[j + 3]);
+      }
     };
     if constexpr (STATES) {
-      store(decay_pow(log2w, t1 - t0));
+      start(decay_pow(log2w, t1 - t0));
+      tc_fence_before();
       mbar_arrive(&sm.sb_full);
-      load(&sm.o_full[0], 0);
-      if (ok && mine) put(p.work + seg * work_seg + work_at + r * D);
+      reach(&sm.o_full[0], 0);
+      if (ok) finish(p.work + seg * work_seg + work_at + r * D);
     } else {
+      start(1.0f);
       const float full = decay_pow(log2w, C::C);
+      uint8_t* row = sm.sb + r * 128;
       for (int n = 0; ok && n < chunks; ++n) {
-        if (n > 0) load(&sm.kv_done, n - 1);
+        if (n > 0) reach(&sm.kv_done, n - 1);
         float down = 1.0f;
         if constexpr (!BF16) {
           // fp16: one power of two for the whole operand, its largest element below 2^15.
           float m = 0.0f;
-          if (mine)
+          if (mine) {
+#pragma unroll 1
+            for (int i = 0; i < 64; i += 32) {
+              uint32_t a[32];
+              tmem_ld32(at + i, a);
+              tmem_ld_wait();
+              reg_fence(a);
 #pragma unroll
-            for (int i = 0; i < 64; ++i) m = fmaxf(m, fabsf(s[i]));
+              for (int j = 0; j < 32; ++j) m = fmaxf(m, fabsf(__uint_as_float(a[j])));
+            }
+          }
           const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
           if (lane == 0) sm.part[wq] = top;
           // (Every thread comes here, aborted or not, and all leave together.)
@@ -441,23 +460,38 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
         if (ok && n > 0) ok = __all_sync(0xffffffffu, w.wait(&sm.sb_empty, (n - 1) & 1, kErrLinearWait));
         if constexpr (!BF16) ok = !named_bar_or(1, 128, !ok);  // (also: sm.part has been read)
         if (!ok) break;
-        if (mine) {
-          uint8_t* row = sm.sb + r * 128;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            uint32_t x[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] = pack16<BF16>(s[8 * i + 2 * j] * down, s[8 * i + 2 * j + 1] * down);
-            *reinterpret_cast<uint4*>(row + ((i ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
-          }
-        }
         const int m = t1 - t0 - n * C::C;
-        store(m >= C::C ? full : decay_pow(log2w, m));
+        const float f = m >= C::C ? full : decay_pow(log2w, m);
+        if (mine) {
+#pragma unroll 1
+          for (int i = 0; i < 64; i += 32) {
+            uint32_t a[32];
+            tmem_ld32(at + i, a);
+            tmem_ld_wait();
+            reg_fence(a);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t x[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float lo = __uint_as_float(a[8 * j + 2 * e]), hi = __uint_as_float(a[8 * j + 2 * e + 1]);
+                if constexpr (!BF16) lo *= down, hi *= down;
+                x[e] = pack16<BF16>(lo, hi);
+              }
+              *reinterpret_cast<uint4*>(row + (((i / 8 + j) ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) a[j] = __float_as_uint(__uint_as_float(a[j]) * f);
+            tmem_st32(at + i, a);
+          }
+          tmem_st_wait();
+        }
+        tc_fence_before();
         fence_proxy_async_smem();
         mbar_arrive(&sm.sb_full);
       }
-      if (ok && last && chunks > 0) load(&sm.kv_done, chunks - 1);
-      if (ok && last && mine && p.state_out != nullptr && slot >= 0) put(p.state_out + state_at);
+      if (ok && last && chunks > 0) reach(&sm.kv_done, chunks - 1);
+      if (ok && last && p.state_out != nullptr && slot >= 0) finish(p.state_out + state_at);
     }
   } else if (warp < 12) {
     // ===================== values and output =====================================
@@ -483,7 +517,7 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
                       : r < live              ? decay_pow(log2w, (STATES ? left : live) - 1 - r)
                                               : 0.0f;
       uint8_t* src = sm.v[st] + r * 128;
-#pragma unroll
+#pragma unroll 2
       for (int i = 0; i < 8; ++i) {
         const int at = (i ^ (r & 7)) << 4;
         const uint4 x = *reinterpret_cast<const uint4*>(src + at);
@@ -507,7 +541,7 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
         ok = __all_sync(0xffffffffu, w.wait(&sm.qk_full[st], (n >> 1) & 1, kErrLinearWait));
         if (!ok) return;
         if (r >= live) {
-#pragma unroll
+#pragma unroll 1
           for (int i = 0; i < 8; ++i) {
             *reinterpret_cast<uint4*>(src + i * 16) = make_uint4(0, 0, 0, 0);
 #pragma unroll
@@ -528,8 +562,7 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
         fi = sm.row_scale[n & 1][r];
         fs *= sm.state_scale[n & 3];
       }
-      uint32_t pk[32];
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < 64; c += 32) {
         uint32_t a[32], x[32];
         tmem_ld32(tmem + C::tm_pv(n & 1) + lanes + c, a);
@@ -537,19 +570,28 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
         tmem_ld_wait();
         reg_fence(a);
         reg_fence(x);
+        const uint64_t fs2 = f2_pack(fs, fs);
 #pragma unroll
-        for (int j = 0; j < 32; j += 2)
-          pk[(c + j) / 2] = pack16<BF16>(fmaf(__uint_as_float(x[j]), fs, __uint_as_float(a[j]) * fi),
-                                         fmaf(__uint_as_float(x[j + 1]), fs, __uint_as_float(a[j + 1]) * fi));
+        for (int i = 0; i < 4; ++i) {
+          uint32_t pk[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = 8 * i + 2 * e;
+            uint64_t o2 = f2_pack(__uint_as_float(a[j]), __uint_as_float(a[j + 1]));
+            if constexpr (!BF16) o2 = f2_mul(o2, f2_pack(fi, fi));
+            o2 = f2_fma(f2_pack(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), fs2, o2);
+            float lo, hi;
+            f2_unpack(o2, lo, hi);
+            pk[e] = pack16<BF16>(lo, hi);
+          }
+          stage[lane * 8 + ((c / 8 + i) ^ (lane & 7))] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+        }
       }
       tc_fence_before();
       mbar_arrive(&sm.o_empty[n & 1]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        stage[lane * 8 + (i ^ (lane & 7))] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
       __syncwarp();
       const int first = t0 + n * C::C;
-#pragma unroll
+#pragma unroll 4
       for (int i = 0; i < 8; ++i) {
         const int rw = 4 * i + (lane >> 3), q = lane & 7, t = first + wq * 32 + rw;
         if (t < t1)
