@@ -10,6 +10,7 @@ constexpr int kLinearChunk = 128;  // tokens per chunk
 
 struct LinearParams {
   CUtensorMap tm_q, tm_k, tm_v;  // 4-D (d, rows, heads, batch), box {64, 128, 1, 1}
+  CUtensorMap tm_o;              // the same with box {32, 32, 1, 1} and 64-byte swizzle
   void* o;
   const float* log_decay;
   const float* state_in;   // [num_states][Hq][d][d] or nullptr: zeros

@@ -146,14 +146,17 @@ attn_status linear_fwd(const void* q, const void* k, const void* v, void* o, con
     const bool batches = cu == nullptr && B > 1;
     for (const attn_strides* s : {&sq, &sk, &sv, &so})
       if (!strides_ok(*s, true, batches)) return ATTN_ERR_INVALID;
-    const uint32_t box[4] = {64, kLinearChunk, 1, 1};
-    auto map = [&](CUtensorMap* m, const void* base, const attn_strides& s, int heads) {
+    const uint32_t box[4] = {64, kLinearChunk, 1, 1}, obox[4] = {32, 32, 1, 1};
+    auto map = [&](CUtensorMap* m, const void* base, const attn_strides& s, int heads, bool out) {
       const uint64_t dims[4] = {(uint64_t)d, (uint64_t)rows, (uint64_t)heads, cu != nullptr ? 1u : (uint64_t)B};
       const uint64_t st[3] = {(uint64_t)s.row * 2, (uint64_t)s.head * 2,
                               batches ? (uint64_t)s.batch * 2 : (uint64_t)s.head * 2};
-      return host_make_map(m, base, bf16, 4, dims, st, box);
+      return host_make_map(m, base, bf16, 4, dims, st, out ? obox : box,
+                           out ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
     };
-    if (!map(&p.tm_q, q, sq, Hq) || !map(&p.tm_k, k, sk, Hkv) || !map(&p.tm_v, v, sv, Hkv)) return ATTN_ERR_INVALID;
+    if (!map(&p.tm_q, q, sq, Hq, false) || !map(&p.tm_k, k, sk, Hkv, false) || !map(&p.tm_v, v, sv, Hkv, false) ||
+        !map(&p.tm_o, o, so, Hq, true))
+      return ATTN_ERR_INVALID;
   }
   linear_segments(B, Hq, max_len, d, &p.segs, &p.seg_chunks);
   if (attn_linear_workspace_bytes(B, Hq, max_len, d) > 0 &&

@@ -22,7 +22,8 @@
 //            tensor memory over the columns it came from.
 //   two warps issue loads and products.
 // V has three stages, as V' is wanted early and P V comes late in a chunk; o is staged in
-// the stage it leaves.  Each role's loop is kept short, in rolled pieces of 32 columns:
+// the stage it leaves and goes out by tensor stores (straight from registers, 16 or 32 bytes
+// a row: 137 and 124 us).  Each role's loop is kept short, in rolled pieces of 32 columns:
 // unrolled throughout, the roles' code pushed each other out of the instruction caches
 // (2 x 8192 x 32 heads: 283 us against 126).
 //
@@ -56,11 +57,11 @@ struct LinearCfg {
   static constexpr int W_TMA = 16, W_MMA = 17;
   static constexpr int NV = 3;                    // stages of V
   // Tensor memory: chunk n's Q K^T at 128 (n & 1), P in the first 16 of every 32 columns
-  // of it, Q S at 256 + 64 (n & 1), P V at 384, the state at 448.
+  // of it, Q S at 256, P V at 320, the state in two parts at 384 (what the second
+  // piece of V' adds is kept apart, so that one product of 128 columns reads K once).
   static constexpr uint32_t TM_COLS = 512;
   __device__ static constexpr uint32_t tm_s(int b) { return 128u * b; }
-  __device__ static constexpr uint32_t tm_qs(int b) { return 256u + 64u * b; }
-  static constexpr uint32_t TM_PV = 384, TM_STATE = 448;
+  static constexpr uint32_t TM_QS = 256, TM_PV = 320, TM_STATE = 384, TM_STATE2 = 448;
 };
 
 template <int D>
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
     }
     for (int i = 0; i < C::NV; ++i) {
       mbar_init(&sm.v_full[i], 1);
-      mbar_init(&sm.v_empty[i], STATES ? 1 : 256);
+      mbar_init(&sm.v_empty[i], STATES ? 1 : 8);
     }
     mbar_init(&sm.o_full, 1);
     mbar_init(&sm.o_empty, 256);
@@ -205,7 +206,7 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
     const uint32_t lead = elect_one() ? 1u : 0u;
     constexpr uint32_t id_s = idesc_f16_f32(BF16, 128, 128, false, false);
     constexpr uint32_t id_pv = idesc_f16_f32(BF16, 128, 64, false, true);
-    constexpr uint32_t id_kv = idesc_f16_f32(BF16, 128, 64, true, true);
+    constexpr uint32_t id_kv = idesc_f16_f32(BF16, 128, 128, true, true);
     const uint64_t qd0 = sdesc_sw128(smem_u32(sm.q[0]), 16, 1024), kd0 = sdesc_sw128(smem_u32(sm.k[0]), 16, 1024);
     // d = 64: the second 64 rows of K^T re-read the first (leading offset 0), and rows
     // 64 .. 127 of S are ignored.
@@ -240,17 +241,20 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
       for (int i = 0; i < C::C / 16; ++i) {
         const uint64_t ka = ktd0 + static_cast<uint64_t>(s * (C::TILE >> 4) + ((i * 16 * 128) >> 4));
         umma_ss_warp(tmem + C::TM_STATE, ka, vpd0 + ((i * 16 * 128) >> 4), id_kv, 1u, lead);
-        umma_ss_warp(tmem + C::TM_STATE, ka, vpd0 + ((C::ATOM + i * 16 * 128) >> 4), id_kv, 1u, lead);
       }
       umma_commit_warp(&sm.kv_done, lead);
       if constexpr (STATES) {
         umma_commit_warp(&sm.qk_empty[s], lead);
         umma_commit_warp(&sm.v_empty[n % C::NV], lead);
       } else {
-        // Q S (its columns were read before the P V of the chunk before was issued)
+        // Q S, once the o of the chunk before has been read
+        if (n > 0) {
+          if (!(ok = w.wait(&sm.o_empty, (n - 1) & 1, kErrLinearWait))) break;
+          tc_fence_after();
+        }
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
-          umma_ss_warp(tmem + C::tm_qs(s), qd0 + static_cast<uint64_t>(s * (C::TILE >> 4) + (((i >> 2) * C::ATOM + (i & 3) * 32) >> 4)),
+          umma_ss_warp(tmem + C::TM_QS, qd0 + static_cast<uint64_t>(s * (C::TILE >> 4) + (((i >> 2) * C::ATOM + (i & 3) * 32) >> 4)),
                        sbd + ((i * 16 * 128) >> 4), id_pv, i > 0 ? 1u : 0u, lead);
         umma_commit_warp(&sm.sb_empty, lead);
         umma_commit_warp(&sm.qk_empty[s], lead);
@@ -261,7 +265,6 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
         }
         // P V
         if (!(ok = w.wait(&sm.p_full[s], (n >> 1) & 1, kErrLinearWait))) break;
-        if (n > 0 && !(ok = w.wait(&sm.o_empty, (n - 1) & 1, kErrLinearWait))) break;
         tc_fence_after();
         const uint64_t vd = vd0 + static_cast<uint64_t>((n % C::NV) * (C::ATOM >> 4));
 #pragma unroll
@@ -476,15 +479,27 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
 #pragma unroll
         for (int j = 0; j < 32; ++j) a[j] = __float_as_uint(s[j] * f);
         tmem_st32(at, a);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) a[j] = 0u;
+        tmem_st32(at + 64, a);
         tmem_st_wait();
       }
     }
+    // Both parts of S.
+    auto read = [&](uint32_t (&a)[32]) {
+      uint32_t c[32];
+      tmem_ld32(at, a);
+      tmem_ld32(at + 64, c);
+      tmem_ld_wait();
+      reg_fence(a);
+      reg_fence(c);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) a[j] = __float_as_uint(__uint_as_float(a[j]) + __uint_as_float(c[j]));
+    };
     auto finish = [&](float* to) {  // S to memory
       if (!mine) return;
       uint32_t a[32];
-      tmem_ld32(at, a);
-      tmem_ld_wait();
-      reg_fence(a);
+      read(a);
 #pragma unroll
       for (int j = 0; j < 32; j += 4) *reinterpret_cast<uint4*>(to + j) = make_uint4(a[j], a[j + 1], a[j + 2], a[j + 3]);
     };
@@ -501,11 +516,7 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
       auto state = [&](int n) -> bool {
         if (ok && n > 0) reach(&sm.kv_done, n - 1);
         uint32_t a[32];
-        if (ok && mine) {
-          tmem_ld32(at, a);
-          tmem_ld_wait();
-          reg_fence(a);
-        }
+        if (ok && mine) read(a);
         float down = 1.0f;
         if constexpr (!BF16) {
           // fp16: one power of two for the whole operand, its largest element below 2^15.
@@ -544,6 +555,9 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
 #pragma unroll
           for (int j = 0; j < 32; ++j) a[j] = __float_as_uint(__uint_as_float(a[j]) * f);
           tmem_st32(at, a);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) a[j] = 0u;
+          tmem_st32(at + 64, a);
           tmem_st_wait();
         }
         tc_fence_before();
@@ -561,13 +575,14 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
         }
         uint32_t a[32], x[32];
         tmem_ld32(tmem + C::TM_PV + col + lanes, a);
-        tmem_ld32(tmem + C::tm_qs(n & 1) + col + lanes, x);
+        tmem_ld32(tmem + C::TM_QS + col + lanes, x);
         tmem_ld_wait();
         reg_fence(a);
         reg_fence(x);
         tc_fence_before();
         mbar_arrive(&sm.o_empty);
-        // (P V was the last to read the chunk's V.)
+        // (P V was the last to read the chunk's V.  Rows of 64 bytes, swizzled as the tensor store
+        // reads them: piece i of row x at i ^ ((x >> 1) & 3).)
         uint4* stage = reinterpret_cast<uint4*>(sm.v[n % C::NV]) + (warp - 8) * 128;
         const uint64_t fs2 = f2_pack(fs, fs);
 #pragma unroll
@@ -585,17 +600,28 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
           }
           stage[lane * 4 + (i ^ ((lane >> 1) & 3))] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
         }
+        const int first = t0 + n * C::C + wq * 32;  // the warp's first token
+        fence_proxy_async_smem();  // a tensor store, or the next load of V, comes after these
         __syncwarp();
-        const int first = t0 + n * C::C + wq * 32;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {  // 8 rows x 64 bytes
-          const int rw = 8 * i + (lane >> 2), q = lane & 3, t = first + rw;
-          if (t < t1)
-            *reinterpret_cast<uint4*>(out + static_cast<int64_t>(row0 + t) * p.o_row + q * 8) =
-                stage[rw * 4 + (q ^ ((rw >> 1) & 3))];
+        if (t0 + (n + 1) * C::C <= t1) {
+          if (lane == 0) {
+            tma_store_4d(&p.tm_o, stage, half * C::N + col, row0 + first, h, bc);
+            bulk_commit();
+            bulk_wait_read();
+          }
+        } else {
+          // Rows behind the sequence's end are not written: row by row, 8 x 64 bytes at a time.
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            const int rw = 8 * i + (lane >> 2), q = lane & 3;
+            if (first + rw < t1)
+              *reinterpret_cast<uint4*>(out + static_cast<int64_t>(row0 + first + rw) * p.o_row + q * 8) =
+                  stage[rw * 4 + (q ^ ((rw >> 1) & 3))];
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
         }
-        fence_proxy_async_smem();  // the next load of V comes after these accesses
-        mbar_arrive(&sm.v_empty[n % C::NV]);
+        if (lane == 0) mbar_arrive(&sm.v_empty[n % C::NV]);
       };
 #pragma unroll 1
       for (int n = 0; n <= chunks; ++n) {
@@ -603,6 +629,7 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
         if (ok && n > 0) output(n - 1);
         if (BF16 && !ok) break;
       }
+      if (lane == 0) bulk_wait_all();  // every store has completed before the CTA ends
       if (ok && last && chunks > 0) reach(&sm.kv_done, chunks - 1);
       if (ok && last && p.state_out != nullptr && slot >= 0) finish(p.state_out + state_at);
     }
