@@ -316,8 +316,8 @@ attn_status finish_launch(cudaError_t e) {
 namespace attn {
 attn_status host_device_state(unsigned int** err, int* num_sms) { return device_state(err, num_sms); }
 bool host_make_map(CUtensorMap* m, const void* base, bool bf16, int rank, const uint64_t* dims,
-                   const uint64_t* strides_bytes, const uint32_t* box, CUtensorMapSwizzle swizzle) {
-  return make_map(m, base, bf16 ? ATTN_BF16 : ATTN_F16, rank, dims, strides_bytes, box, swizzle);
+                   const uint64_t* strides_bytes, const uint32_t* box) {
+  return make_map(m, base, bf16 ? ATTN_BF16 : ATTN_F16, rank, dims, strides_bytes, box);
 }
 attn_status host_check_opts(const attn_opts* opts, int Hq, bool allow_bias) {
   return check_opts(opts, Hq, allow_bias);

@@ -7,10 +7,9 @@ namespace attn {
 
 // The current device's error word and SM count.
 attn_status host_device_state(unsigned int** err, int* num_sms);
-// Tensor map over a 16-bit tensor (make_map in api.cu).
+// Tensor map with the 128-byte swizzle over a 16-bit tensor (make_map in api.cu).
 bool host_make_map(CUtensorMap* m, const void* base, bool bf16, int rank, const uint64_t* dims,
-                   const uint64_t* strides_bytes, const uint32_t* box,
-                   CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
+                   const uint64_t* strides_bytes, const uint32_t* box);
 // Options every attention entry point checks, and their resolved values.
 attn_status host_check_opts(const attn_opts* opts, int Hq, bool allow_bias);
 // Left bound of the window (negative: none) and the first tokens visible left of it.

@@ -7,10 +7,10 @@
 namespace attn {
 
 constexpr int kLinearChunk = 128;  // tokens per chunk
+constexpr int kLongestFirst = 128;  // sequences that every CTA ranks for itself
 
 struct LinearParams {
-  CUtensorMap tm_q, tm_k, tm_v;  // 4-D (d, rows, heads, batch), box {64, 128, 1, 1}
-  CUtensorMap tm_o;              // the same with box {32, 32, 1, 1} and 64-byte swizzle
+  CUtensorMap tm_q, tm_k, tm_v, tm_o;  // 4-D (d, rows, heads, batch), box {64, 128, 1, 1}
   void* o;
   const float* log_decay;
   const float* state_in;   // [num_states][Hq][d][d] or nullptr: zeros
@@ -20,6 +20,7 @@ struct LinearParams {
   float* work;             // [segs][B][Hq][d][d]: states of all segments but the last, then state_in
   int num_states, B, Hq, group, L, total;
   int segs, seg_chunks;    // pieces a sequence is cut into, chunks of each
+  int longest_first;       // packed sequences in order of their lengths (B <= kLongestFirst)
   int64_t o_batch, o_head, o_row;
   float scale;
   unsigned int* err;

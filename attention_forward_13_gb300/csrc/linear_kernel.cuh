@@ -20,7 +20,7 @@
 //            the products still read the one before; rows behind the sequence's end cleared.
 //            Then Q K^T from tensor memory (thread = row), decays, mask, P back into
 //            tensor memory over the columns it came from.
-//   two warps issue loads and products.
+//   three warps issue loads, products and stores.
 // V has three stages, as V' is wanted early and P V comes late in a chunk; o is staged in
 // the stage it leaves and goes out by tensor stores (straight from registers, 16 or 32 bytes
 // a row: 137 and 124 us).  Each role's loop is kept short, in rolled pieces of 32 columns:
@@ -52,9 +52,9 @@ struct LinearCfg {
   static constexpr int NCHUNK = D / 64;           // swizzle atoms along d
   static constexpr int TILE = C * D * 2;          // a Q or K tile
   static constexpr int ATOM = C * 128;            // one 64-column atom of it, and a V tile
-  // Warps 0-7 values and weights, 8-15 state and output, then loads and products.
-  static constexpr int THREADS = 18 * 32;
-  static constexpr int W_TMA = 16, W_MMA = 17;
+  // Warps 0-7 values and weights, 8-15 state and output, then loads, products, stores.
+  static constexpr int THREADS = 19 * 32;
+  static constexpr int W_TMA = 16, W_MMA = 17, W_STORE = 18;
   static constexpr int NV = 3;                    // stages of V
   // Tensor memory: chunk n's Q K^T at 128 (n & 1), P in the first 16 of every 32 columns
   // of it, Q S at 256, P V at 320, the state in two parts at 384 (what the second
@@ -75,11 +75,14 @@ struct LinearSmem {
   uint8_t row_max[2][2][128];  // fp16: the exponents of the largest scores in the two parts of a row
   int8_t row_scale[4][128];    // fp16: the powers of two that the rows of P were divided by,
   int state_scale[4];          // and the state (read up to two chunks late)
-  float pw[64];             // [31 + n]: w^n for n >= 0, else 0
   float col[32];            // [j]: w^(31 - j)
+  // Rows of the diagonal block: w^(lane - j), 0 where j > lane, for j = 0 .. 31 is
+  // d[31 - lane + j] with d[m] = w^(31 - m) or 0.  Four copies, the c-th shifted by c, so that every
+  // lane reads 16 aligned bytes; 72 floats apart, so that 8 lanes meet no bank twice.
+  float diag[4][72];
   uint64_t qk_full[2], qk_empty[2], v_full[C::NV], v_empty[C::NV];
   uint64_t s_full[2], p_full[2];
-  uint64_t o_full, o_empty, sb_full, sb_empty, kv_done, vp_full, teardown;
+  uint64_t o_full, o_empty, stage_full, sb_full, sb_empty, kv_done, vp_full, teardown;
   uint32_t tmem_base;
   uint32_t part[2][8];
   int abort_flag;
@@ -112,15 +115,33 @@ __device__ __forceinline__ void unpack16(uint32_t w, float& lo, float& hi) {
   }
 }
 
+template <bool BF16>
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  if constexpr (BF16) asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  else asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  if constexpr (BF16) asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  else asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+
 template <int D, bool BF16, bool STATES>
 __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(const __grid_constant__ LinearParams p) {
   using C = LinearCfg<D>;
-  extern __shared__ uint8_t smem_raw[];
-  LinearSmem<D>& sm =
-      *reinterpret_cast<LinearSmem<D>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  LinearSmem<D>& sm = *reinterpret_cast<LinearSmem<D>*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int half = blockIdx.x, h = blockIdx.y, b = blockIdx.z / p.segs, seg = blockIdx.z - b * p.segs;
+  const int half = blockIdx.x, h = blockIdx.y, place = blockIdx.z / p.segs, seg = blockIdx.z - place * p.segs;
 
+  if (smem_u32(smem_raw) & 1023u) {  // (the swizzled tiles need it; there is no room to round up)
+    if (tid == 0 && p.err) atomicOr(p.err, 1u << kErrLinearTeardown);
+    return;
+  }
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.qk_full[i], 1);
@@ -130,10 +151,11 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
     }
     for (int i = 0; i < C::NV; ++i) {
       mbar_init(&sm.v_full[i], 1);
-      mbar_init(&sm.v_empty[i], STATES ? 1 : 8);
+      mbar_init(&sm.v_empty[i], 1);
     }
     mbar_init(&sm.o_full, 1);
     mbar_init(&sm.o_empty, 256);
+    mbar_init(&sm.stage_full, 256);
     mbar_init(&sm.sb_full, 256);
     mbar_init(&sm.sb_empty, 1);
     mbar_init(&sm.kv_done, 1);
@@ -144,6 +166,25 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
   }
   pdl_launch_dependents();
   pdl_wait();
+  int b = place;
+  if (p.longest_first) {
+    // CTAs start in the order of blockIdx: the place-th longest sequence is this one's.
+    int* lens = reinterpret_cast<int*>(sm.sb);
+    int row, mine = 0;
+    if (tid < p.B) {
+      sequence_rows(p, tid, row, mine);
+      lens[tid] = mine;
+    }
+    __syncthreads();
+    if (tid < p.B) {
+      int rank = 0;
+      for (int i = 0; i < p.B; ++i) rank += lens[i] > mine || (lens[i] == mine && i < tid);
+      if (rank == place) lens[kLongestFirst] = tid;
+    }
+    __syncthreads();
+    b = lens[kLongestFirst];
+    __syncthreads();
+  }
   const int slot = state_of(p.index, p.num_states, b, p.err, half == 0 && h == 0 && seg == 0);
   int row0, len;
   sequence_rows(p, b, row0, len);
@@ -157,8 +198,11 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
   if ((t0 >= len && seg > 0) || (STATES && last)) return;
   const int chunks = (t1 - t0 + C::C - 1) / C::C;
   const float log2w = p.log_decay[h] * kLog2e;
-  if (tid < 64) sm.pw[tid] = tid < 31 ? 0.0f : decay_pow(log2w, tid - 31);
-  else if (tid < 96) sm.col[tid - 64] = decay_pow(log2w, 95 - tid);
+  if (tid < 32) sm.col[tid] = decay_pow(log2w, 31 - tid);
+  if (tid >= 64 && tid < 64 + 4 * 72) {
+    const int c = (tid - 64) / 72, m = (tid - 64) % 72 + c;
+    sm.diag[c][m - c] = m <= 31 ? decay_pow(log2w, 31 - m) : 0.0f;
+  }
   if (warp == C::W_MMA) {
     tmem_alloc(&sm.tmem_base, C::TM_COLS);
     tmem_relinquish();
@@ -224,10 +268,14 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
       umma_commit_warp(&sm.s_full[n & 1], lead);
     };
     bool ok = true;
-    if (chunks > 0) {
+    // A chunk that the sequence ends in is multiplied once its rows behind the end have been
+    // cleared (with V'): what they held may be NaN, and the weights there are 0.
+    const int partial = (t1 - t0) % C::C != 0 ? chunks - 1 : -1;
+    if (!STATES && chunks > 0) {
       ok = w.wait(&sm.qk_full[0], 0, kErrLinearWait);
+      if (ok && partial == 0) ok = w.wait(&sm.vp_full, 0, kErrLinearWait);
       tc_fence_after();
-      if (!STATES && ok) issue_s(0);
+      if (ok) issue_s(0);
     }
     for (int n = 0; ok && n < chunks; ++n) {
       const int s = n & 1;
@@ -260,6 +308,7 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
         umma_commit_warp(&sm.qk_empty[s], lead);
         if (n + 1 < chunks) {
           if (!(ok = w.wait(&sm.qk_full[s ^ 1], ((n + 1) >> 1) & 1, kErrLinearWait))) break;
+          if (n + 1 == partial && !(ok = w.wait(&sm.vp_full, (n + 1) & 1, kErrLinearWait))) break;
           tc_fence_after();
           issue_s(n + 1);  // (over the P whose P V was issued before)
         }
@@ -278,14 +327,30 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
     // All products must be done before tensor memory is freed.
     umma_commit_warp(&sm.teardown, lead);
     if (!wait_raw(&sm.teardown, 0, globaltimer_ns() + 50000000ull) && p.err) atomicOr(p.err, 1u << kErrLinearTeardown);
+  } else if (warp == C::W_STORE) {
+    // ===================== stores of whole chunks ================================
+    if (!STATES && lane == 0) {
+      for (int n = 0; n < chunks && t0 + (n + 1) * C::C <= t1; ++n) {
+        if (!w.wait(&sm.stage_full, n & 1, kErrLinearWait)) break;
+        tma_store_4d(&p.tm_o, sm.v[n % C::NV], half * C::N, row0 + t0 + n * C::C, h, bc);
+        bulk_commit();
+        bulk_wait_read();
+        mbar_arrive(&sm.v_empty[n % C::NV]);
+      }
+      bulk_wait_all();  // every store has completed before the CTA ends
+    }
   } else if (warp < 8) {
     // ===================== values and weights =====================================
     const int part = warp >> 2, wq = warp & 3, r = wq * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
     const float full = decay_pow(log2w, C::C - 1 - r);
+    const float* diag = &sm.diag[(31 - lane) & 3][(31 - lane) & ~3];
     bool ok = true;
     // V' = w^(tokens behind it) v: up to where the state is wanted, the chunk's end and in
-    // the first launch the segment's.  Thread = token r, 32 columns.
+    // the first launch the segment's.  Thread = token r, 32 columns.  In packed 16-bit
+    // arithmetic: with the weight f = f1 + f2 in two pieces, hi = f1 v rounded, f1 v - hi is exact
+    // (a product of two significands less its upper half), and lo = that + f2 v: f2's and lo's
+    // roundings are 2^-18 of v' each in bf16.
     auto values = [&](int n) {
       const int sv = n % C::NV;
       ok = __all_sync(0xffffffffu, w.wait(&sm.v_full[sv], (n / C::NV) & 1, kErrLinearWait));
@@ -297,24 +362,25 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
                                               : 0.0f;
       uint8_t* src = sm.v[sv] + r * 128;
       uint32_t hi[16], lo[16];
+      float f1, f2, unused;
+      const uint32_t fw = pack16<BF16>(f, f);
+      unpack16<BF16>(fw, f1, unused);
+      f2 = f - f1;
+      const uint32_t gw = pack16<BF16>(f2, f2);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint4 x = *reinterpret_cast<const uint4*>(src + (((4 * part + i) ^ (r & 7)) << 4));
         const uint32_t in[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float a, c, ah, ch;
-          unpack16<BF16>(r < live ? in[e] : 0u, a, c);  // (rows of nobody may hold anything)
-          a *= f;
-          c *= f;
-          const uint32_t y = pack16<BF16>(a, c);
-          unpack16<BF16>(y, ah, ch);
-          hi[4 * i + e] = y;
-          lo[4 * i + e] = pack16<BF16>(a - ah, c - ch);
+          const uint32_t v2 = r < live ? in[e] : 0u;  // (rows of nobody may hold anything)
+          hi[4 * i + e] = mul2<BF16>(v2, fw);
+          lo[4 * i + e] = fma2<BF16>(v2, gw, fma2<BF16>(v2, fw, hi[4 * i + e] ^ 0x80008000u));
         }
       }
       if (live < C::C) {
-        // What lies behind the end meets weights of 0, and 0 * NaN is not 0.
+        // What lies behind the end meets weights of 0, and 0 * NaN is not 0.  (Q K^T of
+        // this chunk waits for it too.)
         ok = __all_sync(0xffffffffu, w.wait(&sm.qk_full[n & 1], (n >> 1) & 1, kErrLinearWait));
         if (!ok) return;
         if (r >= live) {
@@ -381,32 +447,23 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
         } else {
           uint32_t x[32];
           tmem_ld32(base + 32 * cb, x);
+          // w^(i-j): left of the diagonal block the row's power down to the block's last
+          // column times the column's from there, in it the table's.
+          const float rowf = cb < wq ? f * exp2f(log2w * (lane + 1 + 32 * (wq - 1 - cb))) : f;
+          const float4* c4 = reinterpret_cast<const float4*>(cb < wq ? sm.col : diag);
+          const uint64_t f2 = f2_pack(rowf, rowf);
           tmem_ld_wait();
           reg_fence(x);
-          if (cb < wq) {
-            // w^(i-j) is the row's power down to the block's last column times the
-            // column's from there.
-            const float rowf = f * exp2f(log2w * (lane + 1 + 32 * (wq - 1 - cb)));
-            const uint64_t f2 = f2_pack(rowf, rowf);
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              const float4 c = *reinterpret_cast<const float4*>(&sm.col[j]);
-              float x0, x1, x2, x3;
-              f2_unpack(f2_mul(f2_mul(f2_pack(c.x, c.y), f2), f2_pack(__uint_as_float(x[j]), __uint_as_float(x[j + 1]))),
-                        x0, x1);
-              f2_unpack(
-                  f2_mul(f2_mul(f2_pack(c.z, c.w), f2), f2_pack(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]))),
-                  x2, x3);
-              pk[j / 2] = pack16<BF16>(x0, x1);
-              pk[j / 2 + 1] = pack16<BF16>(x2, x3);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              const float a = __uint_as_float(x[j]) * (f * sm.pw[31 + lane - j]);
-              const float c = __uint_as_float(x[j + 1]) * (f * sm.pw[30 + lane - j]);
-              pk[j / 2] = pack16<BF16>(j <= lane ? a : 0.0f, j + 1 <= lane ? c : 0.0f);
-            }
+          for (int j = 0; j < 32; j += 4) {
+            const float4 c = c4[j / 4];
+            float x0, x1, x2, x3;
+            f2_unpack(f2_mul(f2_mul(f2_pack(c.x, c.y), f2), f2_pack(__uint_as_float(x[j]), __uint_as_float(x[j + 1]))),
+                      x0, x1);
+            f2_unpack(f2_mul(f2_mul(f2_pack(c.z, c.w), f2), f2_pack(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]))),
+                      x2, x3);
+            pk[j / 2] = pack16<BF16>(x0, x1);
+            pk[j / 2 + 1] = pack16<BF16>(x2, x3);
           }
         }
         tmem_st16(base + 32 * cb, pk);
@@ -431,9 +488,11 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
     const int part = (warp - 8) >> 2, wq = warp & 3, r = wq * 32 + lane, col = 32 * part;
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t at = tmem + C::TM_STATE + col + lanes;
-    const bool mine = D == 128 || wq < 2;  // (d = 64: rows 64 .. 127 of tensor memory hold nothing)
-    const int64_t state_at = (static_cast<int64_t>(slot) * p.Hq + h) * head + half * C::N + r * D + col;
-    const int64_t row_at = work_at + r * D + col;
+    // (d = 64: rows 64 .. 127 of tensor memory repeat rows 0 .. 63, and are worked on alike,
+    // but only the first are written.)
+    const bool mine = D == 128 || wq < 2;
+    const int64_t state_at = (static_cast<int64_t>(slot) * p.Hq + h) * head + half * C::N + (r % D) * D + col;
+    const int64_t row_at = work_at + (r % D) * D + col;
     bool ok = true;
     // Waits until the products so far are in S.
     auto reach = [&](uint64_t* bar, int phase) {
@@ -456,13 +515,13 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
           s[i + 3] = fmaf(x.w, f, s[i + 3]);
         }
       };
-      if (mine) {
+      {
         float* copy = p.work + (p.segs - 1) * work_seg + row_at;
         if (seg == 0 && p.state_in != nullptr && slot >= 0) {
           // (Cut sequences: state_out may be state_in, whose last segment may be done before
           // this one starts: it is read from where the first launch has put it.)
           add(STATES || last ? p.state_in + state_at : copy, 1.0f);
-          if constexpr (STATES)
+          if (STATES && mine)
 #pragma unroll
             for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4*>(copy + i) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
         } else if (!STATES && seg > 0) {
@@ -494,12 +553,23 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
       reg_fence(a);
       reg_fence(c);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) a[j] = __float_as_uint(__uint_as_float(a[j]) + __uint_as_float(c[j]));
+      for (int j = 0; j < 32; j += 2) {
+        float x, y;
+        f2_unpack(f2_add(f2_pack(__uint_as_float(a[j]), __uint_as_float(a[j + 1])),
+                         f2_pack(__uint_as_float(c[j]), __uint_as_float(c[j + 1]))), x, y);
+        a[j] = __float_as_uint(x);
+        a[j + 1] = __float_as_uint(y);
+      }
+    };
+    auto clear2 = [&] {  // the second part of S
+      const uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int j = 0; j < 32; j += 8) tmem_st8(at + 64 + j, z);
     };
     auto finish = [&](float* to) {  // S to memory
-      if (!mine) return;
       uint32_t a[32];
       read(a);
+      if (!mine) return;
 #pragma unroll
       for (int j = 0; j < 32; j += 4) *reinterpret_cast<uint4*>(to + j) = make_uint4(a[j], a[j + 1], a[j + 2], a[j + 3]);
     };
@@ -516,12 +586,12 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
       auto state = [&](int n) -> bool {
         if (ok && n > 0) reach(&sm.kv_done, n - 1);
         uint32_t a[32];
-        if (ok && mine) read(a);
+        if (ok) read(a);
         float down = 1.0f;
         if constexpr (!BF16) {
           // fp16: one power of two for the whole operand, its largest element below 2^15.
           float m = 0.0f;
-          if (ok && mine)
+          if (ok)
 #pragma unroll
             for (int j = 0; j < 32; ++j) m = fmaxf(m, fabsf(__uint_as_float(a[j])));
           const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
@@ -540,26 +610,27 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
         if (!ok) return !BF16;
         const int m = t1 - t0 - n * C::C;
         const float f = m >= C::C ? full : decay_pow(log2w, m);
-        if (mine) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t x[4];
+        for (int j = 0; j < 4; ++j) {
+          uint32_t x[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float lo = __uint_as_float(a[8 * j + 2 * e]), hi = __uint_as_float(a[8 * j + 2 * e + 1]);
-              if constexpr (!BF16) lo *= down, hi *= down;
-              x[e] = pack16<BF16>(lo, hi);
-            }
-            *reinterpret_cast<uint4*>(sb_row + (((4 * part + j) ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+          for (int e = 0; e < 4; ++e) {
+            float lo = __uint_as_float(a[8 * j + 2 * e]), hi = __uint_as_float(a[8 * j + 2 * e + 1]);
+            if constexpr (!BF16) lo *= down, hi *= down;
+            x[e] = pack16<BF16>(lo, hi);
           }
-#pragma unroll
-          for (int j = 0; j < 32; ++j) a[j] = __float_as_uint(__uint_as_float(a[j]) * f);
-          tmem_st32(at, a);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) a[j] = 0u;
-          tmem_st32(at + 64, a);
-          tmem_st_wait();
+          if (mine) *reinterpret_cast<uint4*>(sb_row + (((4 * part + j) ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
         }
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+          float x, y;
+          f2_unpack(f2_mul(f2_pack(__uint_as_float(a[j]), __uint_as_float(a[j + 1])), f2_pack(f, f)), x, y);
+          a[j] = __float_as_uint(x);
+          a[j + 1] = __float_as_uint(y);
+        }
+        tmem_st32(at, a);
+        clear2();
+        tmem_st_wait();
         tc_fence_before();
         fence_proxy_async_smem();
         mbar_arrive(&sm.sb_full);
@@ -581,9 +652,8 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
         reg_fence(x);
         tc_fence_before();
         mbar_arrive(&sm.o_empty);
-        // (P V was the last to read the chunk's V.  Rows of 64 bytes, swizzled as the tensor store
-        // reads them: piece i of row x at i ^ ((x >> 1) & 3).)
-        uint4* stage = reinterpret_cast<uint4*>(sm.v[n % C::NV]) + (warp - 8) * 128;
+        // (P V was the last to read the chunk's V.  128-byte swizzle, as the tensor store reads.)
+        uint8_t* stage = sm.v[n % C::NV];
         const uint64_t fs2 = f2_pack(fs, fs);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -598,30 +668,23 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
             f2_unpack(o2, lo, hi);
             pk[e] = pack16<BF16>(lo, hi);
           }
-          stage[lane * 4 + (i ^ ((lane >> 1) & 3))] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          *reinterpret_cast<uint4*>(stage + r * 128 + (((4 * part + i) ^ (r & 7)) << 4)) =
+              make_uint4(pk[0], pk[1], pk[2], pk[3]);
         }
-        const int first = t0 + n * C::C + wq * 32;  // the warp's first token
-        fence_proxy_async_smem();  // a tensor store, or the next load of V, comes after these
-        __syncwarp();
         if (t0 + (n + 1) * C::C <= t1) {
-          if (lane == 0) {
-            tma_store_4d(&p.tm_o, stage, half * C::N + col, row0 + first, h, bc);
-            bulk_commit();
-            bulk_wait_read();
-          }
-        } else {
-          // Rows behind the sequence's end are not written: row by row, 8 x 64 bytes at a time.
-#pragma unroll 1
-          for (int i = 0; i < 4; ++i) {
-            const int rw = 8 * i + (lane >> 2), q = lane & 3;
-            if (first + rw < t1)
-              *reinterpret_cast<uint4*>(out + static_cast<int64_t>(row0 + first + rw) * p.o_row + q * 8) =
-                  stage[rw * 4 + (q ^ ((rw >> 1) & 3))];
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
+          fence_proxy_async_smem();  // the tensor store, and the next load of V, come after these
+          mbar_arrive(&sm.stage_full);
+          return;
         }
-        if (lane == 0) mbar_arrive(&sm.v_empty[n % C::NV]);
+        // The last chunk, cut by the sequence's end: row by row, 8 x 64 bytes at a time.
+        __syncwarp();
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          const int row = wq * 32 + 8 * i + (lane >> 2), q = lane & 3, t = t0 + n * C::C + row;
+          if (t < t1)
+            *reinterpret_cast<uint4*>(out + static_cast<int64_t>(row0 + t) * p.o_row + q * 8) =
+                *reinterpret_cast<const uint4*>(stage + row * 128 + (((4 * part + q) ^ (row & 7)) << 4));
+        }
       };
 #pragma unroll 1
       for (int n = 0; n <= chunks; ++n) {
@@ -629,7 +692,6 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
         if (ok && n > 0) output(n - 1);
         if (BF16 && !ok) break;
       }
-      if (lane == 0) bulk_wait_all();  // every store has completed before the CTA ends
       if (ok && last && chunks > 0) reach(&sm.kv_done, chunks - 1);
       if (ok && last && p.state_out != nullptr && slot >= 0) finish(p.state_out + state_at);
     }
@@ -645,7 +707,7 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
 
 template <int D, bool BF16, bool STATES>
 static cudaError_t launch_linear_t(const LinearParams& p, int segs, cudaStream_t stream) {
-  constexpr size_t smem = sizeof(LinearSmem<D>) + 1024;
+  constexpr size_t smem = sizeof(LinearSmem<D>);
   static_assert(smem <= 227 * 1024, "shared memory per block");
   const dim3 grid(D / 64, static_cast<unsigned>(p.Hq), static_cast<unsigned>(p.B) * segs);
   return launch_pdl_upto<linear_chunk_kernel<D, BF16, STATES>>(smem, grid, LinearCfg<D>::THREADS, smem, stream, p);
