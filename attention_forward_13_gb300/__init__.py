@@ -81,6 +81,7 @@ def _ptr(t):
 # The current stream's handle without building a Stream object (3 us a call on a
 # Grace host, the query itself 0.1 us).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream):
@@ -94,7 +95,7 @@ def _call(fn, device, *args):
     """Calls a library function whose last argument is the stream: ``device``'s current one."""
     if device.type != "cuda":
         raise ValueError("the tensors must be on a CUDA device")
-    here = torch.cuda.current_device()
+    here = _current_device()
     if device.index != here:
         with torch.cuda.device(device):
             return fn(*args, _stream(None))
@@ -603,7 +604,8 @@ def attn_cache_slots(block_table, seqlens, add, num_tokens, page_size, num_pages
     n = int(num_tokens)
     if n < 0:
         raise ValueError("num_tokens must not be negative")
-    slots, positions, sequence = (torch.empty(n, dtype=torch.int32, device=dev) for _ in range(3))
+    slots = torch.empty(n, dtype=torch.int32, device=dev)
+    positions, sequence = torch.empty_like(slots), torch.empty_like(slots)
     cu = torch.empty(B + 1, dtype=torch.int32, device=dev)
     _check(_call(library().attn_cache_slots, dev, block_table.data_ptr(), seqlens.data_ptr(), add.data_ptr(),
                  slots.data_ptr(), positions.data_ptr(), cu.data_ptr(), sequence.data_ptr(), B, n, max_pages,
@@ -640,17 +642,25 @@ def _rope_opts(inv_freq, d, device, interleaved, inverse, scale):
 def _like(t, out, name):
     """A new contiguous tensor like t, or ``out`` checked to be one (any strides)."""
     if out is None:
-        return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
     if out.dtype is not t.dtype or out.device != t.device or out.shape != t.shape:
         raise ValueError(f"{name} must be like its input")
     return out
 
 
+@functools.lru_cache(maxsize=512)
+def _stride_struct(batch, head, row):
+    return _lib.attn_strides(batch, head, row)
+
+
 def _rows(t):
     """Strides of dense [B,H,L,d] or packed [N,H,d] rows (None: no tensor)."""
     if t is None:
-        return _lib.attn_strides(0, 0, 0)
-    return _strides_bhld(t) if t.dim() == 4 else _strides_thd(t)
+        return _stride_struct(0, 0, 0)
+    s = t.stride()
+    if s[-1] != 1:
+        raise ValueError("innermost (head-dim) stride must be 1")
+    return _stride_struct(s[0], s[1], s[2]) if len(s) == 4 else _stride_struct(0, s[1], s[0])
 
 
 @_on_stream
@@ -659,25 +669,27 @@ def attn_rope(q, k, inv_freq, positions=None, interleaved=False, inverse=False, 
     first 2 * len(inv_freq) elements of a head turn by position * inv_freq (attn_rope_freqs),
     in halves or interleaved pairs, times ``scale``.  positions int32 [L] or [B,L], packed [N];
     None: the row.  ``inverse`` turns back.  q_out and k_out may be q and k.  Returns (q_out, k_out)."""
-    dims, dev = q.dim(), q.device
-    if dims not in (3, 4):
-        raise ValueError("q must be [B,Hq,L,d] or [N,Hq,d]")
-    if dims == 4:
-        B, Hq, L, d = q.shape
+    shape, dev = q.shape, q.device
+    if len(shape) == 4:
+        B, Hq, L, d = shape
+    elif len(shape) == 3:
+        B, (L, Hq, d) = 1, shape
     else:
-        B, (L, Hq, d) = 1, q.shape
+        raise ValueError("q must be [B,Hq,L,d] or [N,Hq,d]")
     Hkv = 0
     if k is not None:
-        if k.dtype is not q.dtype or k.device != dev or k.dim() != dims or k.shape[-1] != d or \
-                (k.shape[0], k.shape[2]) != (B, L) and dims == 4 or dims == 3 and k.shape[0] != L:
+        other = k.shape
+        if len(other) == len(shape):
+            Hkv = other[1]
+        if k.dtype is not q.dtype or k.device != dev or \
+                other != ((B, Hkv, L, d) if len(shape) == 4 else (L, Hkv, d)):
             raise ValueError("k must be like q but for its heads")
-        Hkv = k.shape[1]
     stride = 0
     if positions is not None:
         _ints(dev, "positions", positions)
         if positions.shape == (L,):
             pass
-        elif dims == 4 and positions.shape == (B, L):
+        elif len(shape) == 4 and positions.shape == (B, L):
             stride = L
         else:
             raise ValueError("positions must be [L] or [B,L], of packed rows [N]")
@@ -731,6 +743,7 @@ def attn_cache_append(k, v, k_pool, v_pool, slots, q=None, inv_freq=None, positi
     return q_out
 
 
+@functools.lru_cache(maxsize=256)
 def attn_linear_workspace_bytes(B, Hq, max_seqlen, d) -> int:
     """Bytes of device memory attn_linear_fwd and attn_linear_fwd_varlen work in (may be 0)."""
     return int(library().attn_linear_workspace_bytes(B, Hq, max_seqlen, d))
@@ -793,8 +806,7 @@ def attn_linear_fwd(q, k, v, log_decay, state=None, state_out=True, state_index=
     work, size = _linear_workspace(workspace, B, Hq, L, d, dev)
     st = _call(library().attn_linear_fwd, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
                log_decay.data_ptr(), _ptr(state), _ptr(state_out), _ptr(state_index), n, B, Hq, Hkv, L, d,
-               _dtype_code(q), _strides_bhld(q), _strides_bhld(k), _strides_bhld(v), _strides_bhld(o),
-               float(scale or 0.0), _ptr(work), size)
+               _dtype_code(q), _rows(q), _rows(k), _rows(v), _rows(o), float(scale or 0.0), _ptr(work), size)
     _check(st, "attn_linear_fwd")
     return o, state_out
 
@@ -819,8 +831,8 @@ def attn_linear_fwd_varlen(q, k, v, cu_seqlens, max_seqlen, log_decay, state=Non
     work, size = _linear_workspace(workspace, B, Hq, int(max_seqlen), d, dev)
     st = _call(library().attn_linear_fwd_varlen, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
                cu_seqlens.data_ptr(), log_decay.data_ptr(), _ptr(state), _ptr(state_out), _ptr(state_index), n, B,
-               total, int(max_seqlen), Hq, Hkv, d, _dtype_code(q), _strides_thd(q), _strides_thd(k),
-               _strides_thd(v), _strides_thd(o), float(scale or 0.0), _ptr(work), size)
+               total, int(max_seqlen), Hq, Hkv, d, _dtype_code(q), _rows(q), _rows(k), _rows(v), _rows(o),
+               float(scale or 0.0), _ptr(work), size)
     _check(st, "attn_linear_fwd_varlen")
     return o, state_out
 
@@ -848,7 +860,7 @@ def _step_strides(t):
     s = t.stride()
     if s[2] != 1:
         raise ValueError("innermost (head-dim) stride must be 1")
-    return _lib.attn_strides(s[0], s[1], 0)
+    return _stride_struct(s[0], s[1], 0)
 
 
 @_on_stream
