@@ -11,7 +11,11 @@
 //
 // Memory bound: every element is read and written once, about 4 operations each.
 // A thread keeps the cosines and sines of its 8 pairs of one token and walks over
-// heads with them, so that their cost (some 30 instructions a pair) is shared.
+// heads with them, so that their cost (some 30 instructions a pair) is shared.  The
+// work, (tile of tokens, head) in this order, is dealt to the CTAs that the GPU holds at
+// once in equal runs: with a grid of tiles x groups of heads a third wave of a few
+// CTAs ended the launch (2 x 8192 tokens of 32 + 8 heads: 66 us, so 55.3, where a copy of
+// as many bytes takes 51.8).
 #include "host.h"
 #include "launch.h"
 #include "ptx.cuh"
@@ -24,6 +28,7 @@ using namespace attn;
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kPerSm = 4;  // CTAs that an SM holds (at 3, 5 and 6: 57.8, 61.7 and 66.9 us for that prompt)
 constexpr int kMaxDim = 512;
 
 // A tensor's rows: element strides of batch, head and row.
@@ -42,7 +47,7 @@ struct RopeParams {
   int64_t num_slots;
   const double* inv_freq;
   int tokens, L, d, rot;  // tokens = batch * L
-  int per_cta;            // heads of one CTA
+  int share, extra;       // entries of the (tile, head) list per CTA, and CTAs with one more
   int interleaved;
   float sign, scale;      // sign -1: the inverse rotation
   unsigned int* err;
@@ -121,63 +126,88 @@ __device__ __forceinline__ int64_t slot_of(const RopeParams& p, int token) {
 // multiple of 16): a thread owns two pieces, 8 pairs, or one piece behind the
 // rotated elements.  Neighbouring threads take neighbouring pieces of a row, then
 // the next token's.
+// This CTA's run of the (tile, head) list: the tile, and heads [h0, h1) of it, then
+// the next tile's.  (A tile has as many tokens as the CTA has rows of threads.)
+struct Run {
+  int left, tile, h0;
+  __device__ __forceinline__ Run(const RopeParams& p, int heads) {
+    const int cta = blockIdx.x, first = cta * p.share + min(cta, p.extra);
+    left = p.share + (cta < p.extra ? 1 : 0);
+    tile = first / heads;
+    h0 = first - tile * heads;
+  }
+  __device__ __forceinline__ int end(int heads) const { return min(heads, h0 + left); }
+  __device__ __forceinline__ void next(int h1) {
+    left -= h1 - h0;
+    h0 = 0;
+    ++tile;
+  }
+};
+
 template <bool BF16, bool INTER>
-__global__ void __launch_bounds__(kThreads) rope_pairs_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads, kPerSm) rope_pairs_kernel(const RopeParams p) {
   __shared__ unsigned long long freq[kMaxDim / 2];
   pdl_launch_dependents();
   pdl_wait();
   for (int i = threadIdx.x; i < p.rot / 2; i += kThreads) freq[i] = turns_of(p.inv_freq[i]);
-  const int turned = p.rot / 16, units = turned + (p.d - p.rot) / 8;
-  const int per = kThreads / units;  // tokens of a CTA
-  const int tt = threadIdx.x / units, u = threadIdx.x - tt * units;
-  const int token = blockIdx.x * per + tt;
-  const bool mine = tt < per && token < p.tokens;
-  const int b = mine ? token / p.L : 0, l = mine ? token - b * p.L : 0;
-  const int pos = !mine ? 0 : p.positions != nullptr ? p.positions[b * p.pos_batch + l] : l;
-  const int64_t slot = mine ? slot_of(p, token) : -1;
   __syncthreads();
-  if (!mine) return;
+  const int turned = p.rot / 16, units = turned + (p.d - p.rot) / 8;
+  const int per = kThreads / units;  // tokens of a tile
+  const int tt = threadIdx.x / units, u = threadIdx.x - tt * units;
   const bool rot = u < turned;
   // First and second piece of the thread, in pieces of 8 elements.
   const int e0 = rot ? (INTER ? 2 * u : u) : 2 * turned + (u - turned);
   const int e1 = rot ? (INTER ? 2 * u + 1 : turned + u) : e0;
-  float c[8], s[8];
-  if (rot) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) turn(freq[8 * u + i], pos, p.sign, p.scale, c[i], s[i]);
-  }
   const int heads = p.part[0].heads + p.part[1].heads + p.part[2].heads;
-  const int h_end = min(heads, (static_cast<int>(blockIdx.y) + 1) * p.per_cta);
-#pragma unroll 2
-  for (int h = blockIdx.y * p.per_cta; h < h_end; ++h) {
-    const Place w = place(p, h, b, l, slot);
-    if (!w.write) continue;
-    const uint4 x = w.src[e0];
-    if (!rot) {
-      w.dst[e0] = x;
-      continue;
-    }
-    const uint4 y = w.src[e1];
-    if (!w.rotate) {
-      w.dst[e0] = x;
-      w.dst[e1] = y;
-      continue;
-    }
-    const uint32_t a[4] = {x.x, x.y, x.z, x.w}, d[4] = {y.x, y.y, y.z, y.w};
-    uint32_t oa[4], od[4];
+  for (Run run(p, heads); run.left > 0;) {
+    const int h0 = run.h0, h1 = run.end(heads), token = run.tile * per + tt;
+    run.next(h1);
+    if (tt >= per || token >= p.tokens) continue;
+    const int b = token / p.L, l = token - b * p.L;
+    const int64_t slot = slot_of(p, token);
+    float c[8], s[8];
+    if (rot) {
+      const int pos = p.positions != nullptr ? p.positions[b * p.pos_batch + l] : l;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 fa = widen<BF16>(a[i]), fd = widen<BF16>(d[i]);
-      if constexpr (INTER) {  // a: pairs i, d: pairs 4 + i
-        oa[i] = narrow<BF16>(fa.x * c[i] - fa.y * s[i], fa.y * c[i] + fa.x * s[i]);
-        od[i] = narrow<BF16>(fd.x * c[4 + i] - fd.y * s[4 + i], fd.y * c[4 + i] + fd.x * s[4 + i]);
-      } else {
-        oa[i] = narrow<BF16>(fa.x * c[2 * i] - fd.x * s[2 * i], fa.y * c[2 * i + 1] - fd.y * s[2 * i + 1]);
-        od[i] = narrow<BF16>(fd.x * c[2 * i] + fa.x * s[2 * i], fd.y * c[2 * i + 1] + fa.y * s[2 * i + 1]);
-      }
+      for (int i = 0; i < 8; ++i) turn(freq[8 * u + i], pos, p.sign, p.scale, c[i], s[i]);
     }
-    w.dst[e0] = make_uint4(oa[0], oa[1], oa[2], oa[3]);
-    w.dst[e1] = make_uint4(od[0], od[1], od[2], od[3]);
+    // The next head's pieces are on their way while this one's are turned.
+    Place now = place(p, h0, b, l, slot);
+    uint4 x = now.src[e0], y = now.src[e1];
+#pragma unroll 1
+    for (int h = h0; h < h1; ++h) {
+      Place next = now;
+      uint4 nx = x, ny = y;
+      if (h + 1 < h1) {
+        next = place(p, h + 1, b, l, slot);
+        nx = next.src[e0];
+        ny = next.src[e1];
+      }
+      if (now.write) {
+        if (rot && now.rotate) {
+          const uint32_t a[4] = {x.x, x.y, x.z, x.w}, d[4] = {y.x, y.y, y.z, y.w};
+          uint32_t oa[4], od[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 fa = widen<BF16>(a[i]), fd = widen<BF16>(d[i]);
+            if constexpr (INTER) {  // a: pairs i, d: pairs 4 + i
+              oa[i] = narrow<BF16>(fa.x * c[i] - fa.y * s[i], fa.y * c[i] + fa.x * s[i]);
+              od[i] = narrow<BF16>(fd.x * c[4 + i] - fd.y * s[4 + i], fd.y * c[4 + i] + fd.x * s[4 + i]);
+            } else {
+              oa[i] = narrow<BF16>(fa.x * c[2 * i] - fd.x * s[2 * i], fa.y * c[2 * i + 1] - fd.y * s[2 * i + 1]);
+              od[i] = narrow<BF16>(fd.x * c[2 * i] + fa.x * s[2 * i], fd.y * c[2 * i + 1] + fa.y * s[2 * i + 1]);
+            }
+          }
+          x = make_uint4(oa[0], oa[1], oa[2], oa[3]);
+          y = make_uint4(od[0], od[1], od[2], od[3]);
+        }
+        now.dst[e0] = x;
+        if (rot) now.dst[e1] = y;
+      }
+      now = next;
+      x = nx;
+      y = ny;
+    }
   }
 }
 
@@ -185,65 +215,68 @@ __global__ void __launch_bounds__(kThreads) rope_pairs_kernel(const RopeParams p
 // shared memory, where the CTA has put its rows of the head before any of them is
 // written (the output may be the input).
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) rope_any_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads, kPerSm) rope_any_kernel(const RopeParams p) {
   __shared__ unsigned long long freq[kMaxDim / 2];
   __shared__ uint4 rows[2][kThreads];
   pdl_launch_dependents();
   pdl_wait();
   for (int i = threadIdx.x; i < p.rot / 2; i += kThreads) freq[i] = turns_of(p.inv_freq[i]);
+  __syncthreads();
   const int units = p.d / 8, per = kThreads / units;
   const int tt = threadIdx.x / units, u = threadIdx.x - tt * units;
-  const int token = blockIdx.x * per + tt;
-  const bool mine = tt < per && token < p.tokens;
-  const int b = mine ? token / p.L : 0, l = mine ? token - b * p.L : 0;
-  const int pos = !mine ? 0 : p.positions != nullptr ? p.positions[b * p.pos_batch + l] : l;
-  const int64_t slot = mine ? slot_of(p, token) : -1;
-  __syncthreads();
-  // The partner of each element, and out = x c + partner s.
-  float c[8], s[8];
-  int at[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int e = 8 * u + i, half = p.rot / 2;
-    at[i] = -1;
-    c[i] = 1.0f;
-    s[i] = 0.0f;
-    if (e < p.rot) {
-      const bool second = p.interleaved ? (e & 1) : e >= half;
-      const int pair = p.interleaved ? e >> 1 : second ? e - half : e;
-      at[i] = p.interleaved ? (e ^ 1) : second ? e - half : e + half;
-      turn(freq[pair], pos, p.sign, p.scale, c[i], s[i]);
-      if (!second) s[i] = -s[i];
-    }
-  }
   const int heads = p.part[0].heads + p.part[1].heads + p.part[2].heads;
-  const int h_end = min(heads, (static_cast<int>(blockIdx.y) + 1) * p.per_cta);
   int buf = 0;
-  for (int h = blockIdx.y * p.per_cta; h < h_end; ++h, buf ^= 1) {
-    Place w{nullptr, nullptr, false, false};
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (mine) {
-      w = place(p, h, b, l, slot);
-      if (w.write) x = w.src[u];
-    }
-    rows[buf][threadIdx.x] = x;
-    __syncthreads();  // (one a round: the buffer written next was read before this one)
-    if (!mine || !w.write) continue;
-    if (w.rotate) {
-      const uint16_t* row = reinterpret_cast<const uint16_t*>(&rows[buf][tt * units]);
-      uint32_t v[4] = {x.x, x.y, x.z, x.w};
+  for (Run run(p, heads); run.left > 0;) {
+    const int h0 = run.h0, h1 = run.end(heads), token = run.tile * per + tt;
+    run.next(h1);
+    const bool mine = tt < per && token < p.tokens;
+    const int b = mine ? token / p.L : 0, l = mine ? token - b * p.L : 0;
+    const int pos = !mine ? 0 : p.positions != nullptr ? p.positions[b * p.pos_batch + l] : l;
+    const int64_t slot = mine ? slot_of(p, token) : -1;
+    // The partner of each element, and out = x c + partner s.
+    float c[8], s[8];
+    int at[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = widen<BF16>(v[i]);
-        const uint32_t lo = at[2 * i] >= 0 ? row[at[2 * i]] : 0u, hi = at[2 * i + 1] >= 0 ? row[at[2 * i + 1]] : 0u;
-        const float2 g = widen<BF16>(lo | (hi << 16));
-        const uint32_t o = narrow<BF16>(f.x * c[2 * i] + g.x * s[2 * i], f.y * c[2 * i + 1] + g.y * s[2 * i + 1]);
-        // Elements behind the rotated ones keep their bits.
-        if (at[2 * i] >= 0) v[i] = at[2 * i + 1] >= 0 ? o : (o & 0xffffu) | (v[i] & 0xffff0000u);
+    for (int i = 0; i < 8; ++i) {
+      const int e = 8 * u + i, half = p.rot / 2;
+      at[i] = -1;
+      c[i] = 1.0f;
+      s[i] = 0.0f;
+      if (e < p.rot) {
+        const bool second = p.interleaved ? (e & 1) : e >= half;
+        const int pair = p.interleaved ? e >> 1 : second ? e - half : e;
+        at[i] = p.interleaved ? (e ^ 1) : second ? e - half : e + half;
+        turn(freq[pair], pos, p.sign, p.scale, c[i], s[i]);
+        if (!second) s[i] = -s[i];
       }
-      x = make_uint4(v[0], v[1], v[2], v[3]);
     }
-    w.dst[u] = x;
+    // The next head's pieces are on their way while this one's are turned.
+    Place w{nullptr, nullptr, false, false};
+    uint4 nx = make_uint4(0, 0, 0, 0);
+    if (mine) nx = place(p, h0, b, l, slot).src[u];
+    for (int h = h0; h < h1; ++h, buf ^= 1) {
+      uint4 x = nx;
+      if (mine) {
+        w = place(p, h, b, l, slot);
+        if (h + 1 < h1) nx = place(p, h + 1, b, l, slot).src[u];
+      }
+      rows[buf][threadIdx.x] = x;
+      __syncthreads();  // (one a round: the buffer written next was read before this one)
+      if (!w.write) continue;
+      if (w.rotate) {
+        const uint16_t* row = reinterpret_cast<const uint16_t*>(&rows[buf][tt * units]);
+        uint32_t v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (at[2 * i] < 0) continue;  // (elements behind the rotated ones keep their bits; rot is even)
+          const float2 f = widen<BF16>(v[i]);
+          const float2 g = widen<BF16>(row[at[2 * i]] | (static_cast<uint32_t>(row[at[2 * i + 1]]) << 16));
+          v[i] = narrow<BF16>(f.x * c[2 * i] + g.x * s[2 * i], f.y * c[2 * i + 1] + g.y * s[2 * i + 1]);
+        }
+        x = make_uint4(v[0], v[1], v[2], v[3]);
+      }
+      w.dst[u] = x;
+    }
   }
 }
 
@@ -274,11 +307,11 @@ attn_status launch(RopeParams& p, bool bf16, cudaStream_t stream, const char* na
   const int units = pairs ? p.rot / 16 + (p.d - p.rot) / 8 : p.d / 8;
   const int per = kThreads / units;
   const int heads = p.part[0].heads + p.part[1].heads + p.part[2].heads;
-  const int64_t tiles = (static_cast<int64_t>(p.tokens) + per - 1) / per;
-  // Heads per CTA: as few as keep eight CTAs (2048 threads) for every SM.
-  const int64_t want = tiles * heads / (8 * static_cast<int64_t>(sms));
-  p.per_cta = static_cast<int>(std::max<int64_t>(std::min<int64_t>(want, heads), (heads + 65534) / 65535));
-  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>((heads + p.per_cta - 1) / p.per_cta));
+  const int64_t work = (static_cast<int64_t>(p.tokens) + per - 1) / per * heads;
+  if (work > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;  // (more than the GPU's memory holds)
+  const int grid = static_cast<int>(std::min<int64_t>(work, static_cast<int64_t>(kPerSm) * sms));
+  p.share = static_cast<int>(work / grid);
+  p.extra = static_cast<int>(work % grid);
   cudaError_t e;
   if (pairs && p.interleaved)
     e = bf16 ? launch_pdl(rope_pairs_kernel<true, true>, grid, kThreads, 0, stream, p)
