@@ -744,9 +744,10 @@ def attn_cache_append(k, v, k_pool, v_pool, slots, q=None, inv_freq=None, positi
 
 
 @functools.lru_cache(maxsize=256)
-def attn_linear_workspace_bytes(B, Hq, max_seqlen, d) -> int:
-    """Bytes of device memory attn_linear_fwd and attn_linear_fwd_varlen work in (may be 0)."""
-    return int(library().attn_linear_workspace_bytes(B, Hq, max_seqlen, d))
+def attn_linear_workspace_bytes(B, Hq, max_seqlen, tokens, d) -> int:
+    """Bytes of device memory attn_linear_fwd (tokens = B * L) and attn_linear_fwd_varlen (tokens = total)
+    work in (may be 0)."""
+    return int(library().attn_linear_workspace_bytes(B, Hq, max_seqlen, tokens, d))
 
 
 def _linear_states(log_decay, state, state_out, state_index, B, Hq, d, device):
@@ -778,8 +779,8 @@ def _linear_states(log_decay, state, state_out, state_index, B, Hq, d, device):
     return state, state_out, n or 0
 
 
-def _linear_workspace(workspace, B, Hq, max_seqlen, d, device):
-    need = attn_linear_workspace_bytes(B, Hq, max_seqlen, d)
+def _linear_workspace(workspace, B, Hq, max_seqlen, tokens, d, device):
+    need = attn_linear_workspace_bytes(B, Hq, max_seqlen, tokens, d)
     if workspace is None:
         return (torch.empty(need, dtype=torch.uint8, device=device) if need else None), need
     if workspace.device != device or not workspace.is_contiguous():
@@ -803,7 +804,7 @@ def attn_linear_fwd(q, k, v, log_decay, state=None, state_out=True, state_index=
     dev = q.device
     o = _like(q, o, "o")
     state, state_out, n = _linear_states(log_decay, state, state_out, state_index, B, Hq, d, dev)
-    work, size = _linear_workspace(workspace, B, Hq, L, d, dev)
+    work, size = _linear_workspace(workspace, B, Hq, L, B * L, d, dev)
     st = _call(library().attn_linear_fwd, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
                log_decay.data_ptr(), _ptr(state), _ptr(state_out), _ptr(state_index), n, B, Hq, Hkv, L, d,
                _dtype_code(q), _rows(q), _rows(k), _rows(v), _rows(o), float(scale or 0.0), _ptr(work), size)
@@ -828,7 +829,7 @@ def attn_linear_fwd_varlen(q, k, v, cu_seqlens, max_seqlen, log_decay, state=Non
     B = cu_seqlens.shape[0] - 1
     o = _like(q, o, "o")
     state, state_out, n = _linear_states(log_decay, state, state_out, state_index, B, Hq, d, dev)
-    work, size = _linear_workspace(workspace, B, Hq, int(max_seqlen), d, dev)
+    work, size = _linear_workspace(workspace, B, Hq, int(max_seqlen), total, d, dev)
     st = _call(library().attn_linear_fwd_varlen, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
                cu_seqlens.data_ptr(), log_decay.data_ptr(), _ptr(state), _ptr(state_out), _ptr(state_index), n, B,
                total, int(max_seqlen), Hq, Hkv, d, _dtype_code(q), _rows(q), _rows(k), _rows(v), _rows(o),

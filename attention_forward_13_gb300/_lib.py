@@ -87,7 +87,7 @@ def _declare(lib):
     lib.attn_rope_freqs.argtypes = [_I, D, _I, D, D, D, D, ctypes.POINTER(D)]
     lib.attn_rope.argtypes = [_P] * 5 + [ctypes.c_int64] + [_I] * 6 + [S] * 4 + [R, _P]
     lib.attn_cache_append.argtypes = [_P] * 8 + [_I] * 7 + [S] * 4 + [R, _P]
-    lib.attn_linear_workspace_bytes.argtypes = [_I] * 4
+    lib.attn_linear_workspace_bytes.argtypes = [_I, _I, _I, ctypes.c_int64, _I]
     lib.attn_linear_workspace_bytes.restype = Z
     lib.attn_linear_fwd.argtypes = [_P] * 8 + [_I] * 7 + [S] * 4 + [ctypes.c_float, _P, Z, _P]
     lib.attn_linear_fwd_varlen.argtypes = [_P] * 9 + [_I] * 8 + [S] * 4 + [ctypes.c_float, _P, Z, _P]

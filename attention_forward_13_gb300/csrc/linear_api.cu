@@ -157,10 +157,10 @@ attn_status linear_fwd(const void* q, const void* k, const void* v, void* o, con
         !map(&p.tm_o, o, so, Hq))
       return ATTN_ERR_INVALID;
   }
-  linear_segments(B, Hq, max_len, d, &p.segs, &p.seg_chunks);
-  if (attn_linear_workspace_bytes(B, Hq, max_len, d) > 0 &&
-      (workspace == nullptr || !host_aligned(workspace, 16) ||
-       workspace_bytes < attn_linear_workspace_bytes(B, Hq, max_len, d)))
+  const int64_t tokens = cu != nullptr ? rows : static_cast<int64_t>(B) * rows;
+  linear_segments(B, Hq, max_len, tokens, d, &p.segs, &p.seg_chunks);
+  const size_t need = attn_linear_workspace_bytes(B, Hq, max_len, tokens, d);
+  if (need > 0 && (workspace == nullptr || !host_aligned(workspace, 16) || workspace_bytes < need))
     return ATTN_ERR_INVALID;
   p.o = o;
   p.cu = cu;
@@ -193,10 +193,10 @@ attn_status linear_fwd(const void* q, const void* k, const void* v, void* o, con
 
 extern "C" {
 
-size_t attn_linear_workspace_bytes(int B, int Hq, int max_seqlen, int d) {
-  if (B <= 0 || Hq <= 0 || max_seqlen <= 0 || (d != 64 && d != 128)) return 0;
+size_t attn_linear_workspace_bytes(int B, int Hq, int max_seqlen, int64_t tokens, int d) {
+  if (B <= 0 || Hq <= 0 || max_seqlen <= 0 || tokens < 0 || (d != 64 && d != 128)) return 0;
   int segs, chunks;
-  linear_segments(B, Hq, max_seqlen, d, &segs, &chunks);
+  linear_segments(B, Hq, max_seqlen, tokens, d, &segs, &chunks);
   return segs > 1 ? static_cast<size_t>(segs) * B * Hq * d * d * sizeof(float) : 0;
 }
 

@@ -82,7 +82,7 @@ struct LinearSmem {
   float diag[4][72];
   uint64_t qk_full[2], qk_empty[2], v_full[C::NV], v_empty[C::NV];
   uint64_t s_full[2], p_full[2];
-  uint64_t o_full, o_empty, stage_full, sb_full, sb_empty, kv_done, vp_full, teardown;
+  uint64_t o_full, o_empty, stage_full, ready, init, kv_done, teardown;
   uint32_t tmem_base;
   uint32_t part[2][8];
   int abort_flag;
@@ -156,10 +156,9 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
     mbar_init(&sm.o_full, 1);
     mbar_init(&sm.o_empty, 256);
     mbar_init(&sm.stage_full, 256);
-    mbar_init(&sm.sb_full, 256);
-    mbar_init(&sm.sb_empty, 1);
+    mbar_init(&sm.ready, STATES ? 256 : 512);  // V', and (not STATES) S as an operand and decayed
+    mbar_init(&sm.init, 256);                  // (STATES) the state the segment starts from
     mbar_init(&sm.kv_done, 1);
-    mbar_init(&sm.vp_full, 256);
     mbar_init(&sm.teardown, 1);
     sm.abort_flag = 0;
     fence_mbar_init();
@@ -273,16 +272,15 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
     const int partial = (t1 - t0) % C::C != 0 ? chunks - 1 : -1;
     if (!STATES && chunks > 0) {
       ok = w.wait(&sm.qk_full[0], 0, kErrLinearWait);
-      if (ok && partial == 0) ok = w.wait(&sm.vp_full, 0, kErrLinearWait);
+      if (ok && partial == 0) ok = w.wait(&sm.ready, 0, kErrLinearWait);
       tc_fence_after();
       if (ok) issue_s(0);
     }
     for (int n = 0; ok && n < chunks; ++n) {
       const int s = n & 1;
       // S += K^T V'
-      if (!(ok = w.wait(&sm.vp_full, n & 1, kErrLinearWait))) break;
-      if (STATES ? n == 0 : true)
-        if (!(ok = w.wait(&sm.sb_full, STATES ? 0 : n & 1, kErrLinearWait))) break;
+      if (!(ok = w.wait(&sm.ready, n & 1, kErrLinearWait))) break;
+      if (STATES && n == 0 && !(ok = w.wait(&sm.init, 0, kErrLinearWait))) break;
       if (STATES && !(ok = w.wait(&sm.qk_full[s], (n >> 1) & 1, kErrLinearWait))) break;
       tc_fence_after();
 #pragma unroll
@@ -304,11 +302,10 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
         for (int i = 0; i < D / 16; ++i)
           umma_ss_warp(tmem + C::TM_QS, qd0 + static_cast<uint64_t>(s * (C::TILE >> 4) + (((i >> 2) * C::ATOM + (i & 3) * 32) >> 4)),
                        sbd + ((i * 16 * 128) >> 4), id_pv, i > 0 ? 1u : 0u, lead);
-        umma_commit_warp(&sm.sb_empty, lead);
         umma_commit_warp(&sm.qk_empty[s], lead);
         if (n + 1 < chunks) {
           if (!(ok = w.wait(&sm.qk_full[s ^ 1], ((n + 1) >> 1) & 1, kErrLinearWait))) break;
-          if (n + 1 == partial && !(ok = w.wait(&sm.vp_full, (n + 1) & 1, kErrLinearWait))) break;
+          if (n + 1 == partial && !(ok = w.wait(&sm.ready, (n + 1) & 1, kErrLinearWait))) break;
           tc_fence_after();
           issue_s(n + 1);  // (over the P whose P V was issued before)
         }
@@ -403,7 +400,7 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
         *reinterpret_cast<uint4*>(sm.vp[1] + at) = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
       }
       fence_proxy_async_smem();
-      mbar_arrive(&sm.vp_full);
+      mbar_arrive(&sm.ready);
     };
     // P_ij = scale w^(i-j) q_i . k_j in blocks of 32 columns, thread = row i = r: blocks part
     // and part + 2, of which those right of the diagonal one are 0.  False: all threads that
@@ -425,9 +422,13 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
             tmem_ld32(base + 32 * cb, x);
             tmem_ld_wait();
             reg_fence(x);
-            const int seen = cb < wq ? 31 : lane;
+            if (cb == wq) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) m = fmaxf(m, j <= seen ? fabsf(__uint_as_float(x[j])) : 0.0f);
+              for (int j = 0; j < 32; ++j) x[j] = j <= lane ? x[j] : 0u;
+            }
+#pragma unroll
+            for (int j = 0; j < 32; j += 2)
+              m = fmax3(m, fabsf(__uint_as_float(x[j])), fabsf(__uint_as_float(x[j + 1])));
           }
         }
         sm.row_max[n & 1][part][r] = static_cast<uint8_t>(exponent_of(m * p.scale));
@@ -575,7 +576,7 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
     };
     if constexpr (STATES) {
       tc_fence_before();
-      mbar_arrive(&sm.sb_full);
+      mbar_arrive(&sm.init);
       reach(&sm.o_full, 0);
       if (ok) finish(p.work + seg * work_seg + row_at);
     } else {
@@ -593,7 +594,8 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
           float m = 0.0f;
           if (ok)
 #pragma unroll
-            for (int j = 0; j < 32; ++j) m = fmaxf(m, fabsf(__uint_as_float(a[j])));
+            for (int j = 0; j < 32; j += 2)
+              m = fmax3(m, fabsf(__uint_as_float(a[j])), fabsf(__uint_as_float(a[j + 1])));
           const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
           if (lane == 0) sm.part[n & 1][warp - 8] = top;
           // (Every thread comes here, aborted or not, and all leave together.)
@@ -606,7 +608,8 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
           down = two_to(-e);
         }
         if (!ok) return false;
-        if (n > 0) ok = __all_sync(0xffffffffu, w.wait(&sm.sb_empty, (n - 1) & 1, kErrLinearWait));
+        // (Q S of the chunk before has read the operand.)
+        if (n > 0) ok = __all_sync(0xffffffffu, w.wait(&sm.qk_empty[(n - 1) & 1], ((n - 1) >> 1) & 1, kErrLinearWait));
         if (!ok) return !BF16;
         const int m = t1 - t0 - n * C::C;
         const float f = m >= C::C ? full : decay_pow(log2w, m);
@@ -633,7 +636,7 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
         tmem_st_wait();
         tc_fence_before();
         fence_proxy_async_smem();
-        mbar_arrive(&sm.sb_full);
+        mbar_arrive(&sm.ready);
         return true;
       };
       auto output = [&](int n) {

@@ -513,11 +513,11 @@ attn_status attn_cache_append(const void* q, void* q_out, const void* k, const v
  * [B][Hkv][L][d].  attn_linear_fwd_varlen -- packed sequences, as attn_fwd_varlen: rows
  * behind the last sequence are not written.  Sequences of no tokens hand
  * their state on.
- *   workspace: attn_linear_workspace_bytes() bytes (may be 0, then NULL will do),
- *   16-byte aligned; nothing in it has to be set, and calls that may overlap on the GPU
+ *   workspace: attn_linear_workspace_bytes() bytes (may be 0, then NULL will do; tokens: all
+ *   rows, B * L or total), 16-byte aligned; nothing in it has to be set, and calls that may overlap on the GPU
  *   each need one.  Results do not depend on what else runs.
  */
-size_t attn_linear_workspace_bytes(int B, int Hq, int max_seqlen, int d);
+size_t attn_linear_workspace_bytes(int B, int Hq, int max_seqlen, int64_t tokens, int d);
 attn_status attn_linear_fwd(const void* q, const void* k, const void* v, void* o, const float* log_decay,
                             const float* state_in, float* state_out, const int32_t* state_index, int num_states,
                             int B, int Hq, int Hkv, int L, int d, attn_dtype dtype, attn_strides sq, attn_strides sk,
