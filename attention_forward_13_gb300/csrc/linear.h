@@ -4,6 +4,8 @@
 #include "../../include/attn_fwd.h"
 #include "common.cuh"
 
+#include <initializer_list>
+
 namespace attn {
 
 constexpr int kLinearChunk = 128;  // tokens per chunk
@@ -31,21 +33,20 @@ struct LinearParams {
 // the chunks in order; where they leave SMs idle, the walk is cut into segments,
 // whose states are summed up first, in a launch of its own that reads k and v once
 // more (and takes about half the time a chunk).  As many pieces as the longest walk is
-// longer than an SM's share of all chunks; rounded down where all sequences are about as
-// long, as a second round of CTAs would cost what the cut gains, else to the nearest
-// (16 sequences of 1 to 3001 tokens, 16 heads, d = 64: one piece 44.5 us, two FIGURE).
+// longer than an SM's share of all chunks, rounded down (16 heads of 2048 tokens, d = 128:
+// 24.5 -> 21.2 us; sequences of 3000, 200, 100 and 50 tokens, 16 heads, d = 64: 35 -> 23;
+// rounded up, 16 sequences of 1 to 3001: 42 -> 61).  Segments that short sequences do not
+// have are CTAs as well, that leave at once: no more than eight for every SM.
 inline void linear_segments(int B, int Hq, int max_len, int64_t total, int d, int* segs, int* seg_chunks) {
   constexpr int64_t kSms = 152;
   const int chunks = max_len / kLinearChunk + (max_len % kLinearChunk != 0 ? 1 : 0);
-  const int64_t most = static_cast<int64_t>(B) * chunks;
-  int64_t all = total / kLinearChunk + (B + 1) / 2;  // of all sequences, about
-  const bool ragged = 4 * most > 5 * all;
-  all = ragged ? all : most;
-  const int64_t work = all * Hq * (d / 64);
-  int64_t n = work > 0 ? (chunks * kSms + (ragged ? work / 2 : 0)) / work : 1;
-  n = n < chunks / 2 ? n : chunks / 2;
-  n = n < 16 ? n : 16;
-  n = n < 65535 / (B > 0 ? B : 1) ? n : 65535 / (B > 0 ? B : 1);  // (a grid's z)
+  const int64_t ctas = static_cast<int64_t>(B) * Hq * (d / 64), most = static_cast<int64_t>(B) * chunks;
+  int64_t all = total / kLinearChunk + (B + 1) / 2;  // chunks of all sequences, about
+  if (all > most) all = most;
+  int64_t n = all > 0 ? chunks * kSms / (all * Hq * (d / 64)) : 1;
+  for (const int64_t most_segs : {static_cast<int64_t>(chunks / 2), 8 * kSms / (ctas > 0 ? ctas : 1),
+                                  static_cast<int64_t>(65535 / (B > 0 ? B : 1)), static_cast<int64_t>(16)})
+    n = n < most_segs ? n : most_segs;
   n = n > 1 ? n : 1;
   const int per = chunks > 0 ? static_cast<int>((chunks + n - 1) / n) : 1;
   *seg_chunks = per;
