@@ -602,8 +602,8 @@ def attn_cache_slots(block_table, seqlens, add, num_tokens, page_size, num_pages
     [B+1], sequence [num_tokens]), int32."""
     dev, B, max_pages = _cache_state(block_table, seqlens, add)
     n = int(num_tokens)
-    if n < 0:
-        raise ValueError("num_tokens must not be negative")
+    if not 0 <= n < 1 << 30:
+        raise ValueError("num_tokens must not be negative, and below 2^30")
     slots = torch.empty(n, dtype=torch.int32, device=dev)
     positions, sequence = torch.empty_like(slots), torch.empty_like(slots)
     cu = torch.empty(B + 1, dtype=torch.int32, device=dev)

@@ -143,6 +143,7 @@ attn_status linear_fwd(const void* q, const void* k, const void* v, void* o, con
   if (rows > 0) {
     for (const void* x : {q, k, v, static_cast<const void*>(o)})
       if (x == nullptr || !host_aligned(x, 16)) return ATTN_ERR_INVALID;
+    if (o == q || o == k || o == v) return ATTN_ERR_INVALID;  // (CTAs of a head read what others have written)
     const bool batches = cu == nullptr && B > 1;
     for (const attn_strides* s : {&sq, &sk, &sv, &so})
       if (!strides_ok(*s, true, batches)) return ATTN_ERR_INVALID;
@@ -167,7 +168,7 @@ attn_status linear_fwd(const void* q, const void* k, const void* v, void* o, con
   p.log_decay = log_decay;
   p.state_in = state_in;
   p.state_out = state_out;
-  p.index = index;
+  p.index = state_in != nullptr || state_out != nullptr ? index : nullptr;
   p.work = static_cast<float*>(workspace);
   p.num_states = num_states;
   p.B = B;
@@ -237,6 +238,7 @@ attn_status attn_linear_step(const void* q, const void* k, const void* v, void* 
   if (st != ATTN_OK || B == 0) return st;
   for (const void* x : {q, k, v, static_cast<const void*>(o), static_cast<const void*>(state)})
     if (x == nullptr || !host_aligned(x, 16)) return ATTN_ERR_INVALID;
+  if (o == q || o == k || o == v) return ATTN_ERR_INVALID;
   for (const attn_strides* s : {&sq, &sk, &sv, &so})
     if (!strides_ok(*s, false, B > 1)) return ATTN_ERR_INVALID;
   StepParams p{q, k, v, o, log_decay, state, state_index, num_states, Hq, Hq / Hkv,

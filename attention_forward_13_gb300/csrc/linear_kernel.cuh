@@ -138,6 +138,8 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int half = blockIdx.x, h = blockIdx.y, place = blockIdx.z / p.segs, seg = blockIdx.z - place * p.segs;
 
+  pdl_launch_dependents();
+  pdl_wait();
   if (smem_u32(smem_raw) & 1023u) {  // (the swizzled tiles need it; there is no room to round up)
     if (tid == 0 && p.err) atomicOr(p.err, 1u << kErrLinearTeardown);
     return;
@@ -163,8 +165,6 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
     sm.abort_flag = 0;
     fence_mbar_init();
   }
-  pdl_launch_dependents();
-  pdl_wait();
   int b = place;
   if (p.longest_first) {
     // CTAs start in the order of blockIdx: the place-th longest sequence is this one's.

@@ -498,7 +498,8 @@ attn_status attn_cache_append(const void* q, void* q_out, const void* k, const v
  * Linear attention with a decay per head.  With g = log_decay[h] <= 0 (device fp32
  * [Hq], natural log; -inf keeps nothing), per sequence and query head, kv head h / (Hq / Hkv):
  *   S_t = e^g S_(t-1) + k_t v_t^T  (a d x d matrix, rows k, columns v),  o_t = scale * q_t^T S_t.
- * scale <= 0 selects 1 / sqrt(d).  d in {64, 128}, fp16 or bf16, at most 2^30 rows; states fp32
+ * scale <= 0 selects 1 / sqrt(d).  o may not overlap q, k or v.  d in {64, 128}, fp16 or bf16, at
+ * most 2^30 rows; states fp32
  * [num_states][Hq][d][d] contiguous, 16-byte aligned.  state_in NULL: S before the first token is 0;
  * state_out NULL: the last state is not kept; state_out = state_in: in place, else
  * they do not overlap.  state_index: device int32 [B], the state of sequence b in
@@ -506,6 +507,9 @@ attn_status attn_cache_append(const void* q, void* q_out, const void* k, const v
  * [0, num_states), or one that an earlier sequence of the call has, is treated so too and
  * sets the device error word's bit for bad cache indices.
  * log_decay above 0 is allowed as long as nothing overflows: e^(128 g) and the results.
+ * Weights and states of any size that fp32 holds are kept in range (fp16: by powers of two);
+ * in fp16 the terms e^(g n) v that enter a state are held to 2^-25 of v's range or 2^-22 of
+ * themselves, in bf16 to 2^-17 of themselves.
  * NaN or infinity in a sequence's q, k, v or state may make all that sequence's outputs
  * and its state NaN, and no other's; what lies behind a sequence's end may hold anything.
  *

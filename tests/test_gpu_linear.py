@@ -94,7 +94,8 @@ def test_long(B, L, H, dt, d):
     no_device_error()
 
 
-LENS = [[5], [0], [0, 0, 0], [1, 0, 700, 128, 0, 33], [129, 64, 1, 1, 255, 900, 2], [300] * 9]
+LENS = [[5], [0], [0, 0, 0], [1, 0, 700, 128, 0, 33], [129, 64, 1, 1, 255, 900, 2], [300] * 9,
+        [(37 * i * i) % 391 for i in range(30)], [i % 4 for i in range(140)], [1100] + [3] * 5]
 
 
 @pytest.mark.parametrize("lens", LENS, ids=str)
@@ -280,4 +281,46 @@ def test_empty():
     assert not S.any()
     o, S = A.attn_linear_fwd(q[:0], k[:0], v[:0], g)
     assert S.shape == (0, 2, 64, 64)
+    no_device_error()
+
+
+@pytest.mark.parametrize("size_q,size_v,g", [(60.0, 1e-3, 0.01), (0.002, 1e-2, 0.3), (15.0, 30.0, 1.0), (1.0, 200.0, 0.0)])
+def test_fp16_ranges(size_q, size_v, g):
+    """Weights and states far above and below what fp16 holds, where o itself fits it: scores up to 10^6, states up to
+    10^5 (no decay, keys and values that agree)."""
+    q, k, v, _ = make(41, 1, 700, 2, 2, 128, torch.float16, state=False)
+    q, k, v = q * size_q, k.abs() * size_q, v.abs() * size_v
+    g = torch.full((2,), -g, device="cuda")
+    o64, S64, do, dS = plain(q, k, v, g, 1.0, None)[0]
+    most = float(o64.abs().max())
+    scale = min(1.0, 2e4 / most) if size_q > 50 else 100.0 / most
+    o, S = A.attn_linear_fwd(q, k, v, g, scale=scale)
+    check(o[0], S[0], plain(q, k, v, g, scale, None)[0])
+    if size_q > 50:
+        assert torch.matmul(q[0].float(), k[0].float().transpose(1, 2)).abs().max() * scale > 65504
+    if size_v == 200.0:
+        assert S.abs().max() > 65504
+    no_device_error()
+
+
+def test_index_without_states():
+    """Nothing to look up: the index says nothing."""
+    q, k, v, _ = make(42, 2, 140, 2, 2, 64, torch.bfloat16, state=False)
+    g = decays(2)
+    o, S = A.attn_linear_fwd(q, k, v, g, state_out=False, state_index=torch.tensor([9, 9], dtype=torch.int32, device="cuda"))
+    want, _ = A.attn_linear_fwd(q, k, v, g)
+    assert S is None and torch.equal(o, want)
+    no_device_error()
+
+
+@pytest.mark.parametrize("form", ["dense", "step"])
+def test_outputs_over_inputs_refused(form):
+    q, k, v, state = make(43, 2, 1 if form == "step" else 140, 2, 2, 64, torch.bfloat16)
+    g = decays(2)
+    for x in (q, k, v):
+        with pytest.raises(A.AttnError):
+            if form == "dense":
+                A.attn_linear_fwd(q, k, v, g, o=x)
+            else:
+                A.attn_linear_step(q[:, :, 0], k[:, :, 0], v[:, :, 0], g, state, o=x[:, :, 0])
     no_device_error()

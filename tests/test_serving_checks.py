@@ -70,7 +70,7 @@ def test_slots(kw, status):
 
 
 def linear(form="dense", **kw):
-    a = dict(q=P, k=P, v=P, o=P, cu=P, g=P, si=P, so=P, index=None, n=1, B=1, Hq=2, Hkv=2, L=8, total=8, d=64, dtype=1,
+    a = dict(q=P, k=P, v=P, o=2 * P, cu=P, g=P, si=P, so=P, index=None, n=1, B=1, Hq=2, Hkv=2, L=8, total=8, d=64, dtype=1,
              s=OK, scale=0.0, work=P, size=1 << 30)
     a.update(kw)
     lib, s = A.library(), [a["s"]] * 4
@@ -90,7 +90,7 @@ def linear(form="dense", **kw):
     (dict(q=None), 1), (dict(o=None), 1), (dict(v=P + 2), 1), (dict(g=None), 1), (dict(g=P + 1), 1), (dict(si=P + 4), 1),
     (dict(n=0), 1), (dict(B=3, n=2), 1), (dict(index=P + 2), 1), (dict(Hq=3), 1), (dict(Hkv=0), 1), (dict(d=96), 2),
     (dict(dtype=2), 2), (dict(dtype=9), 1), (dict(scale=math.nan), 1), (dict(B=-1), 1), (dict(B=0), 0),
-    (dict(B=70000, n=70000), 2), (dict(s=S(4096, 60, 64)), 1)])
+    (dict(B=70000, n=70000), 2), (dict(s=S(4096, 60, 64)), 1), (dict(o=P), 1)])
 def test_linear(form, kw, status):
     assert linear(form, **kw) == status
 
@@ -137,7 +137,7 @@ def test_append_python(kw):
 def test_slots_python():
     t = torch.zeros(2, 3, dtype=torch.int32)
     n = torch.ones(2, dtype=torch.int32)
-    for a in [(t, n.long(), n, 4, 16, 9), (t, n, n[:1], 4, 16, 9), (t.long(), n, n, 4, 16, 9), (t, n, n, -1, 16, 9)]:
+    for a in [(t, n, n, 1 << 30, 16, 9), (t, n.long(), n, 4, 16, 9), (t, n, n[:1], 4, 16, 9), (t.long(), n, n, 4, 16, 9), (t, n, n, -1, 16, 9)]:
         with pytest.raises(ValueError):
             A.attn_cache_slots(*a)
 
@@ -167,3 +167,15 @@ def test_linear_packed_and_step_python():
     for kw in (dict(k=K[:4], v=K[:4]), dict(state=ST), dict(o=Q[:4]), dict(log_decay=G4[:1])):
         with pytest.raises(ValueError):
             A.attn_linear_step(**{**dict(q=Q, k=K, v=K, log_decay=G4, state=torch.zeros(5, 4, 64, 64)), **kw})
+
+
+def test_linear_workspace():
+    """None where heads fill the GPU or sequences are short; else a state for every piece of each head."""
+    W = A.attn_linear_workspace_bytes
+    assert W(2, 32, 8192, 2 * 8192, 128) == 0 and W(1, 16, 128, 128, 128) == 0 and W(0, 4, 100, 0, 64) == 0
+    assert W(1, 16, 2048, 2048, 128) == 4 * 16 * 128 * 128 * 4
+    assert W(1, 1, 1 << 20, 1 << 20, 64) == 16 * 64 * 64 * 4        # at most 16 pieces
+    assert W(60000, 1, 100000, 200000, 64) == 0                      # a grid's third dimension
+    # the buffer a call needs is the one this says, whatever the lengths
+    assert linear(B=1, Hq=16, Hkv=16, L=2048, d=128, n=1, s=S(1 << 24, 2048 * 128, 128), work=None) == 1
+    assert linear(B=1, Hq=16, Hkv=16, L=2048, d=128, n=1, s=S(1 << 24, 2048 * 128, 128), size=1000) == 1
