@@ -61,7 +61,7 @@ struct LinearCfg {
   // piece of V' adds is kept apart, so that one product of 128 columns reads K once).
   static constexpr uint32_t TM_COLS = 512;
   __device__ static constexpr uint32_t tm_s(int b) { return 128u * b; }
-  static constexpr uint32_t TM_QS = 256, TM_PV = 320, TM_STATE = 384, TM_STATE2 = 448;
+  static constexpr uint32_t TM_QS = 256, TM_PV = 320, TM_STATE = 384, TM_SECOND = 64;  // (the second part, from the first)
 };
 
 template <int D>
@@ -82,7 +82,8 @@ struct LinearSmem {
   float diag[4][72];
   uint64_t qk_full[2], qk_empty[2], v_full[C::NV], v_empty[C::NV];
   uint64_t s_full[2], p_full[2];
-  uint64_t o_full, o_empty, stage_full, ready, init, kv_done, teardown;
+  uint64_t stage_full[C::NV];
+  uint64_t o_full, o_empty, ready, init, kv_done, teardown;
   uint32_t tmem_base;
   uint32_t part[2][8];
   int abort_flag;
@@ -154,10 +155,10 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
     for (int i = 0; i < C::NV; ++i) {
       mbar_init(&sm.v_full[i], 1);
       mbar_init(&sm.v_empty[i], 1);
+      mbar_init(&sm.stage_full[i], 256);
     }
     mbar_init(&sm.o_full, 1);
     mbar_init(&sm.o_empty, 256);
-    mbar_init(&sm.stage_full, 256);
     mbar_init(&sm.ready, STATES ? 256 : 512);  // V', and (not STATES) S as an operand and decayed
     mbar_init(&sm.init, 256);                  // (STATES) the state the segment starts from
     mbar_init(&sm.kv_done, 1);
@@ -328,7 +329,9 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
     // ===================== stores of whole chunks ================================
     if (!STATES && lane == 0) {
       for (int n = 0; n < chunks && t0 + (n + 1) * C::C <= t1; ++n) {
-        if (!w.wait(&sm.stage_full, n & 1, kErrLinearWait)) break;
+        // (One barrier per stage: a slow store may fall chunks behind, but a stage is not
+        // filled again before it has been released here.)
+        if (!w.wait(&sm.stage_full[n % C::NV], (n / C::NV) & 1, kErrLinearWait)) break;
         tma_store_4d(&p.tm_o, sm.v[n % C::NV], half * C::N, row0 + t0 + n * C::C, h, bc);
         bulk_commit();
         bulk_wait_read();
@@ -541,7 +544,7 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
         tmem_st32(at, a);
 #pragma unroll
         for (int j = 0; j < 32; ++j) a[j] = 0u;
-        tmem_st32(at + 64, a);
+        tmem_st32(at + C::TM_SECOND, a);
         tmem_st_wait();
       }
     }
@@ -549,7 +552,7 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
     auto read = [&](uint32_t (&a)[32]) {
       uint32_t c[32];
       tmem_ld32(at, a);
-      tmem_ld32(at + 64, c);
+      tmem_ld32(at + C::TM_SECOND, c);
       tmem_ld_wait();
       reg_fence(a);
       reg_fence(c);
@@ -565,7 +568,7 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
     auto clear2 = [&] {  // the second part of S
       const uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
 #pragma unroll
-      for (int j = 0; j < 32; j += 8) tmem_st8(at + 64 + j, z);
+      for (int j = 0; j < 32; j += 8) tmem_st8(at + C::TM_SECOND + j, z);
     };
     auto finish = [&](float* to) {  // S to memory
       uint32_t a[32];
@@ -676,7 +679,7 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
         }
         if (t0 + (n + 1) * C::C <= t1) {
           fence_proxy_async_smem();  // the tensor store, and the next load of V, come after these
-          mbar_arrive(&sm.stage_full);
+          mbar_arrive(&sm.stage_full[n % C::NV]);
           return;
         }
         // The last chunk, cut by the sequence's end: row by row, 8 x 64 bytes at a time.

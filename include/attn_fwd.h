@@ -519,7 +519,8 @@ attn_status attn_cache_append(const void* q, void* q_out, const void* k, const v
  * their state on.
  *   workspace: attn_linear_workspace_bytes() bytes (may be 0, then NULL will do; tokens: all
  *   rows, B * L or total), 16-byte aligned; nothing in it has to be set, and calls that may overlap on the GPU
- *   each need one.  Results do not depend on what else runs.
+ *   each need one.  Results do not depend on what else runs.  Like the calls above these can be
+ *   captured into a graph, after a first call of the kind (which loads kernels).
  */
 size_t attn_linear_workspace_bytes(int B, int Hq, int max_seqlen, int64_t tokens, int d);
 attn_status attn_linear_fwd(const void* q, const void* k, const void* v, void* o, const float* log_decay,
