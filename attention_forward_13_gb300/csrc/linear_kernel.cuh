@@ -80,7 +80,7 @@ struct LinearSmem {
   // d[31 - lane + j] with d[m] = w^(31 - m) or 0.  Four copies, the c-th shifted by c, so that every
   // lane reads 16 aligned bytes; 72 floats apart, so that 8 lanes meet no bank twice.
   float diag[4][72];
-  uint64_t qk_full[2], qk_empty[2], v_full[C::NV], v_empty[C::NV];
+  uint64_t qk_full[2], k_empty[2], q_empty[2], v_full[C::NV], v_empty[C::NV];
   uint64_t s_full[2], p_full[2];
   uint64_t stage_full[C::NV];
   uint64_t o_full, o_empty, ready, init, kv_done, teardown;
@@ -147,8 +147,9 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
   }
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.qk_full[i], 1);
-      mbar_init(&sm.qk_empty[i], 1);
+      mbar_init(&sm.qk_full[i], STATES ? 1 : 2);
+      mbar_init(&sm.k_empty[i], 1);
+      mbar_init(&sm.q_empty[i], 1);
       mbar_init(&sm.s_full[i], 1);
       mbar_init(&sm.p_full[i], 256);
     }
@@ -225,13 +226,19 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
       auto row_of = [&](int n) { return row0 + t0 + n * C::C; };
       for (int n = 0; n < chunks; ++n) {
         const int s = n & 1, sv = n % C::NV;
-        if (!(ok = w.wait(&sm.qk_empty[s], ((n >> 1) & 1) ^ 1, kErrLinearWait))) break;
-        mbar_arrive_expect_tx(&sm.qk_full[s], STATES ? C::TILE : 2 * C::TILE);
+        // (K is free once K^T V' is done, Q after Q S.)
+        if (!(ok = w.wait(&sm.k_empty[s], ((n >> 1) & 1) ^ 1, kErrLinearWait))) break;
+        mbar_arrive_expect_tx(&sm.qk_full[s], C::TILE);
         ++qk_armed;
 #pragma unroll
-        for (int c = 0; c < C::NCHUNK; ++c) {
+        for (int c = 0; c < C::NCHUNK; ++c)
           tma_load_4d(sm.k[s] + c * C::ATOM, &p.tm_k, &sm.qk_full[s], c * 64, row_of(n), hk, bc);
-          if constexpr (!STATES) tma_load_4d(sm.q[s] + c * C::ATOM, &p.tm_q, &sm.qk_full[s], c * 64, row_of(n), h, bc);
+        if constexpr (!STATES) {
+          if (!(ok = w.wait(&sm.q_empty[s], ((n >> 1) & 1) ^ 1, kErrLinearWait))) break;
+          mbar_arrive_expect_tx(&sm.qk_full[s], C::TILE);
+#pragma unroll
+          for (int c = 0; c < C::NCHUNK; ++c)
+            tma_load_4d(sm.q[s] + c * C::ATOM, &p.tm_q, &sm.qk_full[s], c * 64, row_of(n), h, bc);
         }
         if (!(ok = w.wait(&sm.v_empty[sv], ((n / C::NV) & 1) ^ 1, kErrLinearWait))) break;
         mbar_arrive_expect_tx(&sm.v_full[sv], C::ATOM);
@@ -291,9 +298,10 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
       }
       umma_commit_warp(&sm.kv_done, lead);
       if constexpr (STATES) {
-        umma_commit_warp(&sm.qk_empty[s], lead);
+        umma_commit_warp(&sm.k_empty[s], lead);
         umma_commit_warp(&sm.v_empty[n % C::NV], lead);
       } else {
+        umma_commit_warp(&sm.k_empty[s], lead);
         // Q S, once the o of the chunk before has been read
         if (n > 0) {
           if (!(ok = w.wait(&sm.o_empty, (n - 1) & 1, kErrLinearWait))) break;
@@ -303,7 +311,7 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
         for (int i = 0; i < D / 16; ++i)
           umma_ss_warp(tmem + C::TM_QS, qd0 + static_cast<uint64_t>(s * (C::TILE >> 4) + (((i >> 2) * C::ATOM + (i & 3) * 32) >> 4)),
                        sbd + ((i * 16 * 128) >> 4), id_pv, i > 0 ? 1u : 0u, lead);
-        umma_commit_warp(&sm.qk_empty[s], lead);
+        umma_commit_warp(&sm.q_empty[s], lead);
         if (n + 1 < chunks) {
           if (!(ok = w.wait(&sm.qk_full[s ^ 1], ((n + 1) >> 1) & 1, kErrLinearWait))) break;
           if (n + 1 == partial && !(ok = w.wait(&sm.ready, (n + 1) & 1, kErrLinearWait))) break;
@@ -612,7 +620,7 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
         }
         if (!ok) return false;
         // (Q S of the chunk before has read the operand.)
-        if (n > 0) ok = __all_sync(0xffffffffu, w.wait(&sm.qk_empty[(n - 1) & 1], ((n - 1) >> 1) & 1, kErrLinearWait));
+        if (n > 0) ok = __all_sync(0xffffffffu, w.wait(&sm.q_empty[(n - 1) & 1], ((n - 1) >> 1) & 1, kErrLinearWait));
         if (!ok) return !BF16;
         const int m = t1 - t0 - n * C::C;
         const float f = m >= C::C ? full : decay_pow(log2w, m);
