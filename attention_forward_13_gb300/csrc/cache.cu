@@ -628,7 +628,8 @@ __global__ void __launch_bounds__(128) compact_move_kernel(const CompactParams p
 // ---------------------------------------------------------------------------
 // Slot map: where the new tokens of every sequence go, in packed order.  Latency
 // bound: one launch, each CTA sums the counts for itself (8192 of them: 16 rounds
-// of the block) and finds its tokens' sequences by bisection in shared memory.
+// of the block) and finds its tokens' sequences by bisection in shared memory.  64 tokens
+// 2.6 us, 66,000 of 256 sequences 3.6.
 struct SlotsParams {
   const int32_t *table, *seqlens, *add;
   int32_t *slots, *positions, *cu, *sequence;

