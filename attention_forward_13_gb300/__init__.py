@@ -93,13 +93,13 @@ def _stream(stream):
 
 def _call(fn, device, *args):
     """Calls a library function whose last argument is the stream: ``device``'s current one."""
-    if device.type != "cuda":
+    index = device.index
+    if index is None or device.type != "cuda":
         raise ValueError("the tensors must be on a CUDA device")
-    here = _current_device()
-    if device.index != here:
+    if index != _current_device():
         with torch.cuda.device(device):
             return fn(*args, _stream(None))
-    return fn(*args, _raw_stream(here) if _raw_stream is not None else _stream(None))
+    return fn(*args, _raw_stream(index) if _raw_stream is not None else _stream(None))
 
 
 def _opts(scale, causal, softcap, sink, window=None, top_left=False, alibi=None, bias=None,
@@ -175,6 +175,8 @@ def _on_stream(fn):
 
     @functools.wraps(fn)
     def call(*args, **kwargs):
+        if "stream" not in kwargs and len(args) <= at:
+            return fn(*args, **kwargs)
         stream = kwargs.pop("stream", None)
         if len(args) > at:
             stream, args = args[at], args[:at] + (None,) + args[at + 1:]
