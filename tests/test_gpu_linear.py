@@ -324,3 +324,30 @@ def test_outputs_over_inputs_refused(form):
             else:
                 A.attn_linear_step(q[:, :, 0], k[:, :, 0], v[:, :, 0], g, state, o=x[:, :, 0])
     no_device_error()
+
+
+def test_packed_without_rows():
+    """No rows at all: the states are handed on."""
+    e = torch.zeros(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    cu = torch.zeros(4, dtype=torch.int32, device="cuda")
+    state = torch.randn(3, 2, 64, 64, device="cuda")
+    o, S = A.attn_linear_fwd_varlen(e, e, e, cu, 0, decays(2), state=state)
+    assert o.shape == e.shape and torch.equal(S, state)
+    no_device_error()
+
+
+def test_lengths_past_the_given_most():
+    """max_seqlen below a sequence's length costs balance, not results; cu_seqlens past the rows are cut there."""
+    q, k, v, _ = make(44, 1, 1500, 2, 2, 64, torch.bfloat16, state=False)
+    q, k, v = (x[0].transpose(0, 1).contiguous() for x in (q, k, v))
+    g = decays(2)
+    cu = torch.tensor([0, 1500], dtype=torch.int32, device="cuda")
+    want, S = A.attn_linear_fwd_varlen(q, k, v, cu, 1500, g)
+    for most, ends in ((600, [0, 1500]), (1500, [0, 1 << 30]), (2000, [0, 1500, 1499])):
+        c = torch.tensor(ends, dtype=torch.int32, device="cuda")
+        o, T = A.attn_linear_fwd_varlen(q, k, v, c, most, g)
+        x = [t.transpose(0, 1)[None] for t in (q, k, v)]
+        check(o.transpose(0, 1), T[0], plain(*x, g, 0.125, None)[0], (most, ends))
+        if len(ends) == 3:
+            assert not T[1].any()
+    no_device_error()
