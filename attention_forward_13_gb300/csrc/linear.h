@@ -78,8 +78,9 @@ __device__ __forceinline__ void sequence_rows(const LinearParams& p, int b, int&
   len = p.L;
   if (p.cu != nullptr) {
     const int first = p.cu[b], last = p.cu[b + 1];
+    // (Compared before they are subtracted: an end far below 0 would leave 32 bits.)
     row0 = first;
-    len = first < 0 || first > p.total ? 0 : max(0, min(last, p.total) - first);
+    len = first < 0 || last <= first || first >= p.total ? 0 : min(last, p.total) - first;
   }
 }
 
