@@ -202,6 +202,7 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
   if ((t0 >= len && seg > 0) || (STATES && last)) return;
   const int chunks = (t1 - t0 + C::C - 1) / C::C;
   const float log2w = p.log_decay[h] * kLog2e;
+  const bool grows = log2w > 0.0f;
   if (tid < 32) sm.col[tid] = decay_pow(log2w, 31 - tid);
   if (tid >= 64 && tid < 64 + 4 * 72) {
     const int c = (tid - 64) / 72, m = (tid - 64) % 72 + c;
@@ -416,6 +417,8 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
       fence_proxy_async_smem();
       mbar_arrive(&sm.ready);
     };
+    // The decay from the last token of block cb down to row r, right of it.
+    auto row_decay = [&](int cb) { return exp2f(log2w * (lane + 1 + 32 * (wq - 1 - cb))); };
     // P_ij = scale w^(i-j) q_i . k_j in blocks of 32 columns, thread = row i = r: blocks part
     // and part + 2, of which those right of the diagonal one are 0.  False: all threads that
     // share a barrier leave.
@@ -427,7 +430,9 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
       float f = p.scale;
       if constexpr (!BF16) {
         // fp16: the row's largest score decides a power of two that fits its weights (at
-        // most 2^11: room for decays a little above 1, and 2^35 below for the small).
+        // most 2^11, and 2^35 below for the small).  Decays above 1 make any multiple of a
+        // score: then the scores of 16 columns at a time count with the largest decay there (at
+        // most w^15 more than their own; below 2^15, so that the largest weight lies above w^-15 2^14).
         float m = 0.0f;
         if (ok) {
 #pragma unroll 1
@@ -440,16 +445,26 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
 #pragma unroll
               for (int j = 0; j < 32; ++j) x[j] = j <= lane ? x[j] : 0u;
             }
+            float m0 = 0.0f, m1 = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 32; j += 2)
-              m = fmax3(m, fabsf(__uint_as_float(x[j])), fabsf(__uint_as_float(x[j + 1])));
+            for (int j = 0; j < 16; j += 2) {
+              m0 = fmax3(m0, fabsf(__uint_as_float(x[j])), fabsf(__uint_as_float(x[j + 1])));
+              m1 = fmax3(m1, fabsf(__uint_as_float(x[j + 16])), fabsf(__uint_as_float(x[j + 17])));
+            }
+            if (grows) {
+              const float* c = cb < wq ? sm.col : diag;
+              const float down = cb < wq ? row_decay(cb) : 1.0f;
+              m0 *= c[0] * down;
+              m1 *= c[16] * down;
+            }
+            m = fmax3(m, m0, m1);
           }
         }
         sm.row_max[n & 1][part][r] = static_cast<uint8_t>(exponent_of(m * p.scale));
         // (The two warps of a row come here, aborted or not, and leave together.)
         ok = !named_bar_or(2 + wq, 64, !ok);
         if (!ok) return false;
-        const int e = fit(max(sm.row_max[n & 1][0][r], sm.row_max[n & 1][1][r]), 11);
+        const int e = fit(max(sm.row_max[n & 1][0][r], sm.row_max[n & 1][1][r]), grows ? 15 : 11);
         if (part == 0) sm.row_scale[n & 3][r] = static_cast<int8_t>(e);
         f *= two_to(-e);
       }
@@ -464,7 +479,7 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
           tmem_ld32(base + 32 * cb, x);
           // w^(i-j): left of the diagonal block the row's power down to the block's last
           // column times the column's from there, in it the table's.
-          const float rowf = cb < wq ? f * exp2f(log2w * (lane + 1 + 32 * (wq - 1 - cb))) : f;
+          const float rowf = cb < wq ? f * row_decay(cb) : f;
           const float4* c4 = reinterpret_cast<const float4*>(cb < wq ? sm.col : diag);
           const uint64_t f2 = f2_pack(rowf, rowf);
           tmem_ld_wait();
