@@ -32,9 +32,10 @@
 //
 // Roundings to 16 bits: P and the operand copy of S, each at most half a step of
 // the type, as o itself is.  The state proper stays in 32 bits in tensor memory, and what is added
-// to it is V' in two pieces (v' = hi + lo, lo's own rounding 2^-18 of v' in bf16): one piece would
-// put a 16-bit error into a 32-bit result that later calls build on.  fp16 has no room for either
-// operand's range: the rows of P and the copy of S are scaled by powers of two to fit.
+// to it is V' in two pieces (v' = hi + lo, lo's own rounding 2^-18 of v' in bf16; in fp16 2^-21 of it, or
+// 2^-35): one piece would put a 16-bit error into a 32-bit result that later calls build on.  fp16 has no
+// room for the operands' ranges: the rows of P, the copy of S and the second piece of V' are scaled by
+// powers of two to fit.
 //
 // Few sequences and heads leave SMs idle.  Then the chunks are cut into segments
 // (linear_segments in linear.h): a first launch (STATES) adds up the state every segment
@@ -126,12 +127,21 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
   else asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-template <bool BF16>
-__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
-  if constexpr (BF16) asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  else asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
   return d;
+}
+
+// fp16: what the second piece of V' is multiplied by.  (It is at most a step of the first
+// one, 32: room for 2^10.)
+constexpr float kSecondScale = 1024.0f;
+// a -= kSecondScale x, for both fp16 halves of x.
+__device__ __forceinline__ void subtract_scaled(uint32_t x, float& a0, float& a1) {
+  asm("{\n .reg .b16 x0, x1, m;\n mov.b32 {x0, x1}, %2;\n mov.b16 m, 0xe400;\n"
+      " fma.rn.f32.f16 %0, x0, m, %0;\n fma.rn.f32.f16 %1, x1, m, %1;\n}\n"
+      : "+f"(a0), "+f"(a1)
+      : "r"(x));
 }
 
 template <int D, bool BF16, bool STATES>
@@ -362,7 +372,10 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
     // the first launch the segment's.  Thread = token r, 32 columns.  In packed 16-bit
     // arithmetic: with the weight f = f1 + f2 in two pieces, hi = f1 v rounded, f1 v - hi is exact
     // (a product of two significands less its upper half), and lo = that + f2 v: f2's and lo's
-    // roundings are 2^-18 of v' each in bf16.
+    // roundings are 2^-18 of v' each in bf16.  fp16 has not the exponents for that: lo = f v - hi
+    // comes from 32 bits, where it is exact, and is held at 2^10 of its size, rounded to 2^-21 of
+    // v', or among the subnormal numbers to 2^-35 (2 x 8192 tokens of 32 heads: 118 us with a lo
+    // of its own size, whose error is 2^-24 however small v is, 128 with this one).
     auto values = [&](int n) {
       const int sv = n % C::NV;
       ok = __all_sync(0xffffffffu, w.wait(&sm.v_full[sv], (n / C::NV) & 1, kErrLinearWait));
@@ -374,11 +387,11 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
                                               : 0.0f;
       uint8_t* src = sm.v[sv] + r * 128;
       uint32_t hi[16], lo[16];
-      float f1, f2, unused;
+      float f1, unused;
       const uint32_t fw = pack16<BF16>(f, f);
       unpack16<BF16>(fw, f1, unused);
-      f2 = f - f1;
-      const uint32_t gw = pack16<BF16>(f2, f2);
+      const uint32_t gw = pack_bf16(f - f1, f - f1);
+      const uint64_t up = f2_pack(f * kSecondScale, f * kSecondScale);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint4 x = *reinterpret_cast<const uint4*>(src + (((4 * part + i) ^ (r & 7)) << 4));
@@ -386,8 +399,17 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint32_t v2 = r < live ? in[e] : 0u;  // (rows of nobody may hold anything)
-          hi[4 * i + e] = mul2<BF16>(v2, fw);
-          lo[4 * i + e] = fma2<BF16>(v2, gw, fma2<BF16>(v2, fw, hi[4 * i + e] ^ 0x80008000u));
+          const uint32_t first = mul2<BF16>(v2, fw);
+          hi[4 * i + e] = first;
+          if constexpr (BF16) {
+            lo[4 * i + e] = fma_bf16x2(v2, gw, fma_bf16x2(v2, fw, first ^ 0x80008000u));
+          } else {
+            float x, y;
+            unpack16<BF16>(v2, x, y);
+            f2_unpack(f2_mul(f2_pack(x, y), up), x, y);
+            subtract_scaled(first, x, y);
+            lo[4 * i + e] = pack16<BF16>(x, y);
+          }
         }
       }
       if (live < C::C) {
@@ -585,8 +607,10 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
 #pragma unroll
       for (int j = 0; j < 32; j += 2) {
         float x, y;
-        f2_unpack(f2_add(f2_pack(__uint_as_float(a[j]), __uint_as_float(a[j + 1])),
-                         f2_pack(__uint_as_float(c[j]), __uint_as_float(c[j + 1]))), x, y);
+        const uint64_t first = f2_pack(__uint_as_float(a[j]), __uint_as_float(a[j + 1]));
+        const uint64_t second = f2_pack(__uint_as_float(c[j]), __uint_as_float(c[j + 1]));
+        f2_unpack(BF16 ? f2_add(first, second) : f2_fma(second, f2_pack(1.0f / kSecondScale, 1.0f / kSecondScale), first),
+                  x, y);
         a[j] = __float_as_uint(x);
         a[j + 1] = __float_as_uint(y);
       }
