@@ -213,6 +213,8 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
   const int chunks = (t1 - t0 + C::C - 1) / C::C;
   const float log2w = p.log_decay[h] * kLog2e;
   const bool grows = log2w > 0.0f;
+  // fp16 has no room for weights above 1: those of V' are then taken back to the chunk's start.
+  const bool back = !STATES && !BF16 && grows;
   if (tid < 32) sm.col[tid] = decay_pow(log2w, 31 - tid);
   if (tid >= 64 && tid < 64 + 4 * 72) {
     const int c = (tid - 64) / 72, m = (tid - 64) % 72 + c;
@@ -365,11 +367,12 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
     // ===================== values and weights =====================================
     const int part = warp >> 2, wq = warp & 3, r = wq * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
-    const float full = decay_pow(log2w, C::C - 1 - r);
+    const float full = back ? decay_pow(-log2w, r + 1) : decay_pow(log2w, C::C - 1 - r);
     const float* diag = &sm.diag[(31 - lane) & 3][(31 - lane) & ~3];
     bool ok = true;
     // V' = w^(tokens behind it) v: up to where the state is wanted, the chunk's end and in
-    // the first launch the segment's.  Thread = token r, 32 columns.  In packed 16-bit
+    // the first launch the segment's; with `back` w^-(tokens up to it) v, and the state is multiplied
+    // by w^(tokens of the chunk) when it is read.  Thread = token r, 32 columns.  In packed 16-bit
     // arithmetic: with the weight f = f1 + f2 in two pieces, hi = f1 v rounded, f1 v - hi is exact
     // (a product of two significands less its upper half), and lo = that + f2 v: f2's and lo's
     // roundings are 2^-18 of v' each in bf16.  fp16 has not the exponents for that: lo = f v - hi
@@ -382,9 +385,9 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
       if (!ok) return;
       const int left = t1 - t0 - n * C::C;  // tokens from this chunk on
       const int live = min(left, C::C);
-      const float f = !STATES && live == C::C ? full
-                      : r < live              ? decay_pow(log2w, (STATES ? left : live) - 1 - r)
-                                              : 0.0f;
+      const float f = r >= live                          ? 0.0f
+                      : back || (!STATES && live == C::C) ? full
+                                                          : decay_pow(log2w, (STATES ? left : live) - 1 - r);
       uint8_t* src = sm.v[sv] + r * 128;
       uint32_t hi[16], lo[16];
       float f1, unused;
@@ -596,7 +599,7 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
         tmem_st_wait();
       }
     }
-    // Both parts of S.
+    // Both parts of S (with `back`, before the decays of the chunk that was added last).
     auto read = [&](uint32_t (&a)[32]) {
       uint32_t c[32];
       tmem_ld32(at, a);
@@ -624,6 +627,11 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
       uint32_t a[32];
       read(a);
       if (!mine) return;
+      if (back) {
+        const float f = chunks > 0 ? decay_pow(log2w, t1 - t0 - (chunks - 1) * C::C) : 1.0f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) a[j] = __float_as_uint(__uint_as_float(a[j]) * f);
+      }
 #pragma unroll
       for (int j = 0; j < 32; j += 4) *reinterpret_cast<uint4*>(to + j) = make_uint4(a[j], a[j + 1], a[j + 2], a[j + 3]);
     };
@@ -641,6 +649,7 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
         if (ok && n > 0) reach(&sm.kv_done, n - 1);
         uint32_t a[32];
         if (ok) read(a);
+        const float since_read = back && n > 0 ? full : 1.0f;
         float down = 1.0f;
         if constexpr (!BF16) {
           // fp16: one power of two for the whole operand, its largest element below 2^15.
@@ -649,7 +658,7 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
 #pragma unroll
             for (int j = 0; j < 32; j += 2)
               m = fmax3(m, fabsf(__uint_as_float(a[j])), fabsf(__uint_as_float(a[j + 1])));
-          const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+          const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(m * since_read));
           if (lane == 0) sm.part[n & 1][warp - 8] = top;
           // (Every thread comes here, aborted or not, and all leave together.)
           ok = !named_bar_or(1, 256, !ok);
@@ -658,14 +667,14 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
           for (int i = 0; i < 8; ++i) all = max(all, sm.part[n & 1][i]);
           const int e = fit(exponent_of(__uint_as_float(all)), 15);
           if (warp == 8 && lane == 0) sm.state_scale[n & 3] = e;
-          down = two_to(-e);
+          down = two_to(-e) * since_read;
         }
         if (!ok) return false;
         // (Q S of the chunk before has read the operand.)
         if (n > 0) ok = __all_sync(0xffffffffu, w.wait(&sm.q_empty[(n - 1) & 1], ((n - 1) >> 1) & 1, kErrLinearWait));
         if (!ok) return !BF16;
         const int m = t1 - t0 - n * C::C;
-        const float f = m >= C::C ? full : decay_pow(log2w, m);
+        const float f = back ? since_read : m >= C::C ? full : decay_pow(log2w, m);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           uint32_t x[4];

@@ -39,3 +39,27 @@ def test_weights_of_a_chunk(dt, g, L, d):
     o, _, want = run(q, k, v, torch.tensor([g, g / 2], device="cuda"), states=False)
     check(o, None, want, (dt, g, L, d))
     no_device_error()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("L", [1, 40, 128, 129, 300, 384])
+@pytest.mark.parametrize("g", [0.01, 0.05, 0.08])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_states(dt, g, L, d):
+    """Over several chunks, from a state and from none, and from chunk to chunk in place."""
+    q, k, v, state = make(L + d, 2, L, d, DT[dt], state=True)
+    g = torch.tensor([g, -0.02], device="cuda")
+    for s in (state, None):
+        o, S, want = run(q, k, v, g, s)
+        check(o, S, want, (dt, L, d))
+    no_device_error()
+
+
+def test_the_first_tokens_are_padding():
+    """Zeros at the front, which the largest weights meet."""
+    q, k, v, _ = make(5, 2, 300, 64, torch.float16)
+    for x in (k, v):
+        x[:, :, :120] = 0
+    o, S, want = run(q, k, v, torch.tensor([0.05, 0.1], device="cuda"))
+    check(o, S, want)
+    no_device_error()
