@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
     mbar_init(&sm.o_full, 1);
     mbar_init(&sm.o_empty, 256);
     mbar_init(&sm.ready, STATES ? 256 : 512);  // V', and (not STATES) S as an operand and decayed
-    mbar_init(&sm.init, 256);                  // (STATES) the state the segment starts from
+    mbar_init(&sm.init, 256);                  // (STATES) the state the segment (by_chunk: the chunk) starts from
     mbar_init(&sm.kv_done, 1);
     mbar_init(&sm.teardown, 1);
     sm.abort_flag = 0;
@@ -214,7 +214,10 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
   const float log2w = p.log_decay[h] * kLog2e;
   const bool grows = log2w > 0.0f;
   // fp16 has no room for weights above 1: those of V' are then taken back to the chunk's start.
-  const bool back = !STATES && !BF16 && grows;
+  const bool back = !BF16 && grows;
+  // Decays above 1 leave fp32 over a segment, so that the first launch carries them from chunk
+  // to chunk as the second does.
+  const bool by_chunk = !STATES || grows;
   if (tid < 32) sm.col[tid] = decay_pow(log2w, 31 - tid);
   if (tid >= 64 && tid < 64 + 4 * 72) {
     const int c = (tid - 64) / 72, m = (tid - 64) % 72 + c;
@@ -304,7 +307,7 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
       const int s = n & 1;
       // S += K^T V'
       if (!(ok = w.wait(&sm.ready, n & 1, kErrLinearWait))) break;
-      if (STATES && n == 0 && !(ok = w.wait(&sm.init, 0, kErrLinearWait))) break;
+      if (STATES && (n == 0 || grows) && !(ok = w.wait(&sm.init, n & 1, kErrLinearWait))) break;
       if (STATES && !(ok = w.wait(&sm.qk_full[s], (n >> 1) & 1, kErrLinearWait))) break;
       tc_fence_after();
 #pragma unroll
@@ -385,9 +388,9 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
       if (!ok) return;
       const int left = t1 - t0 - n * C::C;  // tokens from this chunk on
       const int live = min(left, C::C);
-      const float f = r >= live                          ? 0.0f
-                      : back || (!STATES && live == C::C) ? full
-                                                          : decay_pow(log2w, (STATES ? left : live) - 1 - r);
+      const float f = r >= live                            ? 0.0f
+                      : back || (by_chunk && live == C::C) ? full
+                                                           : decay_pow(log2w, (by_chunk ? live : left) - 1 - r);
       uint8_t* src = sm.v[sv] + r * 128;
       uint32_t hi[16], lo[16];
       float f1, unused;
@@ -579,6 +582,19 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
           if (STATES && mine)
 #pragma unroll
             for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4*>(copy + i) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+        } else if (!STATES && seg > 0 && grows) {
+          // (w^seg_len in steps that fp32 holds: what is 0 stays 0, whatever it is.)
+          const float e = log2w * seg_len;
+#pragma unroll 1
+          for (int i = 0; i < seg; ++i) {
+#pragma unroll 1
+            for (int j = 0; i > 0 && j < 3; ++j) {
+              const float f = exp2f(fminf(fmaxf(e - 126.0f * j, 0.0f), 126.0f));
+#pragma unroll
+              for (int x = 0; x < 32; ++x) s[x] *= f;
+            }
+            add(p.work + i * work_seg + row_at, 1.0f);
+          }
         } else if (!STATES && seg > 0) {
 #pragma unroll 1
           for (int i = seg - 1; i >= 0; --i) {
@@ -588,7 +604,7 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
           }
         }
         __syncwarp();
-        const float f = STATES ? decay_pow(log2w, t1 - t0) : 1.0f;
+        const float f = by_chunk ? 1.0f : decay_pow(log2w, t1 - t0);
         uint32_t a[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) a[j] = __float_as_uint(s[j] * f);
@@ -636,9 +652,25 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
       for (int j = 0; j < 32; j += 4) *reinterpret_cast<uint4*>(to + j) = make_uint4(a[j], a[j + 1], a[j + 2], a[j + 3]);
     };
     if constexpr (STATES) {
-      tc_fence_before();
-      mbar_arrive(&sm.init);
-      reach(&sm.o_full, 0);
+#pragma unroll 1
+      for (int n = 0; n < (grows ? chunks : 1); ++n) {
+        if (grows) {
+          if (n > 0) reach(&sm.kv_done, n - 1);
+          if (!ok) break;
+          uint32_t a[32];
+          read(a);
+          // (Chunks of this launch are whole.)
+          const float f = back && n == 0 ? 1.0f : decay_pow(log2w, C::C);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) a[j] = __float_as_uint(__uint_as_float(a[j]) * f);
+          tmem_st32(at, a);
+          clear2();
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        mbar_arrive(&sm.init);
+      }
+      if (ok) reach(&sm.o_full, 0);
       if (ok) finish(p.work + seg * work_seg + row_at);
     } else {
       const float full = decay_pow(log2w, C::C), since = p.scale * decay_pow(log2w, r + 1);
