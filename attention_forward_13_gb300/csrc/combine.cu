@@ -67,7 +67,11 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const CombineParams p
            lane * VPL;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) dst[i] = T(acc[i] * inv);
-  if (lane == 0 && p.lse != nullptr) p.lse[r] = (z != 0.0f) ? (m2 + log2f(z)) * kLn2 : -INFINITY;
+  if (lane == 0 && p.lse != nullptr) {
+    // (Where the sink alone is left the row has its LSE, not what comes back from log2 units.)
+    const bool sink_only = p.sink != nullptr && m == -INFINITY && z == 1.0f;
+    p.lse[r] = sink_only ? p.sink[h] : (z != 0.0f) ? (m2 + log2f(z)) * kLn2 : -INFINITY;
+  }
 }
 
 cudaError_t launch_combine(const CombineParams& p, bool bf16, cudaStream_t stream, char* name,
