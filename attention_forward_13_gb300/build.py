@@ -20,7 +20,7 @@ SOURCES = ["prefill_d128.cu", "prefill_d64.cu", "prefill_keep_d128.cu", "prefill
            "api.cu", "tree_api.cu", "cache.cu", "paged_noalloc.cu", "rope.cu", "linear_api.cu",
            "linear_d128.cu", "linear_d64.cu"]
 HEADERS = ["ptx.cuh", "common.cuh", "softmax.cuh", "launch.h", "host.h", "pages.h", "prefill_kernel.cuh",
-           "decode_kernel.cuh", "tree_kernel.cuh", "linear.h", "linear_kernel.cuh"]
+           "decode_kernel.cuh", "tree_kernel.cuh", "linear.h", "linear_kernel.cuh", "overlap.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v"]
 

@@ -3,6 +3,7 @@
 #include "host.h"
 #include "launch.h"
 #include "linear.h"
+#include "overlap.h"
 #include "ptx.cuh"
 
 #include <algorithm>
@@ -117,6 +118,15 @@ bool strides_ok(const attn_strides& s, bool row, bool batch) {
          (!batch || (s.batch > 0 && s.batch % 8 == 0));
 }
 
+// Whether o shares memory with an input (CTAs of a head read what others have written).
+bool over_inputs(const void* q, const void* k, const void* v, const void* o, const attn_strides& sq,
+                 const attn_strides& sk, const attn_strides& sv, const attn_strides& so, int B, int Hq, int Hkv, int rows,
+                 int d) {
+  const Extent out{o, so, {B, Hq, rows}, d};
+  return o == q || o == k || o == v || overlap(out, {q, sq, {B, Hq, rows}, d}) ||
+         overlap(out, {k, sk, {B, Hkv, rows}, d}) || overlap(out, {v, sv, {B, Hkv, rows}, d});
+}
+
 // What all three entry points ask of their sizes, types and states.
 attn_status check_common(const float* log_decay, const float* state_in, const float* state_out, const int32_t* index,
                          int num_states, int B, int Hq, int Hkv, int d, attn_dtype dtype, float scale) {
@@ -129,6 +139,11 @@ attn_status check_common(const float* log_decay, const float* state_in, const fl
     return ATTN_ERR_INVALID;
   if (state_in != nullptr || state_out != nullptr) {
     if (num_states <= 0 || (index == nullptr && num_states < B)) return ATTN_ERR_INVALID;
+    // (One state is read while another is written: the same buffer, or two.)
+    const uintptr_t in = reinterpret_cast<uintptr_t>(state_in), out = reinterpret_cast<uintptr_t>(state_out);
+    const uint64_t bytes = sizeof(float) * static_cast<uint64_t>(num_states) * Hq * d * d;
+    if (state_in != nullptr && state_out != nullptr && in != out && in < out + bytes && out < in + bytes)
+      return ATTN_ERR_INVALID;
   }
   return ATTN_OK;
 }
@@ -144,10 +159,10 @@ attn_status linear_fwd(const void* q, const void* k, const void* v, void* o, con
   if (rows > 0) {
     for (const void* x : {q, k, v, static_cast<const void*>(o)})
       if (x == nullptr || !host_aligned(x, 16)) return ATTN_ERR_INVALID;
-    if (o == q || o == k || o == v) return ATTN_ERR_INVALID;  // (CTAs of a head read what others have written)
     const bool batches = cu == nullptr && B > 1;
     for (const attn_strides* s : {&sq, &sk, &sv, &so})
       if (!strides_ok(*s, true, batches)) return ATTN_ERR_INVALID;
+    if (over_inputs(q, k, v, o, sq, sk, sv, so, cu == nullptr ? B : 1, Hq, Hkv, rows, d)) return ATTN_ERR_INVALID;
     const uint32_t box[4] = {64, kLinearChunk, 1, 1};
     auto map = [&](CUtensorMap* m, const void* base, const attn_strides& s, int heads) {
       const uint64_t dims[4] = {(uint64_t)d, (uint64_t)rows, (uint64_t)heads, cu != nullptr ? 1u : (uint64_t)B};
@@ -239,9 +254,9 @@ attn_status attn_linear_step(const void* q, const void* k, const void* v, void* 
   if (st != ATTN_OK || B == 0) return st;
   for (const void* x : {q, k, v, static_cast<const void*>(o), static_cast<const void*>(state)})
     if (x == nullptr || !host_aligned(x, 16)) return ATTN_ERR_INVALID;
-  if (o == q || o == k || o == v) return ATTN_ERR_INVALID;
   for (const attn_strides* s : {&sq, &sk, &sv, &so})
     if (!strides_ok(*s, false, B > 1)) return ATTN_ERR_INVALID;
+  if (over_inputs(q, k, v, o, sq, sk, sv, so, B, Hq, Hkv, 1, d)) return ATTN_ERR_INVALID;
   StepParams p{q, k, v, o, log_decay, state, state_index, num_states, Hq, Hq / Hkv,
                sq.batch, sq.head, sk.batch, sk.head, sv.batch, sv.head, so.batch, so.head,
                scale > 0.0f ? scale : 1.0f / sqrtf(static_cast<float>(d)), nullptr};

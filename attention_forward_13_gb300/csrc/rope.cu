@@ -18,6 +18,7 @@
 // as many bytes takes 51.8).
 #include "host.h"
 #include "launch.h"
+#include "overlap.h"
 #include "ptx.cuh"
 
 #include <algorithm>
@@ -326,6 +327,22 @@ attn_status launch(RopeParams& p, bool bf16, cudaStream_t stream, const char* na
   return host_finish(e, name);
 }
 
+// Whether a part's output shares memory with an input that other threads read: an input of other
+// rows, or its own other than in place.
+bool over_inputs(const RopeParams& p, int inputs) {
+  const int B = p.tokens / p.L;
+  const auto in = [&](int i) { return Extent{p.part[i].src, p.part[i].in, {B, p.part[i].heads, p.L}, p.d}; };
+  for (int i = 0; i < (p.slots != nullptr ? 1 : 2); ++i) {
+    if (p.part[i].heads == 0) continue;
+    const Extent out{p.part[i].dst, p.part[i].out, {B, p.part[i].heads, p.L}, p.d};
+    for (int j = 0; j < inputs; ++j)
+      if (p.part[j].heads > 0 && !(i == j && same_rows(out, in(j))) && overlap(out, in(j))) return true;
+    const Extent other{p.part[1].dst, p.part[1].out, {B, p.part[1].heads, p.L}, p.d};
+    if (i == 0 && p.slots == nullptr && p.part[1].heads > 0 && overlap(out, other)) return true;
+  }
+  return false;
+}
+
 attn_status check_dim(int d) {
   if (d <= 0) return ATTN_ERR_INVALID;
   return d % 8 != 0 || d > kMaxDim ? ATTN_ERR_UNSUPPORTED : ATTN_OK;
@@ -404,6 +421,7 @@ attn_status attn_rope(const void* q, void* q_out, const void* k, void* k_out, co
   p.tokens = B * L;
   p.L = L;
   p.d = d;
+  if (over_inputs(p, 2)) return ATTN_ERR_INVALID;
   return launch(p, dtype == ATTN_BF16, static_cast<cudaStream_t>(stream), "attn_rope");
 }
 
@@ -443,6 +461,7 @@ attn_status attn_cache_append(const void* q, void* q_out, const void* k, const v
   p.tokens = num_tokens;
   p.L = num_tokens;
   p.d = d;
+  if (over_inputs(p, 3)) return ATTN_ERR_INVALID;
   return launch(p, dtype == ATTN_BF16, static_cast<cudaStream_t>(stream), "attn_cache_append");
 }
 
