@@ -637,8 +637,11 @@ def _rope_opts(inv_freq, d, device, interleaved, inverse, scale):
     if inv_freq.dtype is not torch.float64 or inv_freq.dim() != 1 or inv_freq.device != device or \
             not inv_freq.is_contiguous() or 2 * inv_freq.shape[0] > d:
         raise ValueError("inv_freq must be contiguous fp64 [rotary_dim / 2] on the same device, rotary_dim <= d")
-    return _lib.attn_rope_opts(inv_freq.data_ptr(), 2 * inv_freq.shape[0], 1 if interleaved else 0,
+    opts = _lib.attn_rope_opts(inv_freq.data_ptr(), 2 * inv_freq.shape[0], 1 if interleaved else 0,
                                1 if inverse else 0, float(scale))
+    if opts.scale == 0:  # (in 32 bits: the library's name for 1)
+        raise ValueError("scale must be above 0")
+    return opts
 
 
 def _like(t, out, name):
