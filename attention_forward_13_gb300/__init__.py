@@ -673,7 +673,8 @@ def attn_rope(q, k, inv_freq, positions=None, interleaved=False, inverse=False, 
     """Rotary positions.  q [B,Hq,L,d] and k [B,Hkv,L,d], or packed [N,H,d] (k may be None); the
     first 2 * len(inv_freq) elements of a head turn by position * inv_freq (attn_rope_freqs),
     in halves or interleaved pairs, times ``scale``.  positions int32 [L] or [B,L], packed [N];
-    None: the row.  ``inverse`` turns back.  q_out and k_out may be q and k.  Returns (q_out, k_out)."""
+    None: the row.  ``inverse`` turns back: with the same ``scale`` the transpose, which takes a gradient
+    back; with 1 / scale it undoes the rotation.  q_out and k_out may be q and k.  Returns (q_out, k_out)."""
     shape, dev = q.shape, q.device
     if len(shape) == 4:
         B, Hq, L, d = shape

@@ -3,11 +3,12 @@
 // include/attn_fwd.h states the rules).
 //
 // Pair i of a head turns by the angle position * f_i.  In 32 bits that angle is
-// worthless far out (at position 10^6 its rounding is 0.03 of a turn), so the
+// of little worth far out (at position 10^6 its rounding is 0.03 radians), so the
 // kernels count in turns, in 64-bit fixed point: F_i = frac(f_i / 2 pi) * 2^64 as
 // an integer, and position * F_i modulo 2^64 is the angle modulo a turn, exact
-// but for F_i's own rounding (position * 2^-65 turns, and 2^-53 of f_i itself).
-// Its upper half goes to sincospi, whose argument is then within one turn.
+// but for F_i's own rounding (position * 2^-65 turns, and 2^-52 of f_i: 1 / 2 pi
+// and the product).  Its upper half goes to sincospi, in 32 bits: cut to 2^-32 of
+// a turn and rounded to 2^-25 of a half turn, 2^-23 radians together.
 //
 // Memory bound: every element is read and written once, about 4 operations each.
 // A thread keeps the cosines and sines of its 8 pairs of one token and walks over
@@ -123,10 +124,6 @@ __device__ __forceinline__ int64_t slot_of(const RopeParams& p, int token) {
   return -1;
 }
 
-// Rows of which both halves of every pair lie in whole 16-byte pieces (rot a
-// multiple of 16): a thread owns two pieces, 8 pairs, or one piece behind the
-// rotated elements.  Neighbouring threads take neighbouring pieces of a row, then
-// the next token's.
 // This CTA's run of the (tile, head) list: the tile, and heads [h0, h1) of it, then
 // the next tile's.  (A tile has as many tokens as the CTA has rows of threads.)
 struct Run {
@@ -145,6 +142,10 @@ struct Run {
   }
 };
 
+// Rows of which both halves of every pair lie in whole 16-byte pieces (rot a
+// multiple of 16): a thread owns two pieces, 8 pairs, or one piece behind the
+// rotated elements.  Neighbouring threads take neighbouring pieces of a row, then
+// the next token's.
 template <bool BF16, bool INTER>
 __global__ void __launch_bounds__(kThreads, kPerSm) rope_pairs_kernel(const RopeParams p) {
   __shared__ unsigned long long freq[kMaxDim / 2];

@@ -437,9 +437,10 @@ attn_status attn_cache_slots(const int32_t* block_table, const int32_t* seqlens,
  * Rotary positions.  Elements 2i, 2i + 1 (interleaved) or i, i + rotary_dim / 2 of
  * a head's first rotary_dim form pair i, which turns by a = position * inv_freq[i]:
  *   (x, y) -> scale * (x cos a - y sin a, y cos a + x sin a),
- * by -a with `inverse` (which undoes it, and with the same scale is also its
- * gradient).  Elements from rotary_dim on are copied as they are.  Angles are
- * exact to 2^-53 of inv_freq at any int32 position; negative ones turn back.
+ * by -a with `inverse`: with the same scale that is the transpose, which takes a gradient
+ * back, and with 1 / scale it undoes the rotation.  Elements from rotary_dim on are copied as
+ * they are.  Positions are any int32, negative ones turn back.  The angle modulo a turn is
+ * off by at most |position| * (2^-52 inv_freq + 2^-64 pi), and by 2^-23 as a 32-bit argument.
  */
 typedef struct {
   const double* inv_freq; /* device fp64 [rotary_dim / 2], radians per position */
