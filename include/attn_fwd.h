@@ -488,7 +488,7 @@ attn_status attn_rope(const void* q, void* q_out, const void* k, void* k_out, co
  * outside the pool neither, and the device error word's bit for bad cache indices
  * is set.  No slot may be named twice (of two such tokens either's 16-byte pieces may
  * stay).  With `rope` (not inverse) k is rotated on the way, by positions [num_tokens], and so
- * is q [num_tokens][Hq][d], every row of it, into q_out (q itself, or not overlapping it).
+ * is q [num_tokens][Hq][d], every row of it, into q_out (q itself, or not overlapping q, k or v).
  * rope NULL: no rotation; Hq = 0: no q.  d a multiple of 8, at most 512; fp16 or bf16. */
 attn_status attn_cache_append(const void* q, void* q_out, const void* k, const void* v, void* k_pool, void* v_pool,
                               const int32_t* slots, const int32_t* positions, int num_tokens, int Hq, int Hkv, int d,
