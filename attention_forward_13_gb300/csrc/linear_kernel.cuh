@@ -9,8 +9,8 @@
 // v (the columns of S are independent); the CTAs of a head's two halves run next
 // to each other and share Q and K in L2.
 //
-// Measured: 2 x 8192 tokens of 32 heads, d = 128, bf16 in 100.6 us, 5.4 TB/s (0.80 of a copy's
-// rate; fp16 115, its operands scaled into range); 16 heads of 2048 in 21.4.
+// Measured: 2 x 8192 tokens of 32 heads, d = 128, bf16 in 101 us, 5.3 TB/s (0.80 of a copy's
+// rate; fp16 128, its operands scaled into range); 16 heads of 2048 in 22.6 (fp16 25.4).
 //
 // What bounds it: a chunk moves 80 KB (d = 128) for 12.6 MFLOP, 1536 cycles of the
 // tensor core against some 1900 of its share of HBM, so everything else has to hide
