@@ -30,7 +30,11 @@ using namespace attn;
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPerSm = 4;  // CTAs that an SM holds (at 3, 5 and 6: 57.8, 61.7 and 66.9 us for that prompt)
+// CTAs that an SM holds.  At 3, 4, 5 and 6: 57.1, 54.8, 62.2 and 68.3 us for that prompt, in fp16
+// by pairs 57.4, 54.8, 60.4 and 75.5, of 32 heads of d = 64 25.7, 24.6, 27.5 and 31.6; 2000 tokens
+// of those 6.0, 7.3, 7.9 and 10.9, 300 tokens of 10 heads 3.2 to 3.7; 4096 tokens into the
+// cache 22.2, 20.9, 22.0 and 25.1.
+constexpr int kPerSm = 4;
 constexpr int kMaxDim = 512;
 
 // A tensor's rows: element strides of batch, head and row.
