@@ -34,9 +34,9 @@ struct LinearParams {
 // whose states are summed up first, in a launch of its own that reads k and v once
 // more (and takes about half the time a chunk).  As many pieces as the longest walk is
 // longer than an SM's share of all chunks, rounded down (16 heads of 2048 tokens, d = 128, bf16
-// and fp16: 24.0 -> 22.6 and 32.5 -> 25.4 us; sequences of 3000, 200, 100 and 50 tokens, 16
+// and fp16: 24.0 -> 22.7 and 33 -> 25.8 us; sequences of 3000, 200, 100 and 50 tokens, 16
 // heads, d = 64: 37 -> 24 and 47 -> 27; rounded up, 16 sequences of 1 to 3001: 36 -> 58 and
-// 46 -> 68).  Segments that short sequences do not
+// 47 -> 68).  Segments that short sequences do not
 // have are CTAs as well, that leave at once: no more than eight for every SM.
 inline void linear_segments(int B, int Hq, int max_len, int64_t total, int d, int* segs, int* seg_chunks) {
   constexpr int64_t kSms = 152;

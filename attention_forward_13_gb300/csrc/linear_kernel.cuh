@@ -10,7 +10,7 @@
 // to each other and share Q and K in L2.
 //
 // Measured: 2 x 8192 tokens of 32 heads, d = 128, bf16 in 101 us, 5.3 TB/s (0.80 of a copy's
-// rate; fp16 128, its operands scaled into range); 16 heads of 2048 in 22.6 (fp16 25.4).
+// rate; fp16 130, its operands scaled into range); 16 heads of 2048 in 22.7 (fp16 25.8).
 //
 // What bounds it: a chunk moves 80 KB (d = 128) for 12.6 MFLOP, 1536 cycles of the
 // tensor core against some 1900 of its share of HBM, so everything else has to hide
@@ -33,7 +33,7 @@
 // Roundings to 16 bits: P and the operand copy of S, each at most half a step of
 // the type, as o itself is.  The state proper stays in 32 bits in tensor memory, and what is added
 // to it is V' in two pieces (v' = hi + lo, lo's own rounding 2^-18 of v' in bf16; in fp16 2^-21 of it, or
-// 2^-35): one piece would put a 16-bit error into a 32-bit result that later calls build on.  fp16 has no
+// 2^-36): one piece would put a 16-bit error into a 32-bit result that later calls build on.  fp16 has no
 // room for the operands' ranges: the rows of P, the copy of S and the second piece of V' are scaled by
 // powers of two to fit.
 //
@@ -120,11 +120,9 @@ __device__ __forceinline__ void unpack16(uint32_t w, float& lo, float& hi) {
   }
 }
 
-template <bool BF16>
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t d;
-  if constexpr (BF16) asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  else asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
@@ -133,12 +131,12 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
   return d;
 }
 
-// fp16: what the second piece of V' is multiplied by.  (It is at most a step of the first
-// one, 32: room for 2^10.)
-constexpr float kSecondScale = 1024.0f;
+// fp16: what the second piece of V' is multiplied by.  (It is at most half a step of the
+// first one, 16: room for 2^11.)
+constexpr float kSecondScale = 2048.0f;
 // a -= kSecondScale x, for both fp16 halves of x.
 __device__ __forceinline__ void subtract_scaled(uint32_t x, float& a0, float& a1) {
-  asm("{\n .reg .b16 x0, x1, m;\n mov.b32 {x0, x1}, %2;\n mov.b16 m, 0xe400;\n"
+  asm("{\n .reg .b16 x0, x1, m;\n mov.b32 {x0, x1}, %2;\n mov.b16 m, 0xe800;\n"
       " fma.rn.f32.f16 %0, x0, m, %0;\n fma.rn.f32.f16 %1, x1, m, %1;\n}\n"
       : "+f"(a0), "+f"(a1)
       : "r"(x));
@@ -378,10 +376,10 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
     // by w^(tokens of the chunk) when it is read.  Thread = token r, 32 columns.  In packed 16-bit
     // arithmetic: with the weight f = f1 + f2 in two pieces, hi = f1 v rounded, f1 v - hi is exact
     // (a product of two significands less its upper half), and lo = that + f2 v: f2's and lo's
-    // roundings are 2^-18 of v' each in bf16.  fp16 has not the exponents for that: lo = f v - hi
-    // comes from 32 bits, where it is exact, and is held at 2^10 of its size, rounded to 2^-21 of
-    // v', or among the subnormal numbers to 2^-35 (2 x 8192 tokens of 32 heads: 118 us with a lo
-    // of its own size, whose error is 2^-24 however small v is, 128 with this one).
+    // roundings are 2^-18 of v' each in bf16.  fp16 has not the exponents for that: v' in 32 bits,
+    // hi rounded from it, and lo = v' - hi, which is exact there, at 2^11 of its size: rounded to 2^-22
+    // of v', or among the subnormal numbers to 2^-36 (2 x 8192 tokens of 32 heads: 118 us with a lo
+    // of its own size, whose error is 2^-24 however small v is, 130 with this one).
     auto values = [&](int n) {
       const int sv = n % C::NV;
       ok = __all_sync(0xffffffffu, w.wait(&sm.v_full[sv], (n / C::NV) & 1, kErrLinearWait));
@@ -394,10 +392,10 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
       uint8_t* src = sm.v[sv] + r * 128;
       uint32_t hi[16], lo[16];
       float f1, unused;
-      const uint32_t fw = pack16<BF16>(f, f);
-      unpack16<BF16>(fw, f1, unused);
+      const uint32_t fw = pack_bf16(f, f);
+      unpack16<true>(fw, f1, unused);
       const uint32_t gw = pack_bf16(f - f1, f - f1);
-      const uint64_t up = f2_pack(f * kSecondScale, f * kSecondScale);
+      const uint64_t weight = f2_pack(f, f), up = f2_pack(f * kSecondScale, f * kSecondScale);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint4 x = *reinterpret_cast<const uint4*>(src + (((4 * part + i) ^ (r & 7)) << 4));
@@ -405,16 +403,19 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint32_t v2 = r < live ? in[e] : 0u;  // (rows of nobody may hold anything)
-          const uint32_t first = mul2<BF16>(v2, fw);
-          hi[4 * i + e] = first;
+          uint32_t &first = hi[4 * i + e], &second = lo[4 * i + e];
           if constexpr (BF16) {
-            lo[4 * i + e] = fma_bf16x2(v2, gw, fma_bf16x2(v2, fw, first ^ 0x80008000u));
+            first = mul_bf16x2(v2, fw);
+            second = fma_bf16x2(v2, gw, fma_bf16x2(v2, fw, first ^ 0x80008000u));
           } else {
             float x, y;
             unpack16<BF16>(v2, x, y);
-            f2_unpack(f2_mul(f2_pack(x, y), up), x, y);
+            const uint64_t both = f2_pack(x, y);
+            f2_unpack(f2_mul(both, weight), x, y);
+            first = pack16<BF16>(x, y);
+            f2_unpack(f2_mul(both, up), x, y);
             subtract_scaled(first, x, y);
-            lo[4 * i + e] = pack16<BF16>(x, y);
+            second = pack16<BF16>(x, y);
           }
         }
       }

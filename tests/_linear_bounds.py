@@ -7,9 +7,9 @@ o:  weights and the state before a chunk are rounded to 16 bits, each h of its o
     where its largest score lies at 2^10 or more, so by 2^-35 of that score against the sum of |v| (decays above 1: its
     largest weight at 2^14 w^-15 or more, so by 2^-39 w^15 of that); the state where its largest element lies at 2^14 or more, so by 2^-39 of that element against the sum of |q|,
     times up to w^128 if that is above 1.
-S:  the terms e^(g n) v come in two 16-bit pieces.  bf16: h^2 of each term.  fp16: the second piece, at most 2^-10 of
-    the term and exact before, is rounded to 2^-11 of itself; it is held at 2^10 of its size, so that below the normal numbers
-    it is off by 2^-25 2^-10 = 2^-35.  That meets |k| whatever the weight was, n counting the tokens to the end of a chunk of
+S:  the terms e^(g n) v come in two 16-bit pieces.  bf16: h^2 of each term.  fp16: the second piece, at most
+    2^-11 of the term and exact before, is rounded to 2^-11 of itself, and the term was to 2^-24; it is held at 2^11 of
+    its size, so that below the normal numbers it is off by 2^-25 2^-11 = 2^-36.  That meets |k| whatever the weight was, n counting the tokens to the end of a chunk of
     128, or of a piece where the sequence is cut (piece: at least that many tokens), and decays from there on; decays above
     1 are counted from a chunk's start, so that the state then grows by up to w^128.
 32 bits: (64 + c) 2^-23 of the magnitudes over c chunks for the sums, and 2 |g| L 2^-23 for the decays' exponents where
@@ -33,7 +33,7 @@ def bounds(q, k, v, g, scale, state=None, piece=128):
         top[:, t] = most
         kt, vt, qt = k[:, t, :, None], v[:, t, None, :], q[:, t, :, None]
         S, M = S * w + kt * vt, M * w + kt.abs() * vt.abs()
-        before, now = before * w, now + kt.abs() * 2.0 ** -35
+        before, now = before * w, now + kt.abs() * 2.0 ** -36
         if (t + 1) % piece == 0 or t == L - 1:
             before, now = before + now * grown, torch.zeros_like(now)
         o[:, t], A[:, t] = (qt * S).sum(1), (qt.abs() * M).sum(1)
