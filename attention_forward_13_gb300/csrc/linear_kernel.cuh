@@ -32,7 +32,7 @@
 //
 // Roundings to 16 bits: P and the operand copy of S, each at most half a step of
 // the type, as o itself is.  The state proper stays in 32 bits in tensor memory, and what is added
-// to it is V' in two pieces (v' = hi + lo, lo's own rounding 2^-18 of v' in bf16; in fp16 2^-21 of it, or
+// to it is V' in two pieces (hi + lo, within 3 2^-16 of v' in bf16, 2^-18 in the mean; in fp16 2^-21 of it, or
 // 2^-36): one piece would put a 16-bit error into a 32-bit result that later calls build on.  fp16 has no
 // room for the operands' ranges: the rows of P, the copy of S and the second piece of V' are scaled by
 // powers of two to fit.
@@ -375,8 +375,8 @@ __global__ void __launch_bounds__(LinearCfg<D>::THREADS, 1) linear_chunk_kernel(
     // the first launch the segment's; with `back` w^-(tokens up to it) v, and the state is multiplied
     // by w^(tokens of the chunk) when it is read.  Thread = token r, 32 columns.  In packed 16-bit
     // arithmetic: with the weight f = f1 + f2 in two pieces, hi = f1 v rounded, f1 v - hi is exact
-    // (a product of two significands less its upper half), and lo = that + f2 v: f2's and lo's
-    // roundings are 2^-18 of v' each in bf16.  fp16 has not the exponents for that: v' in 32 bits,
+    // (a product of two significands less its upper half), and lo = that + f2 v, at most 2^-7 of v' in
+    // bf16, where its rounding is at most 2^-15 of v' and f2's 2^-16.  fp16 has not the exponents for that: v' in 32 bits,
     // hi rounded from it, and lo = v' - hi, which is exact there, at 2^11 of its size: rounded to 2^-22
     // of v', or among the subnormal numbers to 2^-36 (2 x 8192 tokens of 32 heads: 118 us with a lo
     // of its own size, whose error is 2^-24 however small v is, 130 with this one).

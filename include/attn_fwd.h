@@ -511,7 +511,7 @@ attn_status attn_cache_append(const void* q, void* q_out, const void* k, const v
  * bf16, and the results.
  * Weights and states of any size that fp32 holds are kept in range (fp16: by powers of two).
  * The terms e^(g n) v enter a state, n counted to the end of a chunk of 128 tokens or of a piece
- * (where few heads have a sequence cut), held to 2^-17 of themselves in bf16, and in fp16
+ * (where few heads have a sequence cut), held to 3 * 2^-16 of themselves in bf16, and in fp16
  * to 2^-21 of themselves or 2^-36 (for g above 0: 2^-36 e^(128 g)), whichever is more.
  * NaN or infinity in a sequence's q, k, v or state may make all that sequence's outputs
  * and its state NaN, and no other's; what lies behind a sequence's end may hold anything.

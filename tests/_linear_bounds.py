@@ -7,7 +7,8 @@ o:  weights and the state before a chunk are rounded to 16 bits, each h of its o
     where its largest score lies at 2^10 or more, so by 2^-35 of that score against the sum of |v| (decays above 1: its
     largest weight at 2^14 w^-15 or more, so by 2^-39 w^15 of that); the state where its largest element lies at 2^14 or more, so by 2^-39 of that element against the sum of |q|,
     times up to w^128 if that is above 1.
-S:  the terms e^(g n) v come in two 16-bit pieces.  bf16: h^2 of each term.  fp16: the second piece, at most
+S:  the terms e^(g n) v come in two 16-bit pieces.  bf16: 3 h^2 of each term (the weight's rest, at most h of it, is
+    rounded by h of itself, and the second piece, at most 2 h of the term, by h of that).  fp16: the second piece, at most
     2^-11 of the term and exact before, is rounded to 2^-11 of itself, and the term was to 2^-24; it is held at 2^11 of
     its size, so that below the normal numbers it is off by 2^-25 2^-11 = 2^-36.  That meets |k| whatever the weight was, n counting the tokens to the end of a chunk of
     128, or of a piece where the sequence is cut (piece: at least that many tokens), and decays from there on; decays above
@@ -40,7 +41,7 @@ def bounds(q, k, v, g, scale, state=None, piece=128):
         most = torch.maximum(most, S.abs().amax((1, 2)))
     f32 = ((64 + (L + 127) // 128 + 2 * g.clamp(min=0) * L) * 2.0 ** -23)[:, None, None]
     do = h * (A * scale + o.abs() * scale) + f32 * A * scale + torch.finfo(torch.float16 if f16 else torch.bfloat16).smallest_normal * h
-    dS = (2.0 ** -21 if f16 else h * h) * M + f32 * M + 1e-35
+    dS = (2.0 ** -21 if f16 else 3 * h * h) * M + f32 * M + 1e-35
     if f16:
         i = torch.arange(L, device=q.device)
         best = torch.zeros(H, L, dtype=torch.float64, device=q.device)
